@@ -230,6 +230,115 @@ int swiglu_q_mlp(const void *x,
                  int bits_g, int gs_g, int bits_u, int gs_u, int bits_d, int gs_d,
                  int out_mode, void *out, void *stream);
 
+/*
+ * ---- Microscaled 4-bit floating point (MXFP4) and the experts' MLP -----------
+ *
+ * A second weight format beside the affine one: every value is a 4-bit e2m1
+ * code (bit 3 the sign; 0 .5 1 1.5 2 3 4 6 by the low three bits) times a power of two
+ * shared by 32 consecutive inputs, one e8m0 byte b = 2^(b - 127), 255 = NaN.
+ *   codes    uint32 [rows, K/8]   along K, eight per word, code j of a word in
+ *                                 bits [4j, 4j+4) (the affine codes' packing)
+ *   scales   uint8  [rows, K/32]
+ * With experts, a leading dimension E: [E, rows, K/8] and [E, rows, K/32].  K is
+ * a multiple of 32.  The format is the Open Compute Project's "Microscaling
+ * formats (MX)" specification's MXFP4.
+ *
+ * As above: device pointers, contiguous row-major, work enqueued on `stream`,
+ * arguments checked on the host before any HIP call, deterministic results, no
+ * clearing needed between graph replays.  Codes, x and dequantized output need
+ * 16-byte alignment, scales none, everything else its element size.  The
+ * grouped linear and the experts' MLP take a workspace of the
+ * (device, stream) as described at the top, with the same rules for graphs and
+ * concurrent calls; the others take none.
+ */
+
+/* Element types (and the out_mode values beyond the affine linear's two). */
+#define SWQ_TYPE_BF16    0
+#define SWQ_TYPE_F32     1
+#define SWQ_TYPE_F16     2
+#define SWQ_LINEAR_F16   2  /* float32 sums rounded once to binary16 at the store   */
+
+/* Limits of the router and of the products grouped by expert. */
+#define SWQ_MAX_EXPERTS  1024
+#define SWQ_MAX_CHOSEN   64
+
+/* Weights that swiglu_q_route gives the chosen experts. */
+#define SWQ_ROUTE_SOFTMAX         0  /* softmax over all experts                    */
+#define SWQ_ROUTE_SOFTMAX_CHOSEN  1  /* softmax over the chosen experts             */
+#define SWQ_ROUTE_SIGMOID         2  /* sigmoid of each logit                       */
+#define SWQ_ROUTE_SIGMOID_CHOSEN  3  /* ... divided by the sum over the chosen      */
+
+/*
+ * Quantize x [R, K] (bf16, float32 or binary16 by `type`) to MXFP4.  A block of
+ * 32 takes the scale 2^e, e = floor(log2(max |x|)) - 2 clamped to
+ * [-127, 127] (-127 for a block of zeros); its elements x 2^-e are rounded to the
+ * nearest e2m1 value, ties to even, and saturate at 6.  A block that holds an
+ * infinity or a NaN gets the NaN scale (255) and zero codes.
+ */
+int swiglu_q_mx4_quantize(const void *x, int64_t R, int64_t K, int type,
+                          uint32_t *codes, void *scales, void *stream);
+
+/* The values [R, K] that codes and scales stand for, in `type` (one rounding;
+ * bf16 and float32 hold every value up to their range exactly). */
+int swiglu_q_mx4_dequantize(const uint32_t *codes, const void *scales, int64_t R,
+                            int64_t K, int type, void *out, void *stream);
+
+/*
+ * y = x W^T (+ residual) with MXFP4 W [N, K]: x and residual bf16 or binary16
+ * (type SWQ_TYPE_BF16 or SWQ_TYPE_F16), residual [M, N] or NULL, out [M, N] in x's
+ * type (out_mode = type) or float32 (SWQ_LINEAR_F32).  Exact products, float32
+ * sums, the residual added before the one rounding.  A result past float32's
+ * range is an infinity; a NaN scale makes its row's column NaN.
+ */
+int swiglu_q_mx4_linear(const void *x, const uint32_t *W, const void *s, const void *residual,
+                        int64_t M, int64_t K, int64_t N, int type, int out_mode,
+                        void *out, void *stream);
+
+/* y = A W^T with both A [M, K] and W [N, K] MXFP4 (the scaled matrix
+ * instructions' own format), out [M, N] bf16, float32 or binary16 by out_mode. */
+int swiglu_q_mx4_matmul(const uint32_t *A, const void *sa, const uint32_t *W, const void *sw,
+                        int64_t M, int64_t K, int64_t N, int out_mode, void *out, void *stream);
+
+/*
+ * Product grouped by expert: x [P, K] sorted by expert, expert e's rows being
+ * [offsets[e], offsets[e+1]) (int32 [E + 1] on the device, groups of any size, empty
+ * ones too), y[p] = x[p] W[e]^T with W [E, N, K].  Types and out_mode as
+ * swiglu_q_mx4_linear.  Rows of no group are written as zeros; offsets that
+ * decrease or leave [0, P] are taken as the nearest that do not.
+ */
+int swiglu_q_mx4_grouped_linear(const void *x, const int32_t *offsets, const uint32_t *W, const void *s,
+                                int64_t P, int64_t E, int64_t K, int64_t N, int type, int out_mode,
+                                void *out, void *stream);
+
+/*
+ * Router: the k largest of each row's logits [T, E] (bf16, float32 or binary16),
+ * in descending order, ties to the lowest index, and their weights
+ * (SWQ_ROUTE_*).  ids int32 [T, k], weights float32 [T, k].  A NaN logit ranks as
+ * -inf, +inf as the largest float32.  An expert whose logit is -inf (masked)
+ * is never chosen: slots that are left over get id -1 and weight 0, all of
+ * them in a row with nothing but -inf.
+ */
+int swiglu_q_route(const void *logits, int64_t T, int64_t E, int k, int type, int scoring,
+                   int32_t *ids, float *weights, void *stream);
+
+/*
+ * The experts' MLP: out[t] = residual[t] + sum_j weights[t, j] MLP_e(x[t]) with
+ * e = ids[t, j], MLP_e(x) = (silu(x Wg[e]^T) * (x Wu[e]^T)) Wd[e]^T.  Slots whose id
+ * is outside [0, E) are skipped (their weights are not read as numbers).
+ *   x          [T, H], residual [T, Ho] or NULL: bf16 or binary16 by `type`
+ *   ids        int32 [T, k], weights float32 [T, k] (swiglu_q_route's output)
+ *   Wg, Wu     codes [E, I, H/8], scales [E, I, H/32];  Wd [E, Ho, I/8], [E, Ho, I/32]
+ *   out        [T, Ho] in x's type (out_mode = type) or float32
+ * gate, up, silu and their product are float32; the hidden tensor is rounded
+ * once (bf16; for binary16 x to 16 significant bits), everything after it is
+ * float32 up to the one rounding of out.
+ */
+int swiglu_q_moe_mlp(const void *x, const int32_t *ids, const float *weights,
+                     const uint32_t *Wg, const void *sg, const uint32_t *Wu, const void *su,
+                     const uint32_t *Wd, const void *sd, const void *residual,
+                     int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t Ho,
+                     int type, int out_mode, void *out, void *stream);
+
 /* 1 if the combination is supported by swiglu_q_forward, else 0 (mirrors the
  * pages' support predicate, restricted to what this library implements). */
 int swiglu_q_supported(int64_t H, int bits_g, int gs_g, int bits_u, int gs_u,

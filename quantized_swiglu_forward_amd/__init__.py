@@ -22,7 +22,10 @@ LIB_PATH = os.path.join(PKG, "libswiglu_q.so")
  SWQ_ERR_TOO_LARGE) = range(8)
 SWQ_MATCH, SWQ_F32, SWQ_F32_BF16OUT = 0, 1, 2
 SWQ_PATH_GEMV, SWQ_PATH_MFMA, SWQ_PATH_AUTO = 0, 1, -1
-SWQ_LINEAR_BF16, SWQ_LINEAR_F32 = 0, 1
+SWQ_LINEAR_BF16, SWQ_LINEAR_F32, SWQ_LINEAR_F16 = 0, 1, 2
+SWQ_TYPE_BF16, SWQ_TYPE_F32, SWQ_TYPE_F16 = 0, 1, 2
+SWQ_ROUTE_SOFTMAX, SWQ_ROUTE_SOFTMAX_CHOSEN, SWQ_ROUTE_SIGMOID, SWQ_ROUTE_SIGMOID_CHOSEN = range(4)
+SWQ_MAX_EXPERTS, SWQ_MAX_CHOSEN = 1024, 64
 
 _lib = None
 
@@ -63,6 +66,20 @@ def load_library(path):
     L.swiglu_q_mlp.restype = i32
     L.swiglu_q_debug_gemm.argtypes = [vp] * 7 + [i64, i64, i64, i32, i32, i32, i32, i32, vp, vp, vp]
     L.swiglu_q_debug_gemm.restype = i32
+    L.swiglu_q_mx4_quantize.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    L.swiglu_q_mx4_quantize.restype = i32
+    L.swiglu_q_mx4_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+    L.swiglu_q_mx4_dequantize.restype = i32
+    L.swiglu_q_mx4_linear.argtypes = [vp] * 4 + [i64, i64, i64, i32, i32, vp, vp]
+    L.swiglu_q_mx4_linear.restype = i32
+    L.swiglu_q_mx4_matmul.argtypes = [vp] * 4 + [i64, i64, i64, i32, vp, vp]
+    L.swiglu_q_mx4_matmul.restype = i32
+    L.swiglu_q_mx4_grouped_linear.argtypes = [vp] * 4 + [i64, i64, i64, i64, i32, i32, vp, vp]
+    L.swiglu_q_mx4_grouped_linear.restype = i32
+    L.swiglu_q_route.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, vp]
+    L.swiglu_q_route.restype = i32
+    L.swiglu_q_moe_mlp.argtypes = [vp] * 10 + [i64] * 6 + [i32, i32, vp, vp]
+    L.swiglu_q_moe_mlp.restype = i32
     L.swiglu_q_supported.argtypes = [i64, i32, i32, i32, i32, i32]
     L.swiglu_q_supported.restype = i32
     L.swiglu_q_set_m_threshold.argtypes = [i32]
@@ -142,6 +159,40 @@ def swiglu_q_mlp(x, Wg, sg, bg, Wu, su, bu, Wd, sd, bd, residual, M, H, I, Ho, b
     return lib().swiglu_q_mlp(_ptr(x), _ptr(Wg), _ptr(sg), _ptr(bg), _ptr(Wu), _ptr(su), _ptr(bu), _ptr(Wd),
                               _ptr(sd), _ptr(bd), _ptr(residual), M, H, I, Ho, bits_g, gs_g, bits_u, gs_u, bits_d,
                               gs_d, out_mode, _ptr(out), _stream(stream))
+
+
+def swiglu_q_mx4_quantize(x, R, K, type, codes, scales, stream=None) -> int:
+    return lib().swiglu_q_mx4_quantize(_ptr(x), R, K, type, _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def swiglu_q_mx4_dequantize(codes, scales, R, K, type, out, stream=None) -> int:
+    return lib().swiglu_q_mx4_dequantize(_ptr(codes), _ptr(scales), R, K, type, _ptr(out), _stream(stream))
+
+
+def swiglu_q_mx4_linear(x, W, s, residual, M, K, N, type, out_mode, out, stream=None) -> int:
+    return lib().swiglu_q_mx4_linear(_ptr(x), _ptr(W), _ptr(s), _ptr(residual), M, K, N, type, out_mode, _ptr(out),
+                                     _stream(stream))
+
+
+def swiglu_q_mx4_matmul(A, sa, W, sw, M, K, N, out_mode, out, stream=None) -> int:
+    return lib().swiglu_q_mx4_matmul(_ptr(A), _ptr(sa), _ptr(W), _ptr(sw), M, K, N, out_mode, _ptr(out),
+                                     _stream(stream))
+
+
+def swiglu_q_mx4_grouped_linear(x, offsets, W, s, P, E, K, N, type, out_mode, out, stream=None) -> int:
+    return lib().swiglu_q_mx4_grouped_linear(_ptr(x), _ptr(offsets), _ptr(W), _ptr(s), P, E, K, N, type, out_mode,
+                                             _ptr(out), _stream(stream))
+
+
+def swiglu_q_route(logits, T, E, k, type, scoring, ids, weights, stream=None) -> int:
+    return lib().swiglu_q_route(_ptr(logits), T, E, k, type, scoring, _ptr(ids), _ptr(weights), _stream(stream))
+
+
+def swiglu_q_moe_mlp(x, ids, weights, Wg, sg, Wu, su, Wd, sd, residual, T, k, E, H, I, Ho, type, out_mode, out,
+                     stream=None) -> int:
+    return lib().swiglu_q_moe_mlp(_ptr(x), _ptr(ids), _ptr(weights), _ptr(Wg), _ptr(sg), _ptr(Wu), _ptr(su), _ptr(Wd),
+                                  _ptr(sd), _ptr(residual), T, k, E, H, I, Ho, type, out_mode, _ptr(out),
+                                  _stream(stream))
 
 
 def swiglu_q_path_for(M, H, I) -> int:
@@ -295,6 +346,218 @@ def mlp(x, wg, sg, bg, wu, su, bu, wd, sd, bd, spec_g, spec_u, spec_d, residual=
                       spec_u[0], spec_u[1], spec_d[0], spec_d[1], out_mode, out, stream)
     if rc != SWQ_OK:
         raise SwigluQError(rc, "swiglu_q_mlp")
+    return out
+
+
+# ---- microscaled 4-bit floating point (MXFP4), the router, the experts' MLP ----
+#
+# Codes are int32 (or uint32) words [..., K/8], scales uint8 [..., K/32];
+# experts are a leading dimension.  Every tensor must be contiguous and on x's
+# device; types and shapes that the library does not take raise here.
+
+def _mx4_types():
+    import torch
+    return {torch.bfloat16: SWQ_TYPE_BF16, torch.float32: SWQ_TYPE_F32, torch.float16: SWQ_TYPE_F16}
+
+
+_types = None
+
+
+def _type(t, what, wide=True):
+    global _types
+    if _types is None:
+        _types = _mx4_types()
+    code = _types.get(t.dtype, -1)
+    if code < 0 or (code == SWQ_TYPE_F32 and not wide):
+        raise TypeError(f"{what}: {t.dtype} is not a supported type")
+    return code
+
+
+def _dtype(code):
+    import torch
+    return (torch.bfloat16, torch.float32, torch.float16)[code]
+
+
+def _same_place(what, x, *tensors):
+    for t in (x,) + tensors:
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: every tensor must be contiguous")
+        if not t.is_cuda or t.device != x.device:
+            raise ValueError(f"{what}: every tensor must be on one GPU")
+
+
+def _mx4_shape(codes, scales, what, K=None, dims=2):
+    """Rows (and experts) and K of a matrix of codes and scales."""
+    import torch
+    if codes.dtype not in (torch.int32, torch.uint32) or scales.dtype != torch.uint8:
+        raise TypeError(f"{what}: codes must be int32 or uint32 words and scales uint8")
+    k = codes.shape[-1] * 8
+    if codes.dim() != dims or scales.dim() != dims or codes.shape[:-1] != scales.shape[:-1] \
+            or scales.shape[-1] * 32 != k:
+        raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not one "
+                         f"{dims}-dimensional MXFP4 matrix")
+    if K is not None and k != K:
+        raise ValueError(f"{what}: the weights have {k} inputs, x has {K}")
+    return tuple(codes.shape[:-1])
+
+
+def _out(out, shape, dtype, x, what):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != x.device:
+        raise ValueError(f"{what}: out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {x.device}")
+    return out
+
+
+def _raise_on(rc, what):
+    if rc != SWQ_OK:
+        raise SwigluQError(rc, what)
+
+
+def mx4_quantize(x, codes=None, scales=None, stream=None):
+    """(codes int32 [..., K/8], scales uint8 [..., K/32]) of x [..., K] (bf16,
+    float16 or float32; K a multiple of 32)."""
+    import torch
+    t = _type(x, "mx4_quantize")
+    _same_place("mx4_quantize", x)
+    if x.dim() < 1 or x.shape[-1] % 32 or x.shape[-1] == 0:
+        raise ValueError("mx4_quantize: the last dimension must be a positive multiple of 32")
+    K, lead = int(x.shape[-1]), tuple(x.shape[:-1])
+    codes = _out(codes, lead + (K // 8,), torch.int32, x, "mx4_quantize codes")
+    scales = _out(scales, lead + (K // 32,), torch.uint8, x, "mx4_quantize scales")
+    if x.numel():
+        _raise_on(swiglu_q_mx4_quantize(x, x.numel() // K, K, t, codes, scales, stream), "swiglu_q_mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, dtype=None, out=None, stream=None):
+    """The values [..., K] of codes and scales, in bf16 (default), float16 or float32."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    _mx4_shape(codes, scales, "mx4_dequantize", dims=codes.dim())
+    _same_place("mx4_dequantize", codes, scales)
+    K = int(codes.shape[-1]) * 8
+    out = _out(out, tuple(codes.shape[:-1]) + (K,), dtype, codes, "mx4_dequantize")
+    t = _type(out, "mx4_dequantize")
+    if out.numel():
+        _raise_on(swiglu_q_mx4_dequantize(codes, scales, out.numel() // K, K, t, out, stream),
+                  "swiglu_q_mx4_dequantize")
+    return out
+
+
+def mx4_linear(x, w, s, residual=None, out_mode=None, out=None, stream=None):
+    """``x W^T`` (+ residual) with MXFP4 W [N, K]: x [..., K] bf16 or float16.
+    Returns ``out`` [..., N] in x's type, or float32 with SWQ_LINEAR_F32."""
+    t = _type(x, "mx4_linear", wide=False)
+    K, lead = int(x.shape[-1]), tuple(x.shape[:-1])
+    N, = _mx4_shape(w, s, "mx4_linear", K)
+    out_mode = t if out_mode is None else out_mode
+    if out_mode not in (t, SWQ_LINEAR_F32):
+        raise ValueError("mx4_linear: out_mode must be x's type or SWQ_LINEAR_F32")
+    if residual is not None and (residual.dtype != x.dtype or tuple(residual.shape) != lead + (N,)):
+        raise ValueError(f"mx4_linear: residual must be {x.dtype} of shape {lead + (N,)}")
+    _same_place("mx4_linear", x, w, s, residual)
+    out = _out(out, lead + (N,), _dtype(out_mode), x, "mx4_linear")
+    if out.numel() == 0:
+        return out
+    _raise_on(swiglu_q_mx4_linear(x, w, s, residual, x.numel() // K, K, N, t, out_mode, out, stream),
+              "swiglu_q_mx4_linear")
+    return out
+
+
+def mx4_matmul(a, sa, w, sw, out_mode=SWQ_LINEAR_BF16, out=None, stream=None):
+    """``A W^T`` of two MXFP4 matrices: A [..., K], W [N, K].  Returns ``out``
+    [..., N] (SWQ_LINEAR_BF16, _F32 or _F16)."""
+    lead = _mx4_shape(a, sa, "mx4_matmul", dims=a.dim())
+    K = int(a.shape[-1]) * 8
+    N, = _mx4_shape(w, sw, "mx4_matmul", K)
+    if out_mode not in (SWQ_LINEAR_BF16, SWQ_LINEAR_F32, SWQ_LINEAR_F16):
+        raise ValueError("mx4_matmul: unknown out_mode")
+    _same_place("mx4_matmul", a, sa, w, sw)
+    out = _out(out, lead + (N,), _dtype(out_mode), a, "mx4_matmul")
+    if out.numel() == 0:
+        return out
+    _raise_on(swiglu_q_mx4_matmul(a, sa, w, sw, a.numel() * 8 // K, K, N, out_mode, out, stream),
+              "swiglu_q_mx4_matmul")
+    return out
+
+
+def mx4_grouped_linear(x, offsets, w, s, out_mode=None, out=None, stream=None):
+    """``x[p] W[e]^T`` for rows sorted by expert: x [P, K] bf16 or float16, offsets
+    int32 [E + 1] on the device (expert e has rows offsets[e] .. offsets[e+1]),
+    W [E, N, K].  Returns ``out`` [P, N]; rows of no expert are zero."""
+    import torch
+    t = _type(x, "mx4_grouped_linear", wide=False)
+    if x.dim() != 2:
+        raise ValueError("mx4_grouped_linear: x must be [rows, K]")
+    P, K = int(x.shape[0]), int(x.shape[1])
+    E, N = _mx4_shape(w, s, "mx4_grouped_linear", K, dims=3)
+    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,):
+        raise ValueError(f"mx4_grouped_linear: offsets must be int32 [{E + 1}]")
+    out_mode = t if out_mode is None else out_mode
+    if out_mode not in (t, SWQ_LINEAR_F32):
+        raise ValueError("mx4_grouped_linear: out_mode must be x's type or SWQ_LINEAR_F32")
+    _same_place("mx4_grouped_linear", x, offsets, w, s)
+    out = _out(out, (P, N), _dtype(out_mode), x, "mx4_grouped_linear")
+    if out.numel() == 0:
+        return out
+    _raise_on(swiglu_q_mx4_grouped_linear(x, offsets, w, s, P, E, K, N, t, out_mode, out, stream),
+              "swiglu_q_mx4_grouped_linear")
+    return out
+
+
+def route(logits, k, scoring=SWQ_ROUTE_SOFTMAX, ids=None, weights=None, stream=None):
+    """(ids int32 [..., k], weights float32 [..., k]): the k largest of each row
+    of logits [..., E] and their routing weights (SWQ_ROUTE_*); -1 and 0 where
+    fewer than k logits are above -inf."""
+    import torch
+    t = _type(logits, "route")
+    if logits.dim() < 1:
+        raise ValueError("route: logits need at least one dimension")
+    _same_place("route", logits)
+    E, lead = int(logits.shape[-1]), tuple(logits.shape[:-1])
+    ids = _out(ids, lead + (k,), torch.int32, logits, "route ids")
+    weights = _out(weights, lead + (k,), torch.float32, logits, "route weights")
+    if ids.numel() == 0:
+        return ids, weights
+    _raise_on(swiglu_q_route(logits, logits.numel() // max(E, 1), E, k, t, scoring, ids, weights, stream),
+              "swiglu_q_route")
+    return ids, weights
+
+
+def moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual=None, out_mode=None, out=None, stream=None):
+    """``residual + sum_j weights[t, j] MLP_e(x[t])``, e = ids[t, j], the MLP of
+    each expert being ``(silu(x Wg^T) * (x Wu^T)) Wd^T`` with MXFP4 weights
+    Wg, Wu [E, I, H], Wd [E, Ho, I].  x [..., H] bf16 or float16, ids int32 and
+    weights float32 [..., k] (``route``'s output; an id outside the experts is
+    skipped).  Returns ``out`` [..., Ho] in x's type, or float32 with
+    SWQ_LINEAR_F32."""
+    import torch
+    t = _type(x, "moe_mlp", wide=False)
+    H, lead = int(x.shape[-1]), tuple(x.shape[:-1])
+    E, I = _mx4_shape(wg, sg, "moe_mlp gate", H, dims=3)
+    if _mx4_shape(wu, su, "moe_mlp up", H, dims=3) != (E, I):
+        raise ValueError("moe_mlp: gate and up differ in shape")
+    Ed, Ho = _mx4_shape(wd, sd, "moe_mlp down", I, dims=3)
+    if Ed != E:
+        raise ValueError(f"moe_mlp: {E} experts in the gate, {Ed} in the down projection")
+    if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != weights.shape \
+            or tuple(ids.shape[:-1]) != lead or ids.dim() < 1:
+        raise ValueError(f"moe_mlp: ids must be int32 and weights float32 of shape {lead + ('k',)}")
+    out_mode = t if out_mode is None else out_mode
+    if out_mode not in (t, SWQ_LINEAR_F32):
+        raise ValueError("moe_mlp: out_mode must be x's type or SWQ_LINEAR_F32")
+    if residual is not None and (residual.dtype != x.dtype or tuple(residual.shape) != lead + (Ho,)):
+        raise ValueError(f"moe_mlp: residual must be {x.dtype} of shape {lead + (Ho,)}")
+    _same_place("moe_mlp", x, ids, weights, wg, sg, wu, su, wd, sd, residual)
+    out = _out(out, lead + (Ho,), _dtype(out_mode), x, "moe_mlp")
+    if out.numel() == 0:
+        return out
+    _raise_on(swiglu_q_moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual, x.numel() // H, int(ids.shape[-1]),
+                               E, H, I, Ho, t, out_mode, out, stream), "swiglu_q_moe_mlp")
     return out
 
 

@@ -34,6 +34,7 @@
 #include "../../include/swiglu_q.h"
 #include "swq_device.h"
 #include "swq_kernels.h"
+#include "swq_mx4.h"
 
 using namespace swq;
 
@@ -92,7 +93,8 @@ struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
 };
-// slot 0: the kernels' own staging; slot 1: the whole MLP's hidden tensor
+// slot 0: the kernels' own staging; slot 1: the whole MLP's hidden tensor; slot 2: the experts' order, hidden
+// tensor and partial outputs
 std::map<std::tuple<int, uintptr_t, int>, Workspace> g_ws;
 // Buffers replaced by a larger one.  They stay allocated until
 // swiglu_q_release_workspace(): work already queued on the stream, and HIP
@@ -314,6 +316,14 @@ int64_t staging_bytes(int64_t M, int64_t H, int64_t I, int bits_g, int gs_g, int
   if (path == SWQ_PATH_GEMV) return gemv_needs_rows(M, H, bits_g, bits_u) ? gemv_stage_bytes(M, H, I) : 0;
   return ws_layout(M, H, I, bits_g, gs_g, bits_u, gs_u).total;
 }
+
+}  // namespace
+
+int swq::stream_workspace(hipStream_t stream, size_t need, void** out, int slot) {
+  return get_workspace(stream, need, out, slot);
+}
+
+namespace {
 
 // The staging buffer of a call: the caller's fixed one (fixed != null; it
 // must hold `need` bytes) or the library's per-(device, stream) workspace.

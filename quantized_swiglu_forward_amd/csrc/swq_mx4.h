@@ -1,0 +1,91 @@
+// Internal interface between the host code and the kernels of the microscaled
+// 4-bit (MXFP4) operators, the router and the experts' MLP.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace swq {
+
+// Element types (values fixed by the public header).
+enum : int { kTypeBf16 = 0, kTypeF32 = 1, kTypeF16 = 2 };
+inline int type_bytes(int t) { return t == kTypeF32 ? 4 : 2; }
+
+// Where a product's rows of x come from:
+//   kXBf16   bf16 rows
+//   kXF16    binary16 rows, split into two bf16 operands by the kernel
+//   kXPlanes two bf16 rows (hi, lo), `plane` elements apart
+enum : int { kXBf16 = 0, kXF16 = 1, kXPlanes = 2 };
+
+// One tile of rows of a grouped product.
+struct RowTile {
+  int expert;   // -1: rows of no expert, written as zeros
+  int first;    // first slot (row of the sorted order)
+  int rows;     // 1 .. tile height
+  int pad;
+};
+
+// y[row, n] = sum_k x[row / xdiv, k] w[expert(row)][n, k], or with w2 the SwiGLU
+// of two such sums.  Dense products: tiles null, one expert, rows = M.
+struct MxGemm {
+  const uint16_t* x;
+  int64_t plane;            // kXPlanes: elements between the two planes
+  const uint32_t* w;        // codes [E][N][K/8]
+  const uint8_t* s;         // scales [E][N][K/32]
+  const uint32_t* w2;       // the up matrix, or null
+  const uint8_t* s2;
+  const uint16_t* res;      // residual [rows, N] in x's type, or null
+  void* out;                // [rows, N] in out_type; SwiGLU with hidden_planes: bf16 planes
+  int64_t out_plane;        // elements between the planes of a split hidden tensor
+  int rows, K, N, E;
+  int xsrc;                 // kXBf16, kXF16, kXPlanes
+  int xdiv;                 // row p reads x row p / xdiv
+  int type;                 // x's and the residual's 16-bit type
+  int out_type;
+  int hidden_planes;        // 1: write the hidden tensor as two bf16 planes
+  const RowTile* tiles;     // tile table, or null
+  const int* ntiles;
+  const int* perm;          // slot -> row, or null (the same)
+  int max_tiles;
+};
+
+struct Mx4Matmul {
+  const uint32_t* a;
+  const uint8_t* sa;
+  const uint32_t* w;
+  const uint8_t* s;
+  void* out;
+  int M, K, N, out_type;
+};
+
+struct RoutePlan {
+  const int* ids;           // [P] expert of each row, or null
+  const int* offsets;       // [E + 1] sorted rows' first slots, or null
+  int P, E, tile;           // rows, experts, tile height
+  RowTile* tiles;           // out
+  int* ntiles;              // out
+  int* perm;                // out (ids only)
+};
+// Most tiles a plan of P rows and E experts can have.
+inline int64_t max_row_tiles(int64_t P, int64_t E, int tile) {
+  return P / tile + (E + 2 < P ? E + 2 : P) + 1;
+}
+
+hipError_t launch_mx4_quantize(const void* x, int64_t blocks, int type, uint32_t* codes, uint8_t* scales,
+                               hipStream_t st);
+hipError_t launch_mx4_dequantize(const uint32_t* codes, const uint8_t* scales, int64_t blocks, int type, void* out,
+                                 hipStream_t st);
+hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st);
+int mx4_gemm_tile(const MxGemm& p);
+hipError_t launch_mx4_matmul(const Mx4Matmul& p, hipStream_t st);
+hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
+                        hipStream_t st);
+hipError_t launch_plan(const RoutePlan& p, hipStream_t st);
+// out[t] = residual[t] + sum_j weights[t, j] part[t k + j] over the slots whose id is an expert
+hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
+                          int k, int E, int N, int type, int out_type, void* out, hipStream_t st);
+
+// The library's per-(device, stream) buffers (swq_api.hip).
+int stream_workspace(hipStream_t stream, size_t need, void** out, int slot);
+
+}  // namespace swq

@@ -1,0 +1,254 @@
+// C-ABI entry points of the microscaled 4-bit (MXFP4) operators, the router
+// and the experts' MLP (declared in include/swiglu_q.h): validation on the
+// host, then launches on the caller's stream.
+#include "../../include/swiglu_q.h"
+#include "swq_mx4.h"
+
+using namespace swq;
+
+namespace {
+
+constexpr int kWsSlot = 2;            // the experts' workspace beside the MLP's two
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 20;
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+bool type_ok(int t) { return t == SWQ_TYPE_BF16 || t == SWQ_TYPE_F32 || t == SWQ_TYPE_F16; }
+bool type16_ok(int t) { return t == SWQ_TYPE_BF16 || t == SWQ_TYPE_F16; }
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Shapes of one product: rows of x, inputs, outputs.
+int check_shape(int64_t rows, int64_t K, int64_t N) {
+  if (rows < 0 || K <= 0 || N <= 0) return SWQ_ERR_SHAPE;
+  if (K % 32 != 0 || K > kMaxK || rows > kMaxRows || N > kMaxRows) return SWQ_ERR_SHAPE;
+  // the kernels number their tiles in 31 bits
+  if (((rows + 15) / 16 + 1024) * ((N + 15) / 16) >= (int64_t(1) << 31)) return SWQ_ERR_SHAPE;
+  return SWQ_OK;
+}
+
+// 16-byte aligned codes, the weights' rows per expert below 2^31.
+int check_codes(const uint32_t* W, const void* s) {
+  if (!W || !s) return SWQ_ERR_NULL;
+  return aligned(W, 16) ? SWQ_OK : SWQ_ERR_ALIGN;
+}
+
+int check_status(hipError_t e) { return e == hipSuccess ? SWQ_OK : SWQ_ERR_HIP; }
+
+// Bytes of a plan in the workspace: the tile count, the tile table, the order.
+struct PlanLayout {
+  int64_t tiles, perm, total;
+};
+PlanLayout plan_layout(int64_t P, int64_t E, int tile, bool with_perm) {
+  PlanLayout l;
+  l.tiles = 256;
+  l.perm = l.tiles + align256(max_row_tiles(P, E, tile) * (int64_t)sizeof(RowTile));
+  l.total = l.perm + (with_perm ? align256(P * 4) : 0);
+  return l;
+}
+
+int run_plan(MxGemm& g, char* ws, const PlanLayout& l, const int* ids, const int* offsets, int tile, hipStream_t st) {
+  RoutePlan r{};
+  r.ids = ids;
+  r.offsets = offsets;
+  r.P = g.rows;
+  r.E = g.E;
+  r.tile = tile;
+  r.ntiles = (int*)ws;
+  r.tiles = (RowTile*)(ws + l.tiles);
+  r.perm = ids ? (int*)(ws + l.perm) : nullptr;
+  g.tiles = r.tiles;
+  g.ntiles = r.ntiles;
+  g.perm = r.perm;
+  g.max_tiles = (int)max_row_tiles(g.rows, g.E, tile);
+  return check_status(launch_plan(r, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+int swiglu_q_mx4_quantize(const void* x, int64_t R, int64_t K, int type, uint32_t* codes, void* scales, void* stream) {
+  if (!x || !codes || !scales) return SWQ_ERR_NULL;
+  if (!type_ok(type)) return SWQ_ERR_UNSUPPORTED;
+  if (R < 0 || K <= 0 || K % 32 != 0 || K > kMaxK || R > kMaxRows || R * K >= (int64_t(1) << 41)) return SWQ_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(codes, 16)) return SWQ_ERR_ALIGN;
+  if (R == 0) return SWQ_OK;
+  (void)hipGetLastError();
+  return check_status(launch_mx4_quantize(x, R * (K / 32), type, codes, (uint8_t*)scales, (hipStream_t)stream));
+}
+
+int swiglu_q_mx4_dequantize(const uint32_t* codes, const void* scales, int64_t R, int64_t K, int type, void* out,
+                            void* stream) {
+  if (!codes || !scales || !out) return SWQ_ERR_NULL;
+  if (!type_ok(type)) return SWQ_ERR_UNSUPPORTED;
+  if (R < 0 || K <= 0 || K % 32 != 0 || K > kMaxK || R > kMaxRows || R * K >= (int64_t(1) << 41)) return SWQ_ERR_SHAPE;
+  if (!aligned(codes, 16) || !aligned(out, 16)) return SWQ_ERR_ALIGN;
+  if (R == 0) return SWQ_OK;
+  (void)hipGetLastError();
+  return check_status(
+      launch_mx4_dequantize(codes, (const uint8_t*)scales, R * (K / 32), type, out, (hipStream_t)stream));
+}
+
+int swiglu_q_mx4_linear(const void* x, const uint32_t* W, const void* s, const void* residual, int64_t M, int64_t K,
+                        int64_t N, int type, int out_mode, void* out, void* stream) {
+  if (!x || !out) return SWQ_ERR_NULL;
+  int rc = check_codes(W, s);
+  if (rc != SWQ_OK) return rc;
+  if (!type16_ok(type) || (out_mode != type && out_mode != SWQ_LINEAR_F32)) return SWQ_ERR_UNSUPPORTED;
+  rc = check_shape(M, K, N);
+  if (rc != SWQ_OK) return rc;
+  if (!aligned(x, 16) || !aligned(out, type_bytes(out_mode)) || !aligned(residual, 2)) return SWQ_ERR_ALIGN;
+  if (M == 0) return SWQ_OK;
+  MxGemm g{};
+  g.x = (const uint16_t*)x;
+  g.w = W;
+  g.s = (const uint8_t*)s;
+  g.res = (const uint16_t*)residual;
+  g.out = out;
+  g.rows = (int)M;
+  g.K = (int)K;
+  g.N = (int)N;
+  g.E = 1;
+  g.xsrc = type == SWQ_TYPE_F16 ? kXF16 : kXBf16;
+  g.xdiv = 1;
+  g.type = type;
+  g.out_type = out_mode;
+  (void)hipGetLastError();
+  return check_status(launch_mx4_gemm(g, (hipStream_t)stream));
+}
+
+int swiglu_q_mx4_matmul(const uint32_t* A, const void* sa, const uint32_t* W, const void* sw, int64_t M, int64_t K,
+                        int64_t N, int out_mode, void* out, void* stream) {
+  if (!out) return SWQ_ERR_NULL;
+  int rc = check_codes(A, sa);
+  if (rc != SWQ_OK) return rc;
+  rc = check_codes(W, sw);
+  if (rc != SWQ_OK) return rc;
+  if (!type_ok(out_mode)) return SWQ_ERR_UNSUPPORTED;
+  rc = check_shape(M, K, N);
+  if (rc != SWQ_OK) return rc;
+  if (!aligned(out, type_bytes(out_mode))) return SWQ_ERR_ALIGN;
+  if (M == 0) return SWQ_OK;
+  Mx4Matmul p{A, (const uint8_t*)sa, W, (const uint8_t*)sw, out, (int)M, (int)K, (int)N, out_mode};
+  (void)hipGetLastError();
+  return check_status(launch_mx4_matmul(p, (hipStream_t)stream));
+}
+
+int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uint32_t* W, const void* s, int64_t P,
+                                int64_t E, int64_t K, int64_t N, int type, int out_mode, void* out, void* stream_v) {
+  hipStream_t stream = (hipStream_t)stream_v;
+  if (!x || !offsets || !out) return SWQ_ERR_NULL;
+  int rc = check_codes(W, s);
+  if (rc != SWQ_OK) return rc;
+  if (!type16_ok(type) || (out_mode != type && out_mode != SWQ_LINEAR_F32)) return SWQ_ERR_UNSUPPORTED;
+  if (E < 1 || E > SWQ_MAX_EXPERTS) return SWQ_ERR_SHAPE;
+  rc = check_shape(P, K, N);
+  if (rc != SWQ_OK) return rc;
+  if (!aligned(x, 16) || !aligned(offsets, 4) || !aligned(out, type_bytes(out_mode))) return SWQ_ERR_ALIGN;
+  if (P == 0) return SWQ_OK;
+  MxGemm g{};
+  g.x = (const uint16_t*)x;
+  g.w = W;
+  g.s = (const uint8_t*)s;
+  g.out = out;
+  g.rows = (int)P;
+  g.K = (int)K;
+  g.N = (int)N;
+  g.E = (int)E;
+  g.xsrc = type == SWQ_TYPE_F16 ? kXF16 : kXBf16;
+  g.xdiv = 1;
+  g.type = type;
+  g.out_type = out_mode;
+  const int tile = mx4_gemm_tile(g);
+  const PlanLayout l = plan_layout(P, E, tile, false);
+  void* ws = nullptr;
+  rc = stream_workspace(stream, (size_t)l.total, &ws, kWsSlot);
+  if (rc != SWQ_OK) return rc;
+  (void)hipGetLastError();
+  rc = run_plan(g, (char*)ws, l, nullptr, offsets, tile, stream);
+  if (rc != SWQ_OK) return rc;
+  return check_status(launch_mx4_gemm(g, stream));
+}
+
+int swiglu_q_route(const void* logits, int64_t T, int64_t E, int k, int type, int scoring, int32_t* ids,
+                   float* weights, void* stream) {
+  if (!logits || !ids || !weights) return SWQ_ERR_NULL;
+  if (!type_ok(type) || scoring < SWQ_ROUTE_SOFTMAX || scoring > SWQ_ROUTE_SIGMOID_CHOSEN) return SWQ_ERR_UNSUPPORTED;
+  if (T < 0 || T > kMaxRows || E < 1 || E > SWQ_MAX_EXPERTS || k < 1 || k > SWQ_MAX_CHOSEN || k > E) return SWQ_ERR_SHAPE;
+  if (!aligned(logits, type_bytes(type)) || !aligned(ids, 4) || !aligned(weights, 4)) return SWQ_ERR_ALIGN;
+  if (T == 0) return SWQ_OK;
+  (void)hipGetLastError();
+  return check_status(launch_route(logits, T, (int)E, k, type, scoring, ids, weights, (hipStream_t)stream));
+}
+
+int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, const uint32_t* Wg, const void* sg,
+                     const uint32_t* Wu, const void* su, const uint32_t* Wd, const void* sd, const void* residual,
+                     int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t Ho, int type, int out_mode,
+                     void* out, void* stream_v) {
+  hipStream_t stream = (hipStream_t)stream_v;
+  if (!x || !ids || !weights || !out) return SWQ_ERR_NULL;
+  int rc = check_codes(Wg, sg);
+  if (rc == SWQ_OK) rc = check_codes(Wu, su);
+  if (rc == SWQ_OK) rc = check_codes(Wd, sd);
+  if (rc != SWQ_OK) return rc;
+  if (!type16_ok(type) || (out_mode != type && out_mode != SWQ_LINEAR_F32)) return SWQ_ERR_UNSUPPORTED;
+  if (T < 0 || T > kMaxRows || k < 1 || k > SWQ_MAX_CHOSEN || E < 1 || E > SWQ_MAX_EXPERTS) return SWQ_ERR_SHAPE;
+  const int64_t P = T * k;
+  rc = check_shape(P, H, I);
+  if (rc == SWQ_OK) rc = check_shape(P, I, Ho);
+  if (rc != SWQ_OK) return rc;
+  if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(out, type_bytes(out_mode)) ||
+      !aligned(residual, 2))
+    return SWQ_ERR_ALIGN;
+  if (T == 0) return SWQ_OK;
+  const bool f16 = type == SWQ_TYPE_F16;
+  MxGemm g{};
+  g.x = (const uint16_t*)x;
+  g.w = Wg;
+  g.s = (const uint8_t*)sg;
+  g.w2 = Wu;
+  g.s2 = (const uint8_t*)su;
+  g.rows = (int)P;
+  g.K = (int)H;
+  g.N = (int)I;
+  g.E = (int)E;
+  g.xsrc = f16 ? kXF16 : kXBf16;
+  g.xdiv = (int)k;
+  g.type = type;
+  g.out_type = SWQ_TYPE_BF16;
+  g.hidden_planes = f16;
+  const int tile = mx4_gemm_tile(g);
+  const PlanLayout l = plan_layout(P, E, tile, true);
+  const int64_t hidden = align256(P * I * 2) * (f16 ? 2 : 1);
+  const int64_t part = l.total + hidden;
+  void* ws_v = nullptr;
+  rc = stream_workspace(stream, (size_t)(part + align256(P * Ho * 4)), &ws_v, kWsSlot);
+  if (rc != SWQ_OK) return rc;
+  char* ws = (char*)ws_v;
+  (void)hipGetLastError();
+  rc = run_plan(g, ws, l, ids, nullptr, tile, stream);
+  if (rc != SWQ_OK) return rc;
+  g.out = ws + l.total;
+  g.out_plane = align256(P * I * 2) / 2;
+  rc = check_status(launch_mx4_gemm(g, stream));
+  if (rc != SWQ_OK) return rc;
+  MxGemm d = g;
+  d.x = (const uint16_t*)(ws + l.total);
+  d.plane = g.out_plane;
+  d.w = Wd;
+  d.s = (const uint8_t*)sd;
+  d.w2 = nullptr;
+  d.s2 = nullptr;
+  d.out = ws + part;
+  d.K = (int)I;
+  d.N = (int)Ho;
+  d.xsrc = f16 ? kXPlanes : kXBf16;
+  d.xdiv = 1;
+  d.out_type = SWQ_TYPE_F32;
+  d.hidden_planes = 0;
+  rc = check_status(launch_mx4_gemm(d, stream));
+  if (rc != SWQ_OK) return rc;
+  return check_status(launch_combine((const float*)(ws + part), ids, weights, (const uint16_t*)residual, T, (int)k,
+                                     (int)E, (int)Ho, type, out_mode, out, stream));
+}
+
+}  // extern "C"

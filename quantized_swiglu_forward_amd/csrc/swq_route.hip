@@ -1,0 +1,167 @@
+// The router's choice, the order of a product grouped by expert, and the sum
+// over a token's experts.
+#include "swq_mx4.h"
+#include "swq_mx4_device.h"
+
+namespace swq {
+namespace {
+
+// Routing weights (values fixed by the public header).
+enum : int { kRouteSoftmax = 0, kRouteSoftmaxChosen = 1, kRouteSigmoid = 2, kRouteSigmoidChosen = 3 };
+
+constexpr int kMaxExperts = 1024;
+
+__device__ __forceinline__ float load_logit(const void* p, int64_t at, int type) {
+  const float v = type == kTypeF32 ? ((const float*)p)[at] : from_16(((const uint16_t*)p)[at], type);
+  // NaN ranks below everything; +inf counts as the largest float32
+  return v != v ? -__builtin_inff() : fminf(v, 3.402823466e38f);
+}
+
+// A chosen logit's weight before the division by the sum: e^(v - top), or the sigmoid
+// e^min(v, 0) / (1 + e^-|v|), over the chosen ones times e^-min(top, 0), so that
+// very low logits do not make it 0 / 0.
+__device__ __forceinline__ float routing_term(float v, float top, int scoring) {
+  if (scoring <= kRouteSoftmaxChosen) return expf(v - top);
+  const float from = scoring == kRouteSigmoidChosen ? fminf(top, 0.0f) : 0.0f;
+  return expf(fminf(v, 0.0f) - from) / (1.0f + expf(-fabsf(v)));
+}
+
+// One wave per token.  A logit and its index make one 64-bit key that orders
+// by value, then by the lower index: k rounds of a maximum over the wave.
+__global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ logits, int64_t T, int E, int k, int type,
+                                                    int scoring, int* __restrict__ ids, float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  constexpr int R = kMaxExperts / 64;
+  float v[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) v[i] = 64 * i + lane < E ? load_logit(logits, t * E + 64 * i + lane, type) : -__builtin_inff();
+  float top = -__builtin_inff(), sum = 0.0f;
+  const bool over_all = scoring == kRouteSoftmax;
+  if (over_all) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) top = fmaxf(top, v[i]);
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+#pragma unroll
+    for (int i = 0; i < R; ++i) sum += v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.0f;
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  }
+  int my_id = -1;
+  float my_w = 0.0f, chosen = 0.0f;
+  uint32_t used = 0;
+  for (int j = 0; j < k; ++j) {
+    float bv = -__builtin_inff();
+    int bi = kMaxExperts;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (!(used >> i & 1) && v[i] > bv) bv = v[i], bi = 64 * i + lane;
+    for (int d = 32; d; d >>= 1) {
+      const float ov = __shfl_xor(bv, d);
+      const int oi = __shfl_xor(bi, d);
+      if (ov > bv || (ov == bv && oi < bi)) bv = ov, bi = oi;
+    }
+    if (bi == kMaxExperts) break;              // only -inf is left
+    if ((bi & 63) == lane) used |= 1u << (bi >> 6);
+    if (j == 0) top = bv;
+    const float w = routing_term(bv, top, scoring);
+    chosen += w;
+    if (lane == j) my_id = bi, my_w = w;
+  }
+  if (lane < k) {
+    const float by = over_all ? sum : scoring == kRouteSigmoid ? 1.0f : chosen;
+    ids[t * k + lane] = my_id;
+    weights[t * k + lane] = my_id < 0 ? 0.0f : my_w / by;
+  }
+}
+
+// Order of the rows of a grouped product and its tiles, in one block.  With
+// ids: the slots of each expert's rows (their order within an expert decides
+// no result: every output row depends on its own input row alone).  With
+// offsets: the groups as given, made non-decreasing and cut at P; the rows
+// before the first and after the last group become tiles of no expert.
+__global__ __launch_bounds__(1024) void plan_kernel(RoutePlan p) {
+  __shared__ int count[kMaxExperts + 2], first[kMaxExperts + 2], tile0[kMaxExperts + 2];
+  const int t = threadIdx.x;
+  if (t < p.E) count[t] = 0;
+  __syncthreads();
+  const int groups = p.ids ? p.E : p.E + 2;
+  if (p.ids) {
+    for (int i = t; i < p.P; i += 1024) {
+      const int e = p.ids[i];
+      if (e >= 0 && e < p.E) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+  }
+  if (t == 0) {                                // scan over the experts
+    int at = 0, tiles = 0;
+    if (!p.ids) {
+      at = min(max(p.offsets[0], 0), p.P);
+      first[0] = 0, count[0] = at, tile0[0] = 0;
+      tiles = (at + p.tile - 1) / p.tile;
+    }
+    for (int e = 0; e < p.E; ++e) {
+      const int g = p.ids ? e : e + 1;
+      const int c = p.ids ? count[e] : min(max(p.offsets[e + 1], at), p.P) - at;
+      first[g] = at, count[g] = c, tile0[g] = tiles;
+      at += c;
+      tiles += (c + p.tile - 1) / p.tile;
+    }
+    if (!p.ids) {
+      first[p.E + 1] = at, count[p.E + 1] = p.P - at, tile0[p.E + 1] = tiles;
+      tiles += (p.P - at + p.tile - 1) / p.tile;
+    }
+    *p.ntiles = tiles;
+  }
+  __syncthreads();
+  for (int g = t; g < groups; g += 1024)
+    for (int i = 0; i * p.tile < count[g]; ++i)
+      p.tiles[tile0[g] + i] = RowTile{p.ids ? g : (g == 0 || g == p.E + 1 ? -1 : g - 1), first[g] + i * p.tile,
+                                      min(p.tile, count[g] - i * p.tile), 0};
+  __syncthreads();
+  if (p.ids) {
+    for (int i = t; i < p.P; i += 1024) {
+      const int e = p.ids[i];
+      if (e >= 0 && e < p.E) p.perm[atomicAdd(&first[e], 1)] = i;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
+                                                      const float* __restrict__ weights,
+                                                      const uint16_t* __restrict__ res, int64_t T, int k, int E, int N,
+                                                      int type, int out_type, void* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / N;
+  const int n = (int)(i - t * N);
+  if (t >= T) return;
+  float y = res ? from_16(res[i], type) : 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int e = ids[t * k + j];
+    if (e >= 0 && e < E) y = fmaf(weights[t * k + j], part[(t * k + j) * N + n], y);
+  }
+  if (out_type == kTypeF32) ((float*)out)[i] = y;
+  else ((uint16_t*)out)[i] = to_16(y, out_type);
+}
+
+}  // namespace
+
+hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
+                        hipStream_t st) {
+  route_kernel<<<dim3((unsigned)((T + 3) / 4)), 256, 0, st>>>(logits, T, E, k, type, scoring, ids, weights);
+  return hipGetLastError();
+}
+
+hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {
+  plan_kernel<<<1, 1024, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
+                          int k, int E, int N, int type, int out_type, void* out, hipStream_t st) {
+  combine_kernel<<<dim3((unsigned)((T * N + 255) / 256)), 256, 0, st>>>(part, ids, weights, res, T, k, E, N, type,
+                                                                        out_type, out);
+  return hipGetLastError();
+}
+
+}  // namespace swq
