@@ -25,8 +25,8 @@ struct RowTile {
   int pad;
 };
 
-// y[row, n] = sum_k x[row / xdiv, k] w[expert(row)][n, k], or with w2 the SwiGLU
-// of two such sums.  Dense products: tiles null, one expert, rows = M.
+// out[row(slot), n] = sum_k x[xrow(slot), k] w[expert(slot)][n, k], or with w2 the
+// SwiGLU of two such sums.  Dense products: tiles null, one expert, rows = M.
 struct MxGemm {
   const uint16_t* x;
   int64_t plane;            // kXPlanes: elements between the two planes
@@ -39,13 +39,16 @@ struct MxGemm {
   int64_t out_plane;        // elements between the planes of a split hidden tensor
   int rows, K, N, E;
   int xsrc;                 // kXBf16, kXF16, kXPlanes
-  int xdiv;                 // row p reads x row p / xdiv
+  const int* xperm;         // slot -> row (x row: that / xdiv), or null: slot s reads x row s
+  int xdiv;
+  int xrows;                // rows of x behind xperm
+  int vec;                  // rows of out and the residual allow 8-byte (float32: 16-byte) accesses
   int type;                 // x's and the residual's 16-bit type
   int out_type;
   int hidden_planes;        // 1: write the hidden tensor as two bf16 planes
   const RowTile* tiles;     // tile table, or null
   const int* ntiles;
-  const int* perm;          // slot -> row, or null (the same)
+  const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
 };
 
@@ -75,8 +78,11 @@ hipError_t launch_mx4_quantize(const void* x, int64_t blocks, int type, uint32_t
                                hipStream_t st);
 hipError_t launch_mx4_dequantize(const uint32_t* codes, const uint8_t* scales, int64_t blocks, int type, void* out,
                                  hipStream_t st);
+// binary16 rows [n] to two bf16 planes, n a multiple of 8
+hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int64_t plane, hipStream_t st);
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st);
-int mx4_gemm_tile(const MxGemm& p);
+int mx4_gemm_tile(const MxGemm& p);           // row tile height that the launch takes, for the plan
+bool mx4_gemm_takes_planes(const MxGemm& p);  // binary16 x has to come as planes
 hipError_t launch_mx4_matmul(const Mx4Matmul& p, hipStream_t st);
 hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
                         hipStream_t st);

@@ -45,7 +45,29 @@ PlanLayout plan_layout(int64_t P, int64_t E, int tile, bool with_perm) {
   return l;
 }
 
-int run_plan(MxGemm& g, char* ws, const PlanLayout& l, const int* ids, const int* offsets, int tile, hipStream_t st) {
+// 4-wide stores: N and the bases allow them.
+int vec_ok(int64_t N, const void* out, const void* res, int out_type) {
+  return N % 4 == 0 && aligned(out, 4 * type_bytes(out_type)) && (!res || aligned(res, 8));
+}
+
+// x as the product's kernels read it: binary16 rows become two bf16 planes in
+// the workspace where they ask for it.
+int64_t planes_bytes(const MxGemm& g, int64_t rows) {
+  return g.xsrc == kXF16 && mx4_gemm_takes_planes(g) ? 2 * align256(rows * g.K * 2) : 0;
+}
+int to_planes(MxGemm& g, int64_t rows, void* ws, hipStream_t st) {
+  if (!planes_bytes(g, rows)) return SWQ_OK;
+  const int64_t plane = align256(rows * g.K * 2) / 2;
+  const int rc = check_status(launch_mx4_split(g.x, rows * g.K, (uint16_t*)ws, plane, st));
+  g.x = (const uint16_t*)ws;
+  g.plane = plane;
+  g.xsrc = kXPlanes;
+  return rc;
+}
+
+// Order and tiles of g's rows; with ids, *perm is the order.
+int run_plan(MxGemm& g, char* ws, const PlanLayout& l, const int* ids, const int* offsets, int tile, hipStream_t st,
+             const int** perm = nullptr) {
   RoutePlan r{};
   r.ids = ids;
   r.offsets = offsets;
@@ -55,9 +77,9 @@ int run_plan(MxGemm& g, char* ws, const PlanLayout& l, const int* ids, const int
   r.ntiles = (int*)ws;
   r.tiles = (RowTile*)(ws + l.tiles);
   r.perm = ids ? (int*)(ws + l.perm) : nullptr;
+  if (perm) *perm = r.perm;
   g.tiles = r.tiles;
   g.ntiles = r.ntiles;
-  g.perm = r.perm;
   g.max_tiles = (int)max_row_tiles(g.rows, g.E, tile);
   return check_status(launch_plan(r, st));
 }
@@ -112,6 +134,13 @@ int swiglu_q_mx4_linear(const void* x, const uint32_t* W, const void* s, const v
   g.xdiv = 1;
   g.type = type;
   g.out_type = out_mode;
+  g.vec = vec_ok(N, out, residual, out_mode);
+  if (const int64_t need = planes_bytes(g, M)) {
+    void* ws = nullptr;
+    rc = stream_workspace((hipStream_t)stream, (size_t)need, &ws, kWsSlot);
+    if (rc == SWQ_OK) rc = to_planes(g, M, ws, (hipStream_t)stream);
+    if (rc != SWQ_OK) return rc;
+  }
   (void)hipGetLastError();
   return check_status(launch_mx4_gemm(g, (hipStream_t)stream));
 }
@@ -158,13 +187,15 @@ int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uin
   g.xdiv = 1;
   g.type = type;
   g.out_type = out_mode;
+  g.vec = vec_ok(N, out, nullptr, out_mode);
   const int tile = mx4_gemm_tile(g);
   const PlanLayout l = plan_layout(P, E, tile, false);
   void* ws = nullptr;
-  rc = stream_workspace(stream, (size_t)l.total, &ws, kWsSlot);
+  rc = stream_workspace(stream, (size_t)(l.total + planes_bytes(g, P)), &ws, kWsSlot);
   if (rc != SWQ_OK) return rc;
   (void)hipGetLastError();
   rc = run_plan(g, (char*)ws, l, nullptr, offsets, tile, stream);
+  if (rc == SWQ_OK) rc = to_planes(g, P, (char*)ws + l.total, stream);
   if (rc != SWQ_OK) return rc;
   return check_status(launch_mx4_gemm(g, stream));
 }
@@ -196,6 +227,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   rc = check_shape(P, H, I);
   if (rc == SWQ_OK) rc = check_shape(P, I, Ho);
   if (rc != SWQ_OK) return rc;
+  if (T * H * 2 >= (int64_t(1) << 32) - 16) return SWQ_ERR_SHAPE;   // gathered rows are 32-bit byte offsets
   if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(out, type_bytes(out_mode)) ||
       !aligned(residual, 2))
     return SWQ_ERR_ALIGN;
@@ -216,17 +248,24 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   g.type = type;
   g.out_type = SWQ_TYPE_BF16;
   g.hidden_planes = f16;
+  g.xrows = (int)T;
+  g.vec = I % 4 == 0;
   const int tile = mx4_gemm_tile(g);
+  // workspace: the plan, the hidden tensor in the plan's order (two planes for
+  // binary16), the experts' outputs in the slots' order, x as planes
   const PlanLayout l = plan_layout(P, E, tile, true);
   const int64_t hidden = align256(P * I * 2) * (f16 ? 2 : 1);
-  const int64_t part = l.total + hidden;
+  const int64_t part = l.total + hidden, xplanes = part + align256(P * Ho * 4);
   void* ws_v = nullptr;
-  rc = stream_workspace(stream, (size_t)(part + align256(P * Ho * 4)), &ws_v, kWsSlot);
+  rc = stream_workspace(stream, (size_t)(xplanes + planes_bytes(g, T)), &ws_v, kWsSlot);
   if (rc != SWQ_OK) return rc;
   char* ws = (char*)ws_v;
   (void)hipGetLastError();
-  rc = run_plan(g, ws, l, ids, nullptr, tile, stream);
+  const int* perm = nullptr;
+  rc = run_plan(g, ws, l, ids, nullptr, tile, stream, &perm);
+  if (rc == SWQ_OK) rc = to_planes(g, T, ws + xplanes, stream);
   if (rc != SWQ_OK) return rc;
+  g.xperm = perm;
   g.out = ws + l.total;
   g.out_plane = align256(P * I * 2) / 2;
   rc = check_status(launch_mx4_gemm(g, stream));
@@ -234,17 +273,19 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   MxGemm d = g;
   d.x = (const uint16_t*)(ws + l.total);
   d.plane = g.out_plane;
+  d.xperm = nullptr;
   d.w = Wd;
   d.s = (const uint8_t*)sd;
   d.w2 = nullptr;
   d.s2 = nullptr;
   d.out = ws + part;
+  d.perm = perm;
   d.K = (int)I;
   d.N = (int)Ho;
   d.xsrc = f16 ? kXPlanes : kXBf16;
-  d.xdiv = 1;
   d.out_type = SWQ_TYPE_F32;
   d.hidden_planes = 0;
+  d.vec = Ho % 4 == 0;
   rc = check_status(launch_mx4_gemm(d, stream));
   if (rc != SWQ_OK) return rc;
   return check_status(launch_combine((const float*)(ws + part), ids, weights, (const uint16_t*)residual, T, (int)k,
