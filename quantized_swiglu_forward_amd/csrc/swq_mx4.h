@@ -50,6 +50,7 @@ struct MxGemm {
   const int* ntiles;
   const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
+  const int* ids;           // without tiles: the expert of every row (few rows, taken one by one), or null
 };
 
 struct Mx4Matmul {
@@ -83,6 +84,8 @@ hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int6
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st);
 int mx4_gemm_tile(const MxGemm& p);           // row tile height that the launch takes, for the plan
 bool mx4_gemm_takes_planes(const MxGemm& p);  // binary16 x has to come as planes
+// out[t] = res[t] + sum_j weights[t, j] x[t k + j] W[ids[t k + j]]^T for few tokens (p.rows = tokens k)
+hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st);
 hipError_t launch_mx4_matmul(const Mx4Matmul& p, hipStream_t st);
 hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
                         hipStream_t st);

@@ -9,6 +9,7 @@ using namespace swq;
 namespace {
 
 constexpr int kWsSlot = 2;            // the experts' workspace beside the MLP's two
+constexpr int64_t kDirectTokens = 4;  // most tokens whose slots are taken one by one
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 20;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -250,21 +251,28 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   g.hidden_planes = f16;
   g.xrows = (int)T;
   g.vec = I % 4 == 0;
+  // few tokens: every slot on its own, no plan, the weighted sum in the down
+  // projection.  Else by expert: the workspace holds the plan, the hidden
+  // tensor in the plan's order (two planes for binary16), the experts' outputs
+  // in the slots' order, and x as planes.
+  const bool direct = T <= kDirectTokens;
   const int tile = mx4_gemm_tile(g);
-  // workspace: the plan, the hidden tensor in the plan's order (two planes for
-  // binary16), the experts' outputs in the slots' order, x as planes
-  const PlanLayout l = plan_layout(P, E, tile, true);
+  const PlanLayout l = direct ? PlanLayout{0, 0, 0} : plan_layout(P, E, tile, true);
   const int64_t hidden = align256(P * I * 2) * (f16 ? 2 : 1);
-  const int64_t part = l.total + hidden, xplanes = part + align256(P * Ho * 4);
+  const int64_t part = l.total + hidden, xplanes = part + (direct ? 0 : align256(P * Ho * 4));
   void* ws_v = nullptr;
-  rc = stream_workspace(stream, (size_t)(xplanes + planes_bytes(g, T)), &ws_v, kWsSlot);
+  rc = stream_workspace(stream, (size_t)(xplanes + (direct ? 0 : planes_bytes(g, T))), &ws_v, kWsSlot);
   if (rc != SWQ_OK) return rc;
   char* ws = (char*)ws_v;
   (void)hipGetLastError();
   const int* perm = nullptr;
-  rc = run_plan(g, ws, l, ids, nullptr, tile, stream, &perm);
-  if (rc == SWQ_OK) rc = to_planes(g, T, ws + xplanes, stream);
-  if (rc != SWQ_OK) return rc;
+  if (direct) {
+    g.ids = ids;
+  } else {
+    rc = run_plan(g, ws, l, ids, nullptr, tile, stream, &perm);
+    if (rc == SWQ_OK) rc = to_planes(g, T, ws + xplanes, stream);
+    if (rc != SWQ_OK) return rc;
+  }
   g.xperm = perm;
   g.out = ws + l.total;
   g.out_plane = align256(P * I * 2) / 2;
@@ -286,6 +294,13 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   d.out_type = SWQ_TYPE_F32;
   d.hidden_planes = 0;
   d.vec = Ho % 4 == 0;
+  if (direct) {
+    d.res = (const uint16_t*)residual;
+    d.out = out;
+    d.out_type = out_mode;
+    d.vec = vec_ok(Ho, out, residual, out_mode);
+    return check_status(launch_mx4_down(d, weights, (int)k, stream));
+  }
   rc = check_status(launch_mx4_gemm(d, stream));
   if (rc != SWQ_OK) return rc;
   return check_status(launch_combine((const float*)(ws + part), ids, weights, (const uint16_t*)residual, T, (int)k,

@@ -18,15 +18,8 @@ namespace swq {
 namespace {
 
 constexpr int kTile = 16;
-
-__device__ __forceinline__ void load_x(const MxGemm& p, int64_t at, bf16x8& hi, bf16x8& lo) {
-  if (p.xsrc == kXF16) {
-    split_f16x8(*(const f16x8*)(p.x + at), hi, lo);
-  } else {
-    hi = *(const bf16x8*)(p.x + at);
-    if (p.xsrc == kXPlanes) lo = *(const bf16x8*)(p.x + p.plane + at);
-  }
-}
+// A buffer offset past every buffer's end: the load returns zeros and touches no memory.
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
 
 // XCD-aware order of the tiles: the hardware deals consecutive blocks to the
@@ -71,44 +64,232 @@ __device__ __forceinline__ void finish4(const MxGemm& p, int64_t at, int col, f3
   store4(p.out, at, col, p.N, p.vec, v, p.out_type);
 }
 
-// One wave per 16 x 16 outputs.
-__global__ __launch_bounds__(64) void mx4_tile_kernel(MxGemm p) {
-  const int lane = threadIdx.x, r = lane & 15, h = lane >> 4;
-  const int ntn = (p.N + kTile - 1) / kTile;
-  const int tm = blockIdx.x / ntn, n0 = (blockIdx.x % ntn) * kTile;
-  int expert = 0, first = tm * kTile, rows = min(kTile, p.rows - first);
+// ----------------------------------------------------------- few-row kernel ----
+//
+// Up to 16 RT rows against 16 CT columns per block (SwiGLU: of both matrices).
+// Here the weights' bytes count, not the sums: every wave takes chunks of
+// 128 inputs c = wave, wave + W, ... on its own, weights and x straight to
+// registers, U chunks of loads in flight, and the waves' sums meet in LDS at the
+// end.  No barrier stands between the loads.
+template <int RT, int CT, int XS, bool FUSED, int W, int U>
+__device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first, int rows, int n0, f32x4* lds) {
+  constexpr int NW = FUSED ? 2 * CT : CT, NP = XS == kXBf16 ? 1 : 2, NL = XS == kXPlanes ? 2 : 1;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h = lane >> 4;
+  f32x4 acc[RT][NW];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NW; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (expert >= 0) {
+    // x: rows past the tile's read zeros and touch no memory
+    const bool gather = p.xperm || p.ids;
+    const uint16_t* xb = gather ? p.x : p.x + (int64_t)first * p.K;
+    const uint32_t xbytes = (uint32_t)((int64_t)(gather ? p.xrows : rows) * p.K * 2);
+    __amdgpu_buffer_rsrc_t xr[NL];
+#pragma unroll
+    for (int q = 0; q < NL; ++q)
+      xr[q] = __builtin_amdgcn_make_buffer_rsrc((void*)(xb + q * p.plane), 0, (int)xbytes, 0x00020000);
+    uint32_t xoff[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int lr = 16 * i + r;
+      const int xrow = lr >= rows ? 0 : p.xperm ? p.xperm[first + lr] / p.xdiv : p.ids ? (first + lr) / p.xdiv : lr;
+      xoff[i] = lr >= rows ? kNowhere : (uint32_t)xrow * (uint32_t)p.K * 2u + h * 64;
+    }
+    const int kb = p.K / 32, chunks = (kb + 3) / 4;
+    const int64_t wrow = (int64_t)expert * p.N + n0;
+    const int cols = p.N - n0;
+    const int wbytes = min(cols, 16 * CT) * (p.K / 2);
+    const __amdgpu_buffer_rsrc_t wr[2] = {
+        __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + wrow * (p.K / 8)), 0, wbytes, 0x00020000),
+        __builtin_amdgcn_make_buffer_rsrc((void*)((FUSED ? p.w2 : p.w) + wrow * (p.K / 8)), 0, wbytes, 0x00020000)};
+    const uint8_t* sb[2] = {p.s + wrow * kb, (FUSED ? p.s2 : p.s) + wrow * kb};
+
+    for (int c0 = wave; c0 < chunks; c0 += W * U) {
+      u32x4 w[U][NW], x[U][NL][RT][4];
+      uint32_t s[U][NW];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * W;
+        const bool in = 4 * c + h < kb;
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+          const int col = 16 * (j % CT) + r;
+          w[u][j] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         wr[j / CT], in ? (uint32_t)col * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere, 0, 0));
+          s[u][j] = in ? sb[j / CT][(int64_t)min(col, cols - 1) * kb + 4 * c + h] : 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < NL; ++q)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[u][q][i][k] = __builtin_bit_cast(
+                  u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                             xr[q], in && xoff[i] != kNowhere ? xoff[i] + c * 256 + k * 16 : kNowhere, 0, 0));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          bf16x8 a[NW];
+#pragma unroll
+          for (int j = 0; j < NW; ++j) a[j] = mx4_word(w[u][j][k], e8m0_operand(s[u][j]));
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            bf16x8 b[NP];
+            if constexpr (XS == kXF16) {
+              split_f16x8(__builtin_bit_cast(f16x8, x[u][0][i][k]), b[0], b[NP - 1]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < NP; ++q) b[q] = __builtin_bit_cast(bf16x8, x[u][q % NL][i][k]);
+            }
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+#pragma unroll
+              for (int j = 0; j < NW; ++j) acc[i][j] = mfma_bf16(a[j], b[q], acc[i][j]);
+          }
+        }
+    }
+  }
+
+  // the waves' sums: [wave][i][j][lane], added in wave order
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NW; ++j) lds[((wave * RT + i) * NW + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int f = wave; f < RT * CT; f += W) {
+    const int i = f / CT, j = f % CT;
+    f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      g += lds[((v * RT + i) * NW + j) * 64 + lane];
+      if constexpr (FUSED) u += lds[((v * RT + i) * NW + j + CT) * 64 + lane];
+    }
+    if constexpr (FUSED) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = silu_times(g[e], u[e]);
+    }
+    const int lr = 16 * i + r;
+    if (lr < rows) {
+      const int row = p.perm ? p.perm[first + lr] : first + lr;
+      finish4(p, (int64_t)row * p.N, n0 + 16 * j + 4 * h, g);
+    }
+  }
+}
+
+// Rows of the block: a tile of the table, of a dense product, or the one row
+// (slot) of p.ids.
+template <int RT, int CT, int XS, bool FUSED, int W, int U>
+__global__ __launch_bounds__(64 * W) void mx4_few_kernel(MxGemm p) {
+  constexpr int F = RT * CT * (FUSED ? 2 : 1);
+  __shared__ f32x4 lds[W * F * 64];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int ntn = (p.N + 16 * CT - 1) / (16 * CT);
+  int tm = blockIdx.x / ntn;
+  const int tn = blockIdx.x - tm * ntn;
+  int expert = 0, first = tm * 16 * RT, rows = min(16 * RT, p.rows - first);
   if (p.tiles) {
     if (tm >= *p.ntiles) return;
     const RowTile t = p.tiles[tm];
     expert = t.expert, first = t.first, rows = t.rows;
+  } else if (p.ids) {
+    expert = p.ids[tm], first = tm, rows = 1;
+    if (expert < 0 || expert >= p.E) return;       // a skipped slot: nothing reads its row
   }
-  const int n = min(n0 + r, p.N - 1);
-  const int slot = first + min(r, rows - 1);
-  const int64_t xat = (int64_t)(p.xperm ? p.xperm[slot] / p.xdiv : slot) * p.K;
-  f32x4 g = {}, u = {};
-  if (expert >= 0) {
-    const int64_t wrow = (int64_t)expert * p.N + n;
-    const bool two = p.xsrc != kXBf16;
-    for (int kb = 0; kb < p.K / 32; ++kb) {
-      bf16x8 hi, lo;
-      load_x(p, xat + kb * 32 + 8 * h, hi, lo);
-      const int64_t word = wrow * (p.K / 8) + kb * 4 + h, sc = wrow * (p.K / 32) + kb;
-      const bf16x8 a = mx4_word(p.w[word], e8m0_operand(p.s[sc]));
-      g = mfma_bf16(a, hi, g);
-      if (two) g = mfma_bf16(a, lo, g);
-      if (p.w2) {
-        const bf16x8 b = mx4_word(p.w2[word], e8m0_operand(p.s2[sc]));
-        u = mfma_bf16(b, hi, u);
-        if (two) u = mfma_bf16(b, lo, u);
-      }
-    }
+  expert = __builtin_amdgcn_readfirstlane(expert);
+  first = __builtin_amdgcn_readfirstlane(first);
+  rows = __builtin_amdgcn_readfirstlane(rows);
+  if constexpr (RT > 1) {
+    if (rows <= 16) return few_rows<1, CT, XS, FUSED, W, 2>(p, expert, first, rows, tn * 16 * CT, lds);
   }
-  if (r >= rows) return;
-  if (p.w2) {
+  if constexpr (RT > 2) {
+    if (rows <= 32) return few_rows<2, CT, XS, FUSED, W, 1>(p, expert, first, rows, tn * 16 * CT, lds);
+  }
+  few_rows<RT, CT, XS, FUSED, W, U>(p, expert, first, rows, tn * 16 * CT, lds);
+}
+
+// The experts' down projection of few tokens, one row each, with the weighted
+// sum: block (token, 16 columns), wave v takes the token's slot v % k' and a share
+// of its inputs, and the waves' sums, times the slots' weights, are added in
+// wave order.  k' = k rounded up to a divisor or multiple of the W waves.
+template <int XS, int W>
+__global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float* __restrict__ weights, int k) {
+  constexpr int NL = XS == kXPlanes ? 2 : 1;
+  __shared__ f32x4 lds[W * 64];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h = lane >> 4;
+  const int ntn = (p.N + 15) / 16;
+  const int t = blockIdx.x / ntn, n0 = (blockIdx.x - t * ntn) * 16;
+  const int kb = p.K / 32, chunks = (kb + 3) / 4, cols = p.N - n0;
+  // waves per slot: the largest power of two that leaves no slot waiting
+  int share = W;
+  while (share > 1 && share * k > W) share >>= 1;
+  f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = wave / share; j < k; j += W / share) {
+    const int slot = t * k + j;
+    const int expert = __builtin_amdgcn_readfirstlane(p.ids[slot]);
+    if (expert < 0 || expert >= p.E) continue;
+    const float wt = weights[slot];
+    const int64_t wrow = (int64_t)expert * p.N + n0;
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.w + wrow * (p.K / 8)), 0, min(cols, 16) * (p.K / 2), 0x00020000);
+    const uint8_t* sb = p.s + (wrow + min(r, cols - 1)) * kb;
+    __amdgpu_buffer_rsrc_t xr[NL];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = silu_times(g[i], u[i]);
+    for (int q = 0; q < NL; ++q)
+      xr[q] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.x + q * p.plane + (int64_t)slot * p.K), 0, p.K * 2, 0x00020000);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int U = 2;
+    for (int c0 = wave % share; c0 < chunks; c0 += share * U) {
+      u32x4 w[U], x[U][NL][4];
+      uint32_t s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * share;
+        const bool in = 4 * c + h < kb;
+        w[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             wr, in ? (uint32_t)r * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere, 0, 0));
+        s[u] = in ? sb[4 * c + h] : 0u;
+#pragma unroll
+        for (int q = 0; q < NL; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[u][q][e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       xr[q], in && r == 0 ? c * 256 + h * 64 + e * 16 : kNowhere, 0, 0));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bf16x8 a = mx4_word(w[u][e], e8m0_operand(s[u]));
+#pragma unroll
+          for (int q = 0; q < NL; ++q) acc = mfma_bf16(a, __builtin_bit_cast(bf16x8, x[u][q][e]), acc);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = fmaf(wt, acc[e], sum[e]);
   }
-  finish4(p, (int64_t)(p.perm ? p.perm[slot] : slot) * p.N, n0 + 4 * h, g);
+  lds[wave * 64 + lane] = sum;
+  __syncthreads();
+  if (wave == 0 && r == 0) {
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < W; ++v) y += lds[v * 64 + lane];
+    finish4(p, (int64_t)t * p.N, n0 + 4 * h, y);
+  }
 }
 
 // ------------------------------------------------------------ tiled kernel ----
@@ -127,6 +308,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   constexpr int DMA = ROWS / (4 * W);           // loads per lane and chunk, four rows each per wave
   static_assert(ROWS % (4 * W) == 0 && (!FUSED || NF % 2 == 0));
   __shared__ __attribute__((aligned(1024))) char lds[2][ROWS * 256];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, h = lane >> 4;
   const int wm = wave / WN, wn = wave % WN;
@@ -173,7 +358,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
       for (int i = 0; i < DMA; ++i) {
         const uint32_t base = lds_addr(&lds[buf][(i * 4 * W + wave * 4) * 256]);
         dma16(xr[(i * 4 * W) / BM], __builtin_amdgcn_readfirstlane(base),
-              in ? xoff[i] + (uint32_t)c * 256u : 0xFFFFFFF0u);
+              in ? xoff[i] + (uint32_t)c * 256u : kNowhere);
       }
     };
 
@@ -204,7 +389,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
       for (int j = 0; j < NF; ++j) {
         const bool up = FUSED && j >= NF / 2;
         w[j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(up ? wr1 : wr0, in ? woff[j] + c * 64 : 0xFFFFFFF0u, 0, 0));
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(up ? wr1 : wr0, in ? woff[j] + c * 64 : kNowhere, 0, 0));
         s[j] = in ? (up ? s1 : s0)[(int64_t)scol[j] * kb + 4 * c + h] : 0u;
       }
     };
@@ -290,26 +475,26 @@ __global__ __launch_bounds__(64) void mx4_matmul_tile_kernel(Mx4Matmul p) {
   store4(p.out, m * p.N, n0 + 4 * h, p.N, false, acc, p.out_type);
 }
 
-// Tile shapes (rows): 0 the simple kernel, else the tiled one.
-struct GemmConfig {
-  int bm, bno;
-};
 }  // namespace
 
-static int pick(const MxGemm& p) {
-  if (const char* e = getenv("SWQ_MX4_CFG")) return atoi(e);
-  return p.rows <= 16 ? 0 : 1;
+// Kernel of a product: the few-row kernel below a row count, else the tiled one.
+// A grouped product goes by its rows per expert.
+static bool few(const MxGemm& p) {
+  if (const char* e = getenv("SWQ_MX4_FEW")) return p.rows / p.E < atoi(e);
+  return p.rows / p.E < 64;
 }
-static bool planes_of(const MxGemm& p) { return p.xsrc != kXBf16; }
+
+static int few_tiles(const MxGemm& p) {       // row tiles of 16 of the few-row kernel
+  if (p.ids && !p.tiles) return 1;
+  return p.tiles ? 4 : p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+}
 
 int mx4_gemm_tile(const MxGemm& p) {
-  const int c = pick(p);
-  if (c == 0) return 16;
-  const int bm = c == 3 ? 256 : c == 2 ? 128 : 64;
-  return planes_of(p) && bm == 256 ? 128 : bm;
+  if (few(p)) return 64;
+  return p.xsrc != kXBf16 ? 64 : 128;
 }
 
-bool mx4_gemm_takes_planes(const MxGemm& p) { return pick(p) != 0; }
+bool mx4_gemm_takes_planes(const MxGemm& p) { return !few(p); }
 
 template <int MF, int NF, int WM, int WN, int NP, bool FUSED>
 static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
@@ -321,23 +506,40 @@ static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int RT, int CT, int XS, bool FUSED, int W, int U>
+static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
+  const int64_t ntn = (p.N + 16 * CT - 1) / (16 * CT);
+  const int64_t ntm = p.tiles ? p.max_tiles : p.ids ? p.rows : (p.rows + 16 * RT - 1) / (16 * RT);
+  if (ntm * ntn >= (1LL << 31)) return hipErrorInvalidValue;
+  mx4_few_kernel<RT, CT, XS, FUSED, W, U><<<dim3((unsigned)(ntm * ntn)), 64 * W, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <int XS, bool FUSED>
+static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
+  const int rt = few_tiles(p);
+  if (rt == 1) return launch_few_as<1, 1, XS, FUSED, 8, 2>(p, st);
+  if (rt == 2) return launch_few_as<2, FUSED ? 1 : 2, XS, FUSED, 8, 1>(p, st);
+  return launch_few_as<4, FUSED ? 1 : 2, XS, FUSED, 8, 1>(p, st);
+}
+
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st) {
-  const int c = pick(p);
-  if (c == 0) {
-    const int64_t ntn = (p.N + kTile - 1) / kTile;
-    const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + kTile - 1) / kTile;
-    if (ntn * ntm >= (1LL << 31)) return hipErrorInvalidValue;
-    mx4_tile_kernel<<<dim3((unsigned)(ntn * ntm)), 64, 0, st>>>(p);
-    return hipGetLastError();
+  const bool fused = p.w2;
+  if ((p.ids && !p.tiles) || few(p)) {
+    if (p.xsrc == kXBf16) return fused ? launch_few<kXBf16, true>(p, st) : launch_few<kXBf16, false>(p, st);
+    if (p.xsrc == kXF16) return fused ? launch_few<kXF16, true>(p, st) : launch_few<kXF16, false>(p, st);
+    return fused ? launch_few<kXPlanes, true>(p, st) : launch_few<kXPlanes, false>(p, st);
   }
-  const bool two = planes_of(p), fused = p.w2;
-  if (c == 1) {
-    if (two) return fused ? launch_tiled<4, 2, 1, 8, 2, true>(p, st) : launch_tiled<4, 2, 1, 8, 2, false>(p, st);
-    return fused ? launch_tiled<4, 2, 1, 8, 1, true>(p, st) : launch_tiled<4, 2, 1, 8, 1, false>(p, st);
-  }
-  if (two) return fused ? launch_tiled<4, 4, 2, 4, 2, true>(p, st) : launch_tiled<4, 4, 2, 4, 2, false>(p, st);
-  if (c == 2) return fused ? launch_tiled<4, 4, 2, 4, 1, true>(p, st) : launch_tiled<4, 4, 2, 4, 1, false>(p, st);
-  return fused ? launch_tiled<8, 4, 2, 4, 1, true>(p, st) : launch_tiled<8, 4, 2, 4, 1, false>(p, st);
+  if (p.xsrc != kXBf16) return fused ? launch_tiled<4, 4, 1, 4, 2, true>(p, st) : launch_tiled<4, 4, 1, 4, 2, false>(p, st);
+  return fused ? launch_tiled<8, 4, 1, 4, 1, true>(p, st) : launch_tiled<8, 4, 1, 4, 1, false>(p, st);
+}
+
+hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st) {
+  const int64_t blocks = (int64_t)(p.rows / k) * ((p.N + 15) / 16);
+  if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+  if (p.xsrc == kXPlanes) mx4_down_kernel<kXPlanes, 16><<<dim3((unsigned)blocks), 1024, 0, st>>>(p, weights, k);
+  else mx4_down_kernel<kXBf16, 16><<<dim3((unsigned)blocks), 1024, 0, st>>>(p, weights, k);
+  return hipGetLastError();
 }
 
 namespace {
