@@ -42,7 +42,7 @@ struct MxGemm {
   const int* xperm;         // slot -> row (x row: that / xdiv), or null: slot s reads x row s
   int xdiv;
   int xrows;                // rows of x behind xperm
-  int vec;                  // rows of out and the residual allow 8-byte (float32: 16-byte) accesses
+  int vec;                  // rows of out and the residual allow accesses of 4 (1) or of 4 and 8 (2) outputs
   int type;                 // x's and the residual's 16-bit type
   int out_type;
   int hidden_planes;        // 1: write the hidden tensor as two bf16 planes
@@ -51,6 +51,13 @@ struct MxGemm {
   const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
   const int* ids;           // without tiles: the expert of every row (few rows, taken one by one), or null
+
+#ifdef __HIPCC__
+  // the parts of an output's way to memory that this product has
+  __device__ uint16_t* low_plane() const { return hidden_planes ? (uint16_t*)out + out_plane : nullptr; }
+  __device__ void add_residual(float* f, int64_t at) const;   // eight neighbours, 16-byte aligned
+  __device__ void add_one(float& f, int64_t at) const;
+#endif
 };
 
 struct Mx4Matmul {
@@ -60,6 +67,13 @@ struct Mx4Matmul {
   const uint8_t* s;
   void* out;
   int M, K, N, out_type;
+  int vec;                  // as MxGemm
+
+#ifdef __HIPCC__
+  __device__ uint16_t* low_plane() const { return nullptr; }
+  __device__ void add_residual(float*, int64_t) const {}
+  __device__ void add_one(float&, int64_t) const {}
+#endif
 };
 
 struct RoutePlan {
@@ -86,7 +100,9 @@ int mx4_gemm_tile(const MxGemm& p);           // row tile height that the launch
 bool mx4_gemm_takes_planes(const MxGemm& p);  // binary16 x has to come as planes
 // out[t] = res[t] + sum_j weights[t, j] x[t k + j] W[ids[t k + j]]^T for few tokens (p.rows = tokens k)
 hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st);
-hipError_t launch_mx4_matmul(const Mx4Matmul& p, hipStream_t st);
+// bytes of workspace that the product of two MXFP4 matrices takes (0: none)
+int64_t mx4_matmul_workspace(const Mx4Matmul& p);
+hipError_t launch_mx4_matmul(const Mx4Matmul& p, void* ws, hipStream_t st);
 hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
                         hipStream_t st);
 hipError_t launch_plan(const RoutePlan& p, hipStream_t st);

@@ -46,8 +46,9 @@ PlanLayout plan_layout(int64_t P, int64_t E, int tile, bool with_perm) {
   return l;
 }
 
-// 4-wide stores: N and the bases allow them.
+// Widths that N and the bases allow (MxGemm::vec).
 int vec_ok(int64_t N, const void* out, const void* res, int out_type) {
+  if (N % 8 == 0 && aligned(out, 16) && (!res || aligned(res, 16))) return 2;
   return N % 4 == 0 && aligned(out, 4 * type_bytes(out_type)) && (!res || aligned(res, 8));
 }
 
@@ -158,9 +159,15 @@ int swiglu_q_mx4_matmul(const uint32_t* A, const void* sa, const uint32_t* W, co
   if (rc != SWQ_OK) return rc;
   if (!aligned(out, type_bytes(out_mode))) return SWQ_ERR_ALIGN;
   if (M == 0) return SWQ_OK;
-  Mx4Matmul p{A, (const uint8_t*)sa, W, (const uint8_t*)sw, out, (int)M, (int)K, (int)N, out_mode};
+  Mx4Matmul p{A, (const uint8_t*)sa, W, (const uint8_t*)sw, out, (int)M, (int)K, (int)N, out_mode,
+              vec_ok(N, out, nullptr, out_mode)};
+  void* ws = nullptr;
+  if (const int64_t need = mx4_matmul_workspace(p)) {
+    rc = stream_workspace((hipStream_t)stream, (size_t)need, &ws, kWsSlot);
+    if (rc != SWQ_OK) return rc;
+  }
   (void)hipGetLastError();
-  return check_status(launch_mx4_matmul(p, (hipStream_t)stream));
+  return check_status(launch_mx4_matmul(p, ws, (hipStream_t)stream));
 }
 
 int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uint32_t* W, const void* s, int64_t P,
@@ -250,7 +257,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   g.out_type = SWQ_TYPE_BF16;
   g.hidden_planes = f16;
   g.xrows = (int)T;
-  g.vec = I % 4 == 0;
+  g.vec = 2;
   // few tokens: every slot on its own, no plan, the weighted sum in the down
   // projection.  Else by expert: the workspace holds the plan, the hidden
   // tensor in the plan's order (two planes for binary16), the experts' outputs
@@ -293,7 +300,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   d.xsrc = f16 ? kXPlanes : kXBf16;
   d.out_type = SWQ_TYPE_F32;
   d.hidden_planes = 0;
-  d.vec = Ho % 4 == 0;
+  d.vec = vec_ok(Ho, d.out, nullptr, SWQ_TYPE_F32);
   if (direct) {
     d.res = (const uint16_t*)residual;
     d.out = out;

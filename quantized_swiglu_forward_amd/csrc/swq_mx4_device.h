@@ -62,6 +62,12 @@ __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, uint32_t sa, u32x4 b, uint32_
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
+// What bf16 rounding leaves of a value, for a second bf16 operand (an infinity leaves nothing).
+__device__ __forceinline__ float bf16_rest(float f) {
+  const float hi = round_to_bf16(f);
+  return __builtin_isfinite(hi) ? f - hi : 0.0f;
+}
+
 // 16-bit output types by number (0 bf16, 2 binary16).
 __device__ __forceinline__ uint16_t to_16(float f, int type) { return type == 2 ? f32_to_f16(f) : f32_to_bf16(f); }
 __device__ __forceinline__ float from_16(uint16_t b, int type) { return type == 2 ? f16_to_f32(b) : bf16_to_f32(b); }

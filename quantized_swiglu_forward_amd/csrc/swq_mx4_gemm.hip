@@ -15,6 +15,17 @@
 #include "swq_mx4_device.h"
 
 namespace swq {
+
+__device__ __forceinline__ void MxGemm::add_residual(float* f, int64_t at) const {
+  if (!res) return;
+  const u32x4 q = *(const u32x4*)(res + at);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] += from_16((uint16_t)(q[i >> 1] >> (16 * (i & 1))), type);
+}
+__device__ __forceinline__ void MxGemm::add_one(float& f, int64_t at) const {
+  if (res) f += from_16(res[at], type);
+}
+
 namespace {
 
 constexpr int kTile = 16;
@@ -36,16 +47,68 @@ __device__ __forceinline__ bool tile_of(int b, int ntm, int ntn, int& tm, int& t
   return true;
 }
 
+// Sixteen rows of NT column tiles from a wave's accumulators (v[j]: lane 16 h + r has
+// columns 16 j + 4 h .. + 3 of row r) to memory, through the wave's own stretch
+// of LDS, so that a row leaves as whole lines: 16-byte stores of eight outputs (float32: two
+// stores), or one output per lane where the rows are not aligned for that.
+// row_at(i): the output row of the tile's row i; rows: how many there are.
+constexpr int flush_floats(int nt) { return 16 * (16 * nt + 4); }
+template <int NT, class Spec, class RowAt>
+__device__ __forceinline__ void flush16(const Spec& p, float* buf, const f32x4* v, int rows, int col0, RowAt row_at) {
+  constexpr int COLS = 16 * NT, LD = COLS + 4, UNITS = COLS / 8;
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  asm volatile("" ::: "memory");               // a wave's LDS accesses keep their order
+#pragma unroll
+  for (int j = 0; j < NT; ++j) *(f32x4*)(buf + r * LD + 16 * j + 4 * h) = v[j];
+  asm volatile("" ::: "memory");
+  if (p.vec == 2) {
+#pragma unroll
+    for (int i = 0; i < 16 * UNITS / 64; ++i) {
+      const int u = i * 64 + lane, lr = u / UNITS, c = (u % UNITS) * 8, col = col0 + c;
+      if (lr >= rows || col >= p.N) continue;
+      const f32x4 a = *(const f32x4*)(buf + lr * LD + c), b = *(const f32x4*)(buf + lr * LD + c + 4);
+      float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      const int64_t at = row_at(lr) * p.N + col;
+      p.add_residual(f, at);
+      if (p.out_type == kTypeF32) {
+        *(f32x4*)((float*)p.out + at) = (f32x4){f[0], f[1], f[2], f[3]};
+        *(f32x4*)((float*)p.out + at + 4) = (f32x4){f[4], f[5], f[6], f[7]};
+      } else {
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          q[e] = (uint32_t)to_16(f[2 * e], p.out_type) | (uint32_t)to_16(f[2 * e + 1], p.out_type) << 16;
+        *(u32x4*)((uint16_t*)p.out + at) = (u32x4){q[0], q[1], q[2], q[3]};
+        if (p.low_plane()) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            q[e] = (uint32_t)f32_to_bf16(bf16_rest(f[2 * e])) | (uint32_t)f32_to_bf16(bf16_rest(f[2 * e + 1])) << 16;
+          *(u32x4*)(p.low_plane() + at) = (u32x4){q[0], q[1], q[2], q[3]};
+        }
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int u = lane; u < 16 * COLS; u += 64) {
+      const int lr = u / COLS, c = u % COLS, col = col0 + c;
+      if (lr >= rows || col >= p.N) continue;
+      float f = buf[lr * LD + c];
+      const int64_t at = row_at(lr) * p.N + col;
+      p.add_one(f, at);
+      if (p.out_type == kTypeF32) ((float*)p.out)[at] = f;
+      else ((uint16_t*)p.out)[at] = to_16(f, p.out_type);
+      if (p.low_plane()) p.low_plane()[at] = f32_to_bf16(bf16_rest(f));
+    }
+  }
+}
+
 // Four neighbouring sums of one output row: residual, rounding, store.
 __device__ __forceinline__ void finish4(const MxGemm& p, int64_t at, int col, f32x4 v) {
   if (col >= p.N) return;
   if (p.hidden_planes) {
     f32x4 rest;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float hi = round_to_bf16(v[i]);
-      rest[i] = __builtin_isfinite(hi) ? v[i] - hi : 0.0f;
-    }
+    for (int i = 0; i < 4; ++i) rest[i] = bf16_rest(v[i]);
     store4(p.out, at, col, p.N, p.vec, v, kTypeBf16);
     store4((uint16_t*)p.out + p.out_plane, at, col, p.N, p.vec, rest, kTypeBf16);
     return;
@@ -433,26 +496,188 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
     }
   }
 
+  // the stretches of the waves overlay the x buffers
+  constexpr int NT = FUSED ? NF / 2 : NF;
+  static_assert(flush_floats(NT) * W * 4 <= (int)sizeof(lds));
+  float* buf = (float*)lds + wave * flush_floats(NT);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < MF; ++i) {
-    const int lr = (wm * MF + i) * 16 + r;
-    if (lr >= rows) continue;
-    const int row = p.perm ? p.perm[first + lr] : first + lr;
-    const int64_t at = (int64_t)row * p.N;
+    const int r0 = (wm * MF + i) * 16;
+    f32x4 v[NT];
 #pragma unroll
-    for (int j = 0; j < (FUSED ? NF / 2 : NF); ++j) {
-      const int col = n0 + 16 * (FUSED ? wn * (NF / 2) + j : wn * NF + j) + 4 * h;
-      f32x4 v = acc[i][j];
+    for (int j = 0; j < NT; ++j) {
+      v[j] = acc[i][j];
       if constexpr (FUSED) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = silu_times(v[e], acc[i][j + NF / 2][e]);
+        for (int e = 0; e < 4; ++e) v[j][e] = silu_times(v[j][e], acc[i][j + NF / 2][e]);
       }
-      finish4(p, at, col, v);
     }
+    flush16<NT>(p, buf, v, rows - r0, n0 + 16 * NT * wn, [&](int lr) {
+      const int slot = first + r0 + lr;
+      return (int64_t)(p.perm ? p.perm[slot] : slot);
+    });
   }
 }
 
-// Both operands MXFP4: 16 x 16 x 128 scaled MFMA, one block of 32 per lane.
+// ----------------------------------------------------- two MXFP4 operands ----
+//
+// 16 x 16 x 128 scaled MFMA: lane 16 h + r holds row r's block h of a step of
+// 128 inputs, 32 codes in four registers, and the byte of its scale operand
+// that the step selects.
+//
+// The scales' bytes lie K / 32 apart, at any address, and a step needs four per row.  A first
+// kernel lays them out as the MFMA takes them: for 16 rows and 512 inputs one
+// word per lane, byte s for step s (blocks past K: 0).
+__global__ __launch_bounds__(256) void mx4_scale_kernel(const uint8_t* __restrict__ sa, int M,
+                                                        const uint8_t* __restrict__ sw, int N, int kb, int groups,
+                                                        int pad_a, int pad_w, uint32_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [row][group][h]
+  const int h = (int)(i & 3);
+  const int64_t rg = i >> 2;
+  const int row = (int)(rg / groups), g = (int)(rg - (int64_t)row * groups);
+  if (row >= pad_a + pad_w) return;
+  const bool is_a = row < pad_a;
+  const int at = is_a ? row : row - pad_a;
+  const uint8_t* s = is_a ? sa : sw;
+  uint32_t v = 0;
+  if (at < (is_a ? M : N)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int b = 16 * g + 4 * e + h;
+      if (b < kb) v |= (uint32_t)s[(int64_t)at * kb + b] << (8 * e);
+    }
+  }
+  out[((int64_t)(row / 16) * groups + g) * 64 + 16 * h + (row & 15)] = v;
+}
+
+// 256 x 256 outputs per block, 2 x 2 waves of 128 x 128.  A stage is one step,
+// 256 rows of each operand (64 bytes a row), four stages in LDS; a step reads its
+// successor's operands into registers while its MFMAs run and starts the
+// loads of the stage four ahead.  16-byte unit h of a row sits at
+// h ^ (row / 4 & 3): the sixteen rows of a read lie in different banks.
+constexpr int kMmTile = 256, kMmStage = 2 * kMmTile * 64, kMmScales = 2 * kMmTile * 16;
+
+__global__ __launch_bounds__(256, 1) void mx4_matmul_kernel(Mx4Matmul p, const uint32_t* __restrict__ scales,
+                                                            int groups, int pad_a) {
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kMmStage + 2 * kMmScales];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h = lane >> 4;
+  const int wm = wave >> 1, wn = wave & 1;
+  int tm, tn;
+  if (!tile_of(blockIdx.x, (p.M + kMmTile - 1) / kMmTile, (p.N + kMmTile - 1) / kMmTile, tm, tn)) return;
+  const int m0 = tm * kMmTile, n0 = tn * kMmTile;
+  const int steps = (p.K + 127) / 128, row_bytes = p.K / 2;
+
+  // codes: wave w loads rows 16 (4 i + w) + lane / 4 of each operand, a row past the
+  // end repeating the tile's first
+  const int rows_a = min(kMmTile, p.M - m0), rows_w = min(kMmTile, p.N - n0);
+  const i32x4 ra = make_srsrc((const char*)p.a + (int64_t)m0 * row_bytes, (uint32_t)rows_a * row_bytes);
+  const i32x4 rw = make_srsrc((const char*)p.w + (int64_t)n0 * row_bytes, (uint32_t)rows_w * row_bytes);
+  const int lrow = wave * 16 + (lane >> 2);
+  const int unit = (lane & 3) ^ (lane >> 4);           // (row / 4 & 3) == lane / 16
+  uint32_t offa[4], offw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 64 * i + lrow;
+    offa[i] = (uint32_t)(row < rows_a ? row : 0) * row_bytes + unit * 16;
+    offw[i] = (uint32_t)(row < rows_w ? row : 0) * row_bytes + unit * 16;
+  }
+  const uint32_t lds0 = lds_addr(lds);
+  const auto stage = [&](int t, int slot) {
+    const bool in = t * 128 + unit * 32 < p.K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + slot * kMmStage + (i * 4 + wave) * 1024);
+      dma16(ra, base, in ? offa[i] + (uint32_t)t * 64u : kNowhere);
+      dma16(rw, base + kMmTile * 64, in ? offw[i] + (uint32_t)t * 64u : kNowhere);
+    }
+  };
+  // scales of a group of four steps: 16 row groups of 256 bytes for each operand, gathered
+  // 1 KB per load: lane l takes 16 bytes of row group 4 w + l / 16
+  const i32x4 rsa = make_srsrc(scales + (int64_t)(m0 / 16) * groups * 64, (uint32_t)(16 * groups * 256));
+  const i32x4 rsw = make_srsrc(scales + (int64_t)((pad_a + n0) / 16) * groups * 64, (uint32_t)(16 * groups * 256));
+  const uint32_t soff = (uint32_t)(4 * wave + (lane >> 4)) * groups * 256 + (lane & 15) * 16;
+  const auto stage_scales = [&](int g) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + 4 * kMmStage + (g & 1) * kMmScales + wave * 1024);
+    dma16(rsa, base, g < groups ? soff + g * 256 : kNowhere);
+    dma16(rsw, base + kMmTile * 16, g < groups ? soff + g * 256 : kNowhere);
+  };
+
+  f32x4 acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+
+  const uint32_t frag = r * 64 + ((h ^ (r >> 2)) * 16);
+  u32x4 a[2][8], w[2][8];
+  uint32_t sa[8], sw[8];
+  const auto read_codes = [&](int slot, u32x4* fa, u32x4* fw) {
+    const char* s = lds + slot * kMmStage + frag;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fa[i] = *(const u32x4*)(s + (wm * 8 + i) * 1024);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fw[j] = *(const u32x4*)(s + kMmTile * 64 + (wn * 8 + j) * 1024);
+  };
+  const auto read_scales = [&](int g, uint32_t* fa, uint32_t* fw) {
+    const char* s = lds + 4 * kMmStage + (g & 1) * kMmScales + lane * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fa[i] = *(const uint32_t*)(s + (wm * 8 + i) * 256);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fw[j] = *(const uint32_t*)(s + kMmTile * 16 + (wn * 8 + j) * 256);
+  };
+  const auto meet = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  stage_scales(0);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) stage(t, t);
+  wait_vmcnt<24>();
+  meet();
+  read_codes(0, a[0], w[0]);
+
+  // One step.  Loads are issued past the last step too (they read nothing), so the counts below hold to the end.
+  const auto step = [&]<int CUR>(int t) {
+    constexpr int NXT = CUR ^ 1;
+    wait_vmcnt<16>();          // all but the last two stages' loads: stage t + 1 is there
+    meet();
+    if ((t & 3) == 0) {
+      read_scales(t >> 2, sa, sw);
+      stage_scales((t >> 2) + 1);
+    }
+    stage(t + 4, t & 3);
+    read_codes((t + 1) & 3, a[NXT], w[NXT]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = mfma_mx4(w[CUR][j], sw[j], a[CUR][i], sa[i], acc[i][j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sa[i] >>= 8, sw[i] >>= 8;
+  };
+  for (int t = 0; t < steps; t += 2) {
+    step.template operator()<0>(t);
+    step.template operator()<1>(t + 1);
+  }
+  wait_vmcnt<0>();             // no load may write LDS after the block has left
+
+  meet();                      // the waves' stretches overlay the stages
+  float* buf = (float*)lds + wave * flush_floats(8);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r0 = m0 + (wm * 8 + i) * 16;
+    flush16<8>(p, buf, acc[i], p.M - r0, n0 + wn * 128, [&](int lr) { return (int64_t)(r0 + lr); });
+  }
+}
+
+// Few rows: one wave per 16 x 16 outputs, everything straight to registers.
 __global__ __launch_bounds__(64) void mx4_matmul_tile_kernel(Mx4Matmul p) {
   const int lane = threadIdx.x, r = lane & 15, h = lane >> 4;
   const int ntn = (p.N + kTile - 1) / kTile;
@@ -472,7 +697,7 @@ __global__ __launch_bounds__(64) void mx4_matmul_tile_kernel(Mx4Matmul p) {
     acc = mfma_mx4(w, sw, a, sa, acc);
   }
   if (m0 + r >= p.M) return;
-  store4(p.out, m * p.N, n0 + 4 * h, p.N, false, acc, p.out_type);
+  if (n0 + 4 * h < p.N) store4(p.out, m * p.N, n0 + 4 * h, p.N, p.vec, acc, p.out_type);
 }
 
 }  // namespace
@@ -560,10 +785,28 @@ hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int6
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_matmul(const Mx4Matmul& p, hipStream_t st) {
-  const int64_t tiles = (int64_t)((p.N + kTile - 1) / kTile) * ((p.M + kTile - 1) / kTile);
-  if (tiles >= (1LL << 31)) return hipErrorInvalidValue;
-  mx4_matmul_tile_kernel<<<dim3((unsigned)tiles), 64, 0, st>>>(p);
+static int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int64_t mx4_matmul_workspace(const Mx4Matmul& p) {
+  if (p.M < 64) return 0;
+  return (round_up(p.M, kMmTile) + round_up(p.N, kMmTile)) * ((p.K + 511) / 512) * 16;
+}
+
+hipError_t launch_mx4_matmul(const Mx4Matmul& p, void* ws, hipStream_t st) {
+  if (!ws) {
+    const int64_t tiles = (int64_t)((p.N + kTile - 1) / kTile) * ((p.M + kTile - 1) / kTile);
+    if (tiles >= (1LL << 31)) return hipErrorInvalidValue;
+    mx4_matmul_tile_kernel<<<dim3((unsigned)tiles), 64, 0, st>>>(p);
+    return hipGetLastError();
+  }
+  const int groups = (p.K + 511) / 512;
+  const int pad_a = (int)round_up(p.M, kMmTile), pad_w = (int)round_up(p.N, kMmTile);
+  const int64_t words = (int64_t)(pad_a + pad_w) * groups * 4;
+  mx4_scale_kernel<<<dim3((unsigned)((words + 255) / 256)), 256, 0, st>>>(p.sa, p.M, p.s, p.N, p.K / 32, groups, pad_a,
+                                                                        pad_w, (uint32_t*)ws);
+  const int64_t tiles = (int64_t)(pad_a / kMmTile) * (pad_w / kMmTile);
+  if (tiles >= (1LL << 30)) return hipErrorInvalidValue;
+  mx4_matmul_kernel<<<dim3((unsigned)round_up(tiles, 8)), 256, 0, st>>>(p, (const uint32_t*)ws, groups, pad_a);
   return hipGetLastError();
 }
 
