@@ -353,68 +353,102 @@ def mlp(x, wg, sg, bg, wu, su, bu, wd, sd, bd, spec_g, spec_u, spec_d, residual=
 #
 # Codes are int32 (or uint32) words [..., K/8], scales uint8 [..., K/32];
 # experts are a leading dimension.  Every tensor must be contiguous and on x's
-# device; types and shapes that the library does not take raise here.
+# GPU; types and shapes that the library does not take raise here.  A call
+# goes to the current stream of x's GPU unless it is given one.  Small calls
+# cost as much here as on the GPU, so the checks are kept short.
 
-def _mx4_types():
+_types = {}      # torch type -> SWQ_TYPE_*
+_dtypes = ()     # SWQ_TYPE_* -> torch type
+_words = ()      # types of codes
+_bytes = None    # type of scales
+
+
+def _load_types():
+    global _types, _dtypes, _words, _bytes
     import torch
-    return {torch.bfloat16: SWQ_TYPE_BF16, torch.float32: SWQ_TYPE_F32, torch.float16: SWQ_TYPE_F16}
-
-
-_types = None
+    _dtypes = (torch.bfloat16, torch.float32, torch.float16)
+    _words = (torch.int32, torch.uint32)
+    _bytes = torch.uint8
+    _types = {t: i for i, t in enumerate(_dtypes)}
+    return _types
 
 
 def _type(t, what, wide=True):
-    global _types
-    if _types is None:
-        _types = _mx4_types()
-    code = _types.get(t.dtype, -1)
+    code = (_types or _load_types()).get(t.dtype, -1)
     if code < 0 or (code == SWQ_TYPE_F32 and not wide):
         raise TypeError(f"{what}: {t.dtype} is not a supported type")
     return code
 
 
-def _dtype(code):
-    import torch
-    return (torch.bfloat16, torch.float32, torch.float16)[code]
-
-
 def _same_place(what, x, *tensors):
-    for t in (x,) + tensors:
-        if t is None:
-            continue
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: every tensor must be contiguous")
-        if not t.is_cuda or t.device != x.device:
-            raise ValueError(f"{what}: every tensor must be on one GPU")
+    """x's GPU; raises for a tensor that is elsewhere or not contiguous."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: every tensor must be on one GPU")
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: every tensor must be contiguous")
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError(f"{what}: every tensor must be on one GPU")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: every tensor must be contiguous")
+    return dev
 
 
-def _mx4_shape(codes, scales, what, K=None, dims=2):
-    """Rows (and experts) and K of a matrix of codes and scales."""
-    import torch
-    if codes.dtype not in (torch.int32, torch.uint32) or scales.dtype != torch.uint8:
+def _mx4_shape(codes, scales, what, K=-1, dims=2):
+    """The leading sizes of a matrix of codes and scales."""
+    _types or _load_types()
+    if codes.dtype not in _words or scales.dtype is not _bytes:
         raise TypeError(f"{what}: codes must be int32 or uint32 words and scales uint8")
-    k = codes.shape[-1] * 8
-    if codes.dim() != dims or scales.dim() != dims or codes.shape[:-1] != scales.shape[:-1] \
-            or scales.shape[-1] * 32 != k:
-        raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are not one "
+    c, s = codes.shape, scales.shape
+    if len(c) != dims or len(s) != dims or c[-1] != 4 * s[-1] or c[:-1] != s[:-1]:
+        raise ValueError(f"{what}: codes {tuple(c)} and scales {tuple(s)} are not one "
                          f"{dims}-dimensional MXFP4 matrix")
-    if K is not None and k != K:
-        raise ValueError(f"{what}: the weights have {k} inputs, x has {K}")
-    return tuple(codes.shape[:-1])
+    if K >= 0 and c[-1] * 8 != K:
+        raise ValueError(f"{what}: the weights have {c[-1] * 8} inputs, x has {K}")
+    return c[:-1]
 
 
 def _out(out, shape, dtype, x, what):
-    import torch
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=x.device)
-    if out.dtype != dtype or tuple(out.shape) != tuple(shape) or not out.is_contiguous() or out.device != x.device:
-        raise ValueError(f"{what}: out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {x.device}")
+        return x.new_empty(shape, dtype=dtype)
+    if out.dtype != dtype or out.shape != tuple(shape) or not out.is_contiguous() \
+            or out.get_device() != x.get_device():
+        raise ValueError(f"{what}: out must be a contiguous {dtype} tensor of shape {tuple(shape)} on x's GPU")
     return out
 
 
-def _raise_on(rc, what):
+def _out_mode(mode, t, what):
+    if mode is None:
+        return t
+    if mode != t and mode != SWQ_LINEAR_F32:
+        raise ValueError(f"{what}: out_mode must be x's type or SWQ_LINEAR_F32")
+    return mode
+
+
+def _residual(residual, x, shape, what):
+    if residual is None:
+        return None
+    if residual.dtype != x.dtype or residual.shape != tuple(shape):
+        raise ValueError(f"{what}: residual must be {x.dtype} of shape {tuple(shape)}")
+    return residual.data_ptr()
+
+
+def _call(fn, dev, stream, *args):
+    """The entry point on the stream (by default the current one) of GPU dev."""
+    import torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
     if rc != SWQ_OK:
-        raise SwigluQError(rc, what)
+        raise SwigluQError(rc, fn.__name__)
 
 
 def mx4_quantize(x, codes=None, scales=None, stream=None):
@@ -422,29 +456,30 @@ def mx4_quantize(x, codes=None, scales=None, stream=None):
     float16 or float32; K a multiple of 32)."""
     import torch
     t = _type(x, "mx4_quantize")
-    _same_place("mx4_quantize", x)
-    if x.dim() < 1 or x.shape[-1] % 32 or x.shape[-1] == 0:
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] % 32 or shape[-1] == 0:
         raise ValueError("mx4_quantize: the last dimension must be a positive multiple of 32")
-    K, lead = int(x.shape[-1]), tuple(x.shape[:-1])
+    dev = _same_place("mx4_quantize", x)
+    K, n, lead = shape[-1], x.numel(), shape[:-1]
     codes = _out(codes, lead + (K // 8,), torch.int32, x, "mx4_quantize codes")
     scales = _out(scales, lead + (K // 32,), torch.uint8, x, "mx4_quantize scales")
-    if x.numel():
-        _raise_on(swiglu_q_mx4_quantize(x, x.numel() // K, K, t, codes, scales, stream), "swiglu_q_mx4_quantize")
+    if n:
+        _call((_lib or lib()).swiglu_q_mx4_quantize, dev, stream, x.data_ptr(), n // K, K, t, codes.data_ptr(),
+              scales.data_ptr())
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, dtype=None, out=None, stream=None):
     """The values [..., K] of codes and scales, in bf16 (default), float16 or float32."""
-    import torch
-    dtype = torch.bfloat16 if dtype is None else dtype
-    _mx4_shape(codes, scales, "mx4_dequantize", dims=codes.dim())
-    _same_place("mx4_dequantize", codes, scales)
-    K = int(codes.shape[-1]) * 8
-    out = _out(out, tuple(codes.shape[:-1]) + (K,), dtype, codes, "mx4_dequantize")
-    t = _type(out, "mx4_dequantize")
-    if out.numel():
-        _raise_on(swiglu_q_mx4_dequantize(codes, scales, out.numel() // K, K, t, out, stream),
-                  "swiglu_q_mx4_dequantize")
+    lead = _mx4_shape(codes, scales, "mx4_dequantize", dims=codes.dim())
+    dtype = _dtypes[0] if dtype is None else dtype
+    dev = _same_place("mx4_dequantize", codes, scales)
+    K = codes.shape[-1] * 8
+    out = _out(out, lead + (K,), dtype, codes, "mx4_dequantize")
+    t, n = _type(out, "mx4_dequantize"), out.numel()
+    if n:
+        _call((_lib or lib()).swiglu_q_mx4_dequantize, dev, stream, codes.data_ptr(), scales.data_ptr(), n // K, K, t,
+              out.data_ptr())
     return out
 
 
@@ -452,19 +487,17 @@ def mx4_linear(x, w, s, residual=None, out_mode=None, out=None, stream=None):
     """``x W^T`` (+ residual) with MXFP4 W [N, K]: x [..., K] bf16 or float16.
     Returns ``out`` [..., N] in x's type, or float32 with SWQ_LINEAR_F32."""
     t = _type(x, "mx4_linear", wide=False)
-    K, lead = int(x.shape[-1]), tuple(x.shape[:-1])
+    K = x.shape[-1]
     N, = _mx4_shape(w, s, "mx4_linear", K)
-    out_mode = t if out_mode is None else out_mode
-    if out_mode not in (t, SWQ_LINEAR_F32):
-        raise ValueError("mx4_linear: out_mode must be x's type or SWQ_LINEAR_F32")
-    if residual is not None and (residual.dtype != x.dtype or tuple(residual.shape) != lead + (N,)):
-        raise ValueError(f"mx4_linear: residual must be {x.dtype} of shape {lead + (N,)}")
-    _same_place("mx4_linear", x, w, s, residual)
-    out = _out(out, lead + (N,), _dtype(out_mode), x, "mx4_linear")
-    if out.numel() == 0:
-        return out
-    _raise_on(swiglu_q_mx4_linear(x, w, s, residual, x.numel() // K, K, N, t, out_mode, out, stream),
-              "swiglu_q_mx4_linear")
+    mode = _out_mode(out_mode, t, "mx4_linear")
+    shape = x.shape[:-1] + (N,)
+    res = _residual(residual, x, shape, "mx4_linear")
+    dev = _same_place("mx4_linear", x, w, s, residual)
+    out = _out(out, shape, _dtypes[mode], x, "mx4_linear")
+    n = x.numel()
+    if n and N:
+        _call((_lib or lib()).swiglu_q_mx4_linear, dev, stream, x.data_ptr(), w.data_ptr(), s.data_ptr(), res, n // K, K,
+              N, t, mode, out.data_ptr())
     return out
 
 
@@ -472,16 +505,16 @@ def mx4_matmul(a, sa, w, sw, out_mode=SWQ_LINEAR_BF16, out=None, stream=None):
     """``A W^T`` of two MXFP4 matrices: A [..., K], W [N, K].  Returns ``out``
     [..., N] (SWQ_LINEAR_BF16, _F32 or _F16)."""
     lead = _mx4_shape(a, sa, "mx4_matmul", dims=a.dim())
-    K = int(a.shape[-1]) * 8
+    K = a.shape[-1] * 8
     N, = _mx4_shape(w, sw, "mx4_matmul", K)
     if out_mode not in (SWQ_LINEAR_BF16, SWQ_LINEAR_F32, SWQ_LINEAR_F16):
         raise ValueError("mx4_matmul: unknown out_mode")
-    _same_place("mx4_matmul", a, sa, w, sw)
-    out = _out(out, lead + (N,), _dtype(out_mode), a, "mx4_matmul")
-    if out.numel() == 0:
-        return out
-    _raise_on(swiglu_q_mx4_matmul(a, sa, w, sw, a.numel() * 8 // K, K, N, out_mode, out, stream),
-              "swiglu_q_mx4_matmul")
+    dev = _same_place("mx4_matmul", a, sa, w, sw)
+    out = _out(out, lead + (N,), _dtypes[out_mode], a, "mx4_matmul")
+    n = a.numel()
+    if n and N:
+        _call((_lib or lib()).swiglu_q_mx4_matmul, dev, stream, a.data_ptr(), sa.data_ptr(), w.data_ptr(), sw.data_ptr(),
+              n * 8 // K, K, N, out_mode, out.data_ptr())
     return out
 
 
@@ -493,19 +526,16 @@ def mx4_grouped_linear(x, offsets, w, s, out_mode=None, out=None, stream=None):
     t = _type(x, "mx4_grouped_linear", wide=False)
     if x.dim() != 2:
         raise ValueError("mx4_grouped_linear: x must be [rows, K]")
-    P, K = int(x.shape[0]), int(x.shape[1])
+    P, K = x.shape
     E, N = _mx4_shape(w, s, "mx4_grouped_linear", K, dims=3)
-    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,):
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,):
         raise ValueError(f"mx4_grouped_linear: offsets must be int32 [{E + 1}]")
-    out_mode = t if out_mode is None else out_mode
-    if out_mode not in (t, SWQ_LINEAR_F32):
-        raise ValueError("mx4_grouped_linear: out_mode must be x's type or SWQ_LINEAR_F32")
-    _same_place("mx4_grouped_linear", x, offsets, w, s)
-    out = _out(out, (P, N), _dtype(out_mode), x, "mx4_grouped_linear")
-    if out.numel() == 0:
-        return out
-    _raise_on(swiglu_q_mx4_grouped_linear(x, offsets, w, s, P, E, K, N, t, out_mode, out, stream),
-              "swiglu_q_mx4_grouped_linear")
+    mode = _out_mode(out_mode, t, "mx4_grouped_linear")
+    dev = _same_place("mx4_grouped_linear", x, offsets, w, s)
+    out = _out(out, (P, N), _dtypes[mode], x, "mx4_grouped_linear")
+    if P and N:
+        _call((_lib or lib()).swiglu_q_mx4_grouped_linear, dev, stream, x.data_ptr(), offsets.data_ptr(), w.data_ptr(),
+              s.data_ptr(), P, E, K, N, t, mode, out.data_ptr())
     return out
 
 
@@ -515,16 +545,16 @@ def route(logits, k, scoring=SWQ_ROUTE_SOFTMAX, ids=None, weights=None, stream=N
     fewer than k logits are above -inf."""
     import torch
     t = _type(logits, "route")
-    if logits.dim() < 1:
+    shape = logits.shape
+    if len(shape) < 1:
         raise ValueError("route: logits need at least one dimension")
-    _same_place("route", logits)
-    E, lead = int(logits.shape[-1]), tuple(logits.shape[:-1])
+    dev = _same_place("route", logits)
+    E, lead, n = shape[-1], shape[:-1], logits.numel()
     ids = _out(ids, lead + (k,), torch.int32, logits, "route ids")
     weights = _out(weights, lead + (k,), torch.float32, logits, "route weights")
-    if ids.numel() == 0:
-        return ids, weights
-    _raise_on(swiglu_q_route(logits, logits.numel() // max(E, 1), E, k, t, scoring, ids, weights, stream),
-              "swiglu_q_route")
+    if ids.numel() or n:
+        _call((_lib or lib()).swiglu_q_route, dev, stream, logits.data_ptr(), n // max(E, 1), E, k, t, scoring,
+              ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -537,7 +567,7 @@ def moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual=None, out_mode=Non
     SWQ_LINEAR_F32."""
     import torch
     t = _type(x, "moe_mlp", wide=False)
-    H, lead = int(x.shape[-1]), tuple(x.shape[:-1])
+    H, lead = x.shape[-1], x.shape[:-1]
     E, I = _mx4_shape(wg, sg, "moe_mlp gate", H, dims=3)
     if _mx4_shape(wu, su, "moe_mlp up", H, dims=3) != (E, I):
         raise ValueError("moe_mlp: gate and up differ in shape")
@@ -545,19 +575,18 @@ def moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual=None, out_mode=Non
     if Ed != E:
         raise ValueError(f"moe_mlp: {E} experts in the gate, {Ed} in the down projection")
     if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != weights.shape \
-            or tuple(ids.shape[:-1]) != lead or ids.dim() < 1:
-        raise ValueError(f"moe_mlp: ids must be int32 and weights float32 of shape {lead + ('k',)}")
-    out_mode = t if out_mode is None else out_mode
-    if out_mode not in (t, SWQ_LINEAR_F32):
-        raise ValueError("moe_mlp: out_mode must be x's type or SWQ_LINEAR_F32")
-    if residual is not None and (residual.dtype != x.dtype or tuple(residual.shape) != lead + (Ho,)):
-        raise ValueError(f"moe_mlp: residual must be {x.dtype} of shape {lead + (Ho,)}")
-    _same_place("moe_mlp", x, ids, weights, wg, sg, wu, su, wd, sd, residual)
-    out = _out(out, lead + (Ho,), _dtype(out_mode), x, "moe_mlp")
-    if out.numel() == 0:
-        return out
-    _raise_on(swiglu_q_moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual, x.numel() // H, int(ids.shape[-1]),
-                               E, H, I, Ho, t, out_mode, out, stream), "swiglu_q_moe_mlp")
+            or ids.dim() < 1 or ids.shape[:-1] != lead:
+        raise ValueError(f"moe_mlp: ids must be int32 and weights float32 of shape {tuple(lead) + ('k',)}")
+    mode = _out_mode(out_mode, t, "moe_mlp")
+    shape = lead + (Ho,)
+    res = _residual(residual, x, shape, "moe_mlp")
+    dev = _same_place("moe_mlp", x, ids, weights, wg, sg, wu, su, wd, sd, residual)
+    out = _out(out, shape, _dtypes[mode], x, "moe_mlp")
+    n = x.numel()
+    if n and Ho:
+        _call((_lib or lib()).swiglu_q_moe_mlp, dev, stream, x.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+              wg.data_ptr(), sg.data_ptr(), wu.data_ptr(), su.data_ptr(), wd.data_ptr(), sd.data_ptr(), res, n // H,
+              ids.shape[-1], E, H, I, Ho, t, mode, out.data_ptr())
     return out
 
 

@@ -110,6 +110,8 @@ hipError_t launch_plan(const RoutePlan& p, hipStream_t st);
 hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
                           int k, int E, int N, int type, int out_type, void* out, hipStream_t st);
 
+// Compute units of the current device (swq_api.hip).
+int device_cus();
 // The library's per-(device, stream) buffers (swq_api.hip).
 int stream_workspace(hipStream_t stream, size_t need, void** out, int slot);
 

@@ -72,6 +72,11 @@ __device__ __forceinline__ float bf16_rest(float f) {
 __device__ __forceinline__ uint16_t to_16(float f, int type) { return type == 2 ? f32_to_f16(f) : f32_to_bf16(f); }
 __device__ __forceinline__ float from_16(uint16_t b, int type) { return type == 2 ? f16_to_f32(b) : bf16_to_f32(b); }
 
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  return (uint32_t)to_16(a, TYPE) | (uint32_t)to_16(b, TYPE) << 16;
+}
+
 // Four consecutive outputs of one row, starting at column n of N.  `vec`: the
 // row and the base allow one wide store.
 __device__ __forceinline__ void store4(void* out, int64_t at, int n, int N, bool vec, f32x4 v, int type) {

@@ -11,6 +11,8 @@
 // binary16 rows are split into two bf16 operands (split_f16), exact too.
 #include <stdlib.h>
 
+#include <algorithm>
+
 #include "swq_mx4.h"
 #include "swq_mx4_device.h"
 
@@ -28,7 +30,6 @@ __device__ __forceinline__ void MxGemm::add_one(float& f, int64_t at) const {
 
 namespace {
 
-constexpr int kTile = 16;
 // A buffer offset past every buffer's end: the load returns zeros and touches no memory.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
@@ -54,13 +55,9 @@ __device__ __forceinline__ bool tile_of(int b, int ntm, int ntn, int& tm, int& t
 // row_at(i): the output row of the tile's row i; rows: how many there are.
 constexpr int flush_floats(int nt) { return 16 * (16 * nt + 4); }
 template <int NT, class Spec, class RowAt>
-__device__ __forceinline__ void flush16(const Spec& p, float* buf, const f32x4* v, int rows, int col0, RowAt row_at) {
+__device__ __forceinline__ void drain16(const Spec& p, const float* buf, int rows, int col0, RowAt row_at) {
   constexpr int COLS = 16 * NT, LD = COLS + 4, UNITS = COLS / 8;
-  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
-  asm volatile("" ::: "memory");               // a wave's LDS accesses keep their order
-#pragma unroll
-  for (int j = 0; j < NT; ++j) *(f32x4*)(buf + r * LD + 16 * j + 4 * h) = v[j];
-  asm volatile("" ::: "memory");
+  const int lane = threadIdx.x & 63;
   if (p.vec == 2) {
 #pragma unroll
     for (int i = 0; i < 16 * UNITS / 64; ++i) {
@@ -88,9 +85,9 @@ __device__ __forceinline__ void flush16(const Spec& p, float* buf, const f32x4* 
       }
     }
   } else {
-#pragma unroll 1
-    for (int u = lane; u < 16 * COLS; u += 64) {
-      const int lr = u / COLS, c = u % COLS, col = col0 + c;
+#pragma unroll 4
+    for (int i = 0; i < COLS / 4; ++i) {
+      const int u = i * 64 + lane, lr = u / COLS, c = u % COLS, col = col0 + c;
       if (lr >= rows || col >= p.N) continue;
       float f = buf[lr * LD + c];
       const int64_t at = row_at(lr) * p.N + col;
@@ -100,6 +97,37 @@ __device__ __forceinline__ void flush16(const Spec& p, float* buf, const f32x4* 
       if (p.low_plane()) p.low_plane()[at] = f32_to_bf16(bf16_rest(f));
     }
   }
+}
+
+template <int NT, class Spec, class RowAt>
+__device__ __forceinline__ void flush16(const Spec& p, float* buf, const f32x4* v, int rows, int col0, RowAt row_at) {
+  constexpr int LD = 16 * NT + 4;
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  asm volatile("" ::: "memory");               // a wave's LDS accesses keep their order
+#pragma unroll
+  for (int j = 0; j < NT; ++j) *(f32x4*)(buf + r * LD + 16 * j + 4 * h) = v[j];
+  asm volatile("" ::: "memory");
+  drain16<NT>(p, buf, rows, col0, row_at);
+}
+
+// Rows 16 q .. of 32 x 32 accumulators v[0 .. WF): lane 32 h + r has columns
+// 32 j + 8 e + 4 h .. + 3 of row r in elements 4 e .. 4 e + 3.
+template <int NT, int WF, class Spec, class RowAt>
+__device__ __forceinline__ void flush_half(const Spec& p, float* buf, const f32x16* v, int q, int rows, int col0,
+                                           RowAt row_at) {
+  constexpr int LD = 16 * NT + 4;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  asm volatile("" ::: "memory");
+  if ((r >> 4) == q) {
+#pragma unroll
+    for (int j = 0; j < WF; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *(f32x4*)(buf + (r & 15) * LD + 32 * j + 8 * e + 4 * h) =
+            (f32x4){v[j][4 * e], v[j][4 * e + 1], v[j][4 * e + 2], v[j][4 * e + 3]};
+  }
+  asm volatile("" ::: "memory");
+  drain16<NT>(p, buf, rows, col0, row_at);
 }
 
 // Four neighbouring sums of one output row: residual, rounding, store.
@@ -522,182 +550,330 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
 
 // ----------------------------------------------------- two MXFP4 operands ----
 //
-// 16 x 16 x 128 scaled MFMA: lane 16 h + r holds row r's block h of a step of
-// 128 inputs, 32 codes in four registers, and the byte of its scale operand
-// that the step selects.
+// 32 x 32 x 64 scaled MFMA: lane 32 h + r holds row r's block h of a k-step of 64
+// inputs, 32 codes in four registers, and the byte of its scale operand that
+// the k-step selects.  (The 16 x 16 x 128 form is held to 27 cycles where
+// its rate would be 16 -- 5.6 PFLOP/s on registers alone, zeros or not; this
+// one reaches 9.7 PFLOP/s on zeros and 6.4 on random codes, the card's power
+// limit.)
 //
-// The scales' bytes lie K / 32 apart, at any address, and a step needs four per row.  A first
-// kernel lays them out as the MFMA takes them: for 16 rows and 512 inputs one
-// word per lane, byte s for step s (blocks past K: 0).
+// The scales' bytes lie K / 32 apart, at any address, and a stage of 128
+// inputs needs four per row.  A first kernel lays them out as the MFMA takes
+// them: for 32 rows and a stage, two bytes per lane, byte e for k-step e
+// (blocks past K: 0).
 __global__ __launch_bounds__(256) void mx4_scale_kernel(const uint8_t* __restrict__ sa, int M,
-                                                        const uint8_t* __restrict__ sw, int N, int kb, int groups,
-                                                        int pad_a, int pad_w, uint32_t* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [row][group][h]
-  const int h = (int)(i & 3);
-  const int64_t rg = i >> 2;
-  const int row = (int)(rg / groups), g = (int)(rg - (int64_t)row * groups);
+                                                        const uint8_t* __restrict__ sw, int N, int kb, int stages,
+                                                        int pad_a, int pad_w, uint16_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [row][stage]
+  const int row = (int)(i / stages), t = (int)(i - (int64_t)row * stages);
   if (row >= pad_a + pad_w) return;
   const bool is_a = row < pad_a;
   const int at = is_a ? row : row - pad_a;
-  const uint8_t* s = is_a ? sa : sw;
-  uint32_t v = 0;
-  if (at < (is_a ? M : N)) {
+  const uint8_t* s = (is_a ? sa : sw) + (int64_t)at * kb;
+  const bool live = at < (is_a ? M : N);
+  uint32_t b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int b = 16 * g + 4 * e + h;
-      if (b < kb) v |= (uint32_t)s[(int64_t)at * kb + b] << (8 * e);
-    }
-  }
-  out[((int64_t)(row / 16) * groups + g) * 64 + 16 * h + (row & 15)] = v;
+  for (int e = 0; e < 4; ++e) b[e] = live && 4 * t + e < kb ? s[4 * t + e] : 0u;
+  uint16_t* o = out + ((int64_t)(row / 32) * stages + t) * 64 + (row & 31);
+  o[0] = (uint16_t)(b[0] | b[2] << 8);
+  o[32] = (uint16_t)(b[1] | b[3] << 8);
 }
 
-// 256 x 256 outputs per block, 2 x 2 waves of 128 x 128.  A stage is one step,
-// 256 rows of each operand (64 bytes a row), four stages in LDS; a step reads its
-// successor's operands into registers while its MFMAs run and starts the
-// loads of the stage four ahead.  16-byte unit h of a row sits at
-// h ^ (row / 4 & 3): the sixteen rows of a read lie in different banks.
-constexpr int kMmTile = 256, kMmStage = 2 * kMmTile * 64, kMmScales = 2 * kMmTile * 16;
+template <int E>
+__device__ __forceinline__ f32x16 mfma_mx4_wide(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x16 c) {
+  const i32x8 A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, E, (int)sa, E, (int)sb);
+}
 
-__global__ __launch_bounds__(256, 1) void mx4_matmul_kernel(Mx4Matmul p, const uint32_t* __restrict__ scales,
-                                                            int groups, int pad_a) {
-  __shared__ __attribute__((aligned(1024))) char lds[4 * kMmStage + 2 * kMmScales];
+// (a lambda that is not inlined would take its captures, buffer descriptors among them, from memory)
+#define SWQ_INLINE __attribute__((always_inline))
+
+// f.operator()<0>(), f.operator()<1>(), ...
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f.template operator()<I>();
+    each<N, I + 1>(f);
+  }
+}
+
+// As dma16, four bytes per lane.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma4(i32x4 rs, uint32_t lds_base, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               ::"s"(lds_base), "v"(voff), "s"(rs) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// A wave's 32 x 32 accumulators to aligned rows: lane 32 h + r has columns 8 e + 4 h .. + 3
+// of row r in elements 4 e ..; for 16-bit outputs the halves of the wave swap
+// pieces of two such quads, so that every lane stores eight neighbours.
+template <int TYPE, int AF, int WF>
+__device__ __forceinline__ void store_wide(const Mx4Matmul& p, const f32x16 (&acc)[AF][WF], int mw, int nw) {
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < AF; ++i) {
+    const int m = mw + 32 * i + r;
+    if (m >= p.M) continue;
+    const int64_t at = (int64_t)m * p.N;
+#pragma unroll
+    for (int j = 0; j < WF; ++j) {
+      const f32x16& v = acc[i][j];
+      if constexpr (TYPE == kTypeF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = nw + 32 * j + 8 * e + 4 * h;
+          if (col < p.N) *(f32x4*)((float*)p.out + at + col) = (f32x4){v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          uint32_t q[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t x = pack16<TYPE>(v[4 * e + 2 * k], v[4 * e + 2 * k + 1]);
+            const uint32_t y = pack16<TYPE>(v[4 * e + 4 + 2 * k], v[4 * e + 5 + 2 * k]);
+            const auto sw = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+            q[k] = sw[0];
+            q[2 + k] = sw[1];
+          }
+          const int col = nw + 32 * j + 8 * (e + h);
+          if (col < p.N) *(u32x4*)((uint16_t*)p.out + at + col) = (u32x4){q[0], q[1], q[2], q[3]};
+        }
+      }
+    }
+  }
+}
+
+// 64 AF x 64 WF outputs per tile, 2 x 2 waves of 32 AF x 32 WF.  A stage is 128 inputs, 64
+// bytes a row of each operand and its scales, S stages in LDS; a k-step reads
+// its successor's operands into registers while its MFMAs run, and a stage that
+// has been read makes room for the loads of the one S ahead.  16-byte unit u of a row sits at
+// u ^ (row / 4 & 3): the rows that a read touches lie in different banks.
+template <int AF, int WF, int S>
+struct MmShape {
+  static constexpr int BM = 64 * AF, BN = 64 * WF, ROWS = BM + BN;
+  static constexpr int CODES = ROWS * 64, STAGE = CODES + 2048, LDS = S * STAGE;
+  static constexpr int LOADS = ROWS / 64, PER = LOADS + 2;     // of one wave: codes, with the scales
+};
+
+template <int AF, int WF, int S, int OCC>
+__global__ __launch_bounds__(256, OCC) void mx4_matmul_kernel(Mx4Matmul p, const uint16_t* __restrict__ scales,
+                                                              int stages, int pad_a) {
+  using Sh = MmShape<AF, WF, S>;
+  constexpr int BM = Sh::BM, BN = Sh::BN;
+  __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int ntm = (p.M + BM - 1) / BM, ntn = (p.N + BN - 1) / BN, row_bytes = p.K / 2;
+  const int unit = (lane & 3) ^ (lane >> 4);           // (row / 4 & 3) == lane / 16
+
+  // One tile's loads.  Codes: load i of wave w takes rows 16 (4 i + w) + lane / 4 of the two operands put
+  // together, a row past the end repeating the tile's first.  Scales: load i of wave w
+  // takes the 128 bytes of row groups 8 i + 2 w and the next (the operands put together).
+  int m0 = 0, n0 = 0;
+  i32x4 ra, rw, rs[2];
+  uint32_t off[Sh::LOADS], soff[2];
+  const auto aim = [&](int block) SWQ_INLINE {
+    int tm, tn;
+    if (!tile_of(block, ntm, ntn, tm, tn)) return false;
+    m0 = tm * BM, n0 = tn * BN;
+    const int rows_a = min(BM, p.M - m0), rows_w = min(BN, p.N - n0);
+    ra = make_srsrc((const char*)p.a + (int64_t)m0 * row_bytes, (uint32_t)rows_a * row_bytes);
+    rw = make_srsrc((const char*)p.w + (int64_t)n0 * row_bytes, (uint32_t)rows_w * row_bytes);
+#pragma unroll
+    for (int i = 0; i < Sh::LOADS; ++i) {
+      const int row = 64 * i + wave * 16 + (lane >> 2), of = i < AF ? row : row - BM, n = i < AF ? rows_a : rows_w;
+      off[i] = (uint32_t)(of < n ? of : 0) * row_bytes + unit * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int grp = 8 * i + 2 * wave;
+      const bool of_a = grp < BM / 32;
+      rs[i] = make_srsrc(scales + (int64_t)(of_a ? m0 : pad_a + n0) / 32 * stages * 64,
+                         (uint32_t)(of_a ? BM : BN) / 32 * stages * 128);
+      soff[i] = grp < Sh::ROWS / 32 ? (uint32_t)(grp + h - (of_a ? 0 : BM / 32)) * stages * 128 + r * 4 : 0x80000000u;
+    }
+    return true;
+  };
+  const uint32_t lds0 = lds_addr(lds);
+  // load i of a stage: codes, then scales
+  const auto load = [&]<int i>(int t, int slot) SWQ_INLINE {
+    const uint32_t base = lds0 + slot * Sh::STAGE;
+    if constexpr (i < Sh::LOADS)
+      dma16(i < AF ? ra : rw, __builtin_amdgcn_readfirstlane(base + wave * 1024 + i * 4096),
+            t * 128 + unit * 32 < p.K ? off[i] + (uint32_t)t * 64u : kNowhere);
+    else
+      dma4(rs[i - Sh::LOADS], __builtin_amdgcn_readfirstlane(base + Sh::CODES + wave * 256 + (i - Sh::LOADS) * 1024),
+           t < stages ? soff[i - Sh::LOADS] + (uint32_t)t * 128u : kNowhere);
+  };
+
+  f32x16 acc[AF][WF];
+  u32x4 a[2][AF], w[2][WF];
+  uint32_t sa[2][AF], sw[2][WF];
+  // operand i of k-step k: first x's, then w's
+  const auto read_code = [&]<int k, int i>(int slot) SWQ_INLINE {
+    const char* s = lds + slot * Sh::STAGE + r * 64 + (((2 * k + h) ^ (r >> 2 & 3)) * 16);
+    if constexpr (i < AF) a[k][i] = *(const u32x4*)(s + (wm * AF + i) * 2048);
+    else w[k][i - AF] = *(const u32x4*)(s + BM * 64 + (wn * WF + i - AF) * 2048);
+  };
+  const auto read_scale = [&]<int set, int i>(int slot) SWQ_INLINE {
+    const char* s = lds + slot * Sh::STAGE + Sh::CODES + lane * 2;
+    if constexpr (i < AF) sa[set][i] = *(const uint16_t*)(s + (wm * AF + i) * 128);
+    else sw[set][i - AF] = *(const uint16_t*)(s + (2 * AF + wn * WF + i - AF) * 128);
+  };
+  const auto meet = [&]() SWQ_INLINE {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // A k-step's MFMAs; before(n) is issued in front of the n-th, so that one LDS
+  // read and one load at a time share its cycles.
+  const auto products = [&]<int E, int SET>(auto before) SWQ_INLINE {
+    each<AF * WF>([&]<int n>() SWQ_INLINE {
+      constexpr int i = n / WF, j = n % WF;
+      before.template operator()<n>();
+      acc[i][j] = mfma_mx4_wide<E>(w[E][j], sw[SET][j], a[E][i], sa[SET][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  const auto begin = [&]() SWQ_INLINE {
+    each<S>([&]<int t>() SWQ_INLINE { each<Sh::PER>([&]<int i>() SWQ_INLINE { load.template operator()<i>(t, t); }); });
+  };
+  // One stage.  Loads are issued past the last stage too (they read nothing),
+  // so the counts hold to the end.
+  constexpr int FRAGS = AF + WF, M = AF * WF;
+  constexpr int READS = (FRAGS + M - 1) / M, ISSUES = (Sh::PER + M - 1) / M;
+  int slot = 0;
+  const auto one = [&]<int SET>(int t) SWQ_INLINE {
+    products.template operator()<0, SET>([&]<int n>() SWQ_INLINE {
+      each<READS>([&]<int e>() SWQ_INLINE {
+        if constexpr (n * READS + e < FRAGS) read_code.template operator()<1, n * READS + e>(slot);
+      });
+    });
+    wait_vmcnt<(S - 2) * Sh::PER>();           // stage t + 1 is there
+    meet();
+    const int was = slot;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    products.template operator()<1, SET>([&]<int n>() SWQ_INLINE {
+      each<READS>([&]<int e>() SWQ_INLINE {
+        if constexpr (n * READS + e < FRAGS) {
+          read_code.template operator()<0, n * READS + e>(slot);
+          read_scale.template operator()<(SET ^ 1), n * READS + e>(slot);
+        }
+      });
+      each<ISSUES>([&]<int e>() SWQ_INLINE {
+        if constexpr (n * ISSUES + e < Sh::PER) load.template operator()<n * ISSUES + e>(t + S, was);
+      });
+    });
+  };
+
+  // The block's tiles, one after another: the next one's first loads are on their way
+  // while this one's sums go out.
+  int block = blockIdx.x;
+  if (!aim(block)) return;
+  begin();
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < AF; ++i)
+#pragma unroll
+      for (int j = 0; j < WF; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    wait_vmcnt<(S - 1) * Sh::PER>();
+    meet();
+    slot = 0;
+    each<FRAGS>([&]<int i>() SWQ_INLINE {
+      read_code.template operator()<0, i>(0);
+      read_scale.template operator()<0, i>(0);
+    });
+    for (int t = 0; t < stages; t += 2) {      // an odd count's last half adds zeros
+      one.template operator()<0>(t);
+      one.template operator()<1>(t + 1);
+    }
+    wait_vmcnt<0>();           // no load past the end may still write LDS
+    meet();
+
+    const int mw = m0 + wm * 32 * AF, nw = n0 + wn * 32 * WF;
+    if (p.vec != 2) {          // rows out of line: through LDS, one output per lane
+      constexpr int NT = 2 * WF;
+      static_assert(4 * flush_floats(NT) * 4 <= Sh::LDS);
+      float* buf = (float*)lds + wave * flush_floats(NT);
+#pragma unroll
+      for (int i = 0; i < AF; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          flush_half<NT, WF>(p, buf, acc[i], q, p.M - mw - 32 * i - 16 * q, nw,
+                             [&](int lr) SWQ_INLINE { return (int64_t)(mw + 32 * i + 16 * q + lr); });
+      meet();
+    }
+    block += gridDim.x;
+    const bool more = aim(block);
+    if (more) begin();
+    if (p.vec == 2) {
+      if (p.out_type == kTypeF32) store_wide<kTypeF32, AF, WF>(p, acc, mw, nw);
+      else if (p.out_type == kTypeF16) store_wide<kTypeF16, AF, WF>(p, acc, mw, nw);
+      else store_wide<kTypeBf16, AF, WF>(p, acc, mw, nw);
+    }
+    if (!more) break;
+  }
+}
+
+// Few rows of x: 16 x 16 outputs per block, everything straight to registers; the W
+// waves take steps of 128 inputs in turn, U of them in flight, and add their
+// sums in wave order.  (16 x 16 x 128 MFMA: lane 16 h + r holds row r's block h.)
+template <int W, int U>
+__global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
+  __shared__ f32x4 lds[W * 64];
 #ifdef SWQ_LDS_POISON
   lds_poison(lds, sizeof(lds), kPoisonFloat);
   __syncthreads();
 #endif
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, h = lane >> 4;
-  const int wm = wave >> 1, wn = wave & 1;
-  int tm, tn;
-  if (!tile_of(blockIdx.x, (p.M + kMmTile - 1) / kMmTile, (p.N + kMmTile - 1) / kMmTile, tm, tn)) return;
-  const int m0 = tm * kMmTile, n0 = tn * kMmTile;
-  const int steps = (p.K + 127) / 128, row_bytes = p.K / 2;
-
-  // codes: wave w loads rows 16 (4 i + w) + lane / 4 of each operand, a row past the
-  // end repeating the tile's first
-  const int rows_a = min(kMmTile, p.M - m0), rows_w = min(kMmTile, p.N - n0);
-  const i32x4 ra = make_srsrc((const char*)p.a + (int64_t)m0 * row_bytes, (uint32_t)rows_a * row_bytes);
-  const i32x4 rw = make_srsrc((const char*)p.w + (int64_t)n0 * row_bytes, (uint32_t)rows_w * row_bytes);
-  const int lrow = wave * 16 + (lane >> 2);
-  const int unit = (lane & 3) ^ (lane >> 4);           // (row / 4 & 3) == lane / 16
-  uint32_t offa[4], offw[4];
+  const int ntn = (p.N + 15) / 16;
+  const int m0 = (blockIdx.x / ntn) * 16, n0 = (blockIdx.x % ntn) * 16;
+  const int rows = min(16, p.M - m0), cols = min(16, p.N - n0);
+  const int blocks = p.K / 32, steps = (blocks + 3) / 4;
+  const int64_t m = m0 + min(r, rows - 1), n = n0 + min(r, cols - 1);
+  // rows past the end read zeros and touch no memory
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (int64_t)m0 * (p.K / 8)), 0, rows * (p.K / 2), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rw =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * (p.K / 8)), 0, cols * (p.K / 2), 0x00020000);
+  const uint32_t off = r * (p.K / 2) + h * 16;
+  const uint8_t* sa = p.sa + m * blocks;
+  const uint8_t* sw = p.s + n * blocks;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t0 = wave; t0 < steps; t0 += W * U) {
+    u32x4 a[U], w[U];
+    uint32_t fa[U], fw[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 64 * i + lrow;
-    offa[i] = (uint32_t)(row < rows_a ? row : 0) * row_bytes + unit * 16;
-    offw[i] = (uint32_t)(row < rows_w ? row : 0) * row_bytes + unit * 16;
-  }
-  const uint32_t lds0 = lds_addr(lds);
-  const auto stage = [&](int t, int slot) {
-    const bool in = t * 128 + unit * 32 < p.K;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + slot * kMmStage + (i * 4 + wave) * 1024);
-      dma16(ra, base, in ? offa[i] + (uint32_t)t * 64u : kNowhere);
-      dma16(rw, base + kMmTile * 64, in ? offw[i] + (uint32_t)t * 64u : kNowhere);
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * W;
+      const bool in = 4 * t + h < blocks;
+      a[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? off + t * 64 : kNowhere, 0, 0));
+      w[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? off + t * 64 : kNowhere, 0, 0));
+      fa[u] = in ? sa[4 * t + h] : 0u;
+      fw[u] = in ? sw[4 * t + h] : 0u;
     }
-  };
-  // scales of a group of four steps: 16 row groups of 256 bytes for each operand, gathered
-  // 1 KB per load: lane l takes 16 bytes of row group 4 w + l / 16
-  const i32x4 rsa = make_srsrc(scales + (int64_t)(m0 / 16) * groups * 64, (uint32_t)(16 * groups * 256));
-  const i32x4 rsw = make_srsrc(scales + (int64_t)((pad_a + n0) / 16) * groups * 64, (uint32_t)(16 * groups * 256));
-  const uint32_t soff = (uint32_t)(4 * wave + (lane >> 4)) * groups * 256 + (lane & 15) * 16;
-  const auto stage_scales = [&](int g) {
-    const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + 4 * kMmStage + (g & 1) * kMmScales + wave * 1024);
-    dma16(rsa, base, g < groups ? soff + g * 256 : kNowhere);
-    dma16(rsw, base + kMmTile * 16, g < groups ? soff + g * 256 : kNowhere);
-  };
-
-  f32x4 acc[8][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-
-  const uint32_t frag = r * 64 + ((h ^ (r >> 2)) * 16);
-  u32x4 a[2][8], w[2][8];
-  uint32_t sa[8], sw[8];
-  const auto read_codes = [&](int slot, u32x4* fa, u32x4* fw) {
-    const char* s = lds + slot * kMmStage + frag;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) fa[i] = *(const u32x4*)(s + (wm * 8 + i) * 1024);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) fw[j] = *(const u32x4*)(s + kMmTile * 64 + (wn * 8 + j) * 1024);
-  };
-  const auto read_scales = [&](int g, uint32_t* fa, uint32_t* fw) {
-    const char* s = lds + 4 * kMmStage + (g & 1) * kMmScales + lane * 4;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) fa[i] = *(const uint32_t*)(s + (wm * 8 + i) * 256);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) fw[j] = *(const uint32_t*)(s + kMmTile * 16 + (wn * 8 + j) * 256);
-  };
-  const auto meet = [&]() {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-
-  stage_scales(0);
-#pragma unroll
-  for (int t = 0; t < 4; ++t) stage(t, t);
-  wait_vmcnt<24>();
-  meet();
-  read_codes(0, a[0], w[0]);
-
-  // One step.  Loads are issued past the last step too (they read nothing), so the counts below hold to the end.
-  const auto step = [&]<int CUR>(int t) {
-    constexpr int NXT = CUR ^ 1;
-    wait_vmcnt<16>();          // all but the last two stages' loads: stage t + 1 is there
-    meet();
-    if ((t & 3) == 0) {
-      read_scales(t >> 2, sa, sw);
-      stage_scales((t >> 2) + 1);
-    }
-    stage(t + 4, t & 3);
-    read_codes((t + 1) & 3, a[NXT], w[NXT]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = mfma_mx4(w[CUR][j], sw[j], a[CUR][i], sa[i], acc[i][j]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sa[i] >>= 8, sw[i] >>= 8;
-  };
-  for (int t = 0; t < steps; t += 2) {
-    step.template operator()<0>(t);
-    step.template operator()<1>(t + 1);
+    for (int u = 0; u < U; ++u) acc = mfma_mx4(w[u], fw[u], a[u], fa[u], acc);
   }
-  wait_vmcnt<0>();             // no load may write LDS after the block has left
-
-  meet();                      // the waves' stretches overlay the stages
-  float* buf = (float*)lds + wave * flush_floats(8);
+  lds[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave != 0 || r >= rows || n0 + 4 * h >= p.N) return;
+  f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r0 = m0 + (wm * 8 + i) * 16;
-    flush16<8>(p, buf, acc[i], p.M - r0, n0 + wn * 128, [&](int lr) { return (int64_t)(r0 + lr); });
-  }
-}
-
-// Few rows: one wave per 16 x 16 outputs, everything straight to registers.
-__global__ __launch_bounds__(64) void mx4_matmul_tile_kernel(Mx4Matmul p) {
-  const int lane = threadIdx.x, r = lane & 15, h = lane >> 4;
-  const int ntn = (p.N + kTile - 1) / kTile;
-  const int m0 = (blockIdx.x / ntn) * kTile, n0 = (blockIdx.x % ntn) * kTile;
-  const int64_t n = min(n0 + r, p.N - 1), m = min(m0 + r, p.M - 1);
-  const int blocks = p.K / 32;
-  f32x4 acc = {};
-  for (int kb = 0; kb < blocks; kb += 4) {
-    u32x4 a = {}, w = {};
-    uint32_t sa = 0, sw = 0;
-    if (kb + h < blocks) {
-      a = ((const u32x4*)p.a)[m * blocks + kb + h];
-      w = ((const u32x4*)p.w)[n * blocks + kb + h];
-      sa = p.sa[m * blocks + kb + h];
-      sw = p.s[n * blocks + kb + h];
-    }
-    acc = mfma_mx4(w, sw, a, sa, acc);
-  }
-  if (m0 + r >= p.M) return;
-  if (n0 + 4 * h < p.N) store4(p.out, m * p.N, n0 + 4 * h, p.N, p.vec, acc, p.out_type);
+  for (int v = 0; v < W; ++v) y += lds[v * 64 + lane];
+  store4(p.out, m * p.N, n0 + 4 * h, p.N, p.vec, y, p.out_type);
 }
 
 }  // namespace
@@ -787,27 +963,53 @@ hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int6
 
 static int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+struct MatmulConfig {
+  int bm, bn;
+  hipError_t (*launch)(const Mx4Matmul&, const uint16_t*, int, int, hipStream_t);
+};
+
+template <int AF, int WF, int S, int OCC>
+static hipError_t launch_matmul_as(const Mx4Matmul& p, const uint16_t* ws, int stages, int pad_a, hipStream_t st) {
+  using Sh = MmShape<AF, WF, S>;
+  const int64_t tiles = (int64_t)((p.M + Sh::BM - 1) / Sh::BM) * ((p.N + Sh::BN - 1) / Sh::BN);
+  if (tiles >= (1LL << 30)) return hipErrorInvalidValue;
+  const int64_t blocks = std::min<int64_t>(round_up(tiles, 8), (int64_t)device_cus() / 8 * 8 * OCC);
+  mx4_matmul_kernel<AF, WF, S, OCC><<<dim3((unsigned)blocks), 256, 0, st>>>(p, ws, stages, pad_a);
+  return hipGetLastError();
+}
+
+static const MatmulConfig kMatmul[] = {
+    {128, 256, launch_matmul_as<2, 4, 3, 2>},
+    {128, 128, launch_matmul_as<2, 2, 4, 2>},
+    {64, 64, launch_matmul_as<1, 1, 7, 2>},
+};
+
+static const MatmulConfig* matmul_config(const Mx4Matmul& p) {
+  if (const char* e = getenv("SWQ_MX4_MM")) return atoi(e) < 0 ? nullptr : &kMatmul[atoi(e)];
+  if (p.M <= 32) return nullptr;
+  const auto tiles = [&](const MatmulConfig& c) { return round_up(p.M, c.bm) / c.bm * (round_up(p.N, c.bn) / c.bn); };
+  return tiles(kMatmul[0]) >= device_cus() ? &kMatmul[0] : tiles(kMatmul[1]) >= device_cus() / 2 ? &kMatmul[1] : &kMatmul[2];
+}
+
 int64_t mx4_matmul_workspace(const Mx4Matmul& p) {
-  if (p.M < 64) return 0;
-  return (round_up(p.M, kMmTile) + round_up(p.N, kMmTile)) * ((p.K + 511) / 512) * 16;
+  const MatmulConfig* c = matmul_config(p);
+  return c ? (round_up(p.M, c->bm) + round_up(p.N, c->bn)) * ((p.K + 127) / 128) * 4 : 0;
 }
 
 hipError_t launch_mx4_matmul(const Mx4Matmul& p, void* ws, hipStream_t st) {
-  if (!ws) {
-    const int64_t tiles = (int64_t)((p.N + kTile - 1) / kTile) * ((p.M + kTile - 1) / kTile);
+  const MatmulConfig* c = matmul_config(p);
+  if (!c) {
+    const int64_t tiles = (int64_t)((p.N + 15) / 16) * ((p.M + 15) / 16);
     if (tiles >= (1LL << 31)) return hipErrorInvalidValue;
-    mx4_matmul_tile_kernel<<<dim3((unsigned)tiles), 64, 0, st>>>(p);
+    mx4_matmul_few_kernel<8, 2><<<dim3((unsigned)tiles), 512, 0, st>>>(p);
     return hipGetLastError();
   }
-  const int groups = (p.K + 511) / 512;
-  const int pad_a = (int)round_up(p.M, kMmTile), pad_w = (int)round_up(p.N, kMmTile);
-  const int64_t words = (int64_t)(pad_a + pad_w) * groups * 4;
-  mx4_scale_kernel<<<dim3((unsigned)((words + 255) / 256)), 256, 0, st>>>(p.sa, p.M, p.s, p.N, p.K / 32, groups, pad_a,
-                                                                        pad_w, (uint32_t*)ws);
-  const int64_t tiles = (int64_t)(pad_a / kMmTile) * (pad_w / kMmTile);
-  if (tiles >= (1LL << 30)) return hipErrorInvalidValue;
-  mx4_matmul_kernel<<<dim3((unsigned)round_up(tiles, 8)), 256, 0, st>>>(p, (const uint32_t*)ws, groups, pad_a);
-  return hipGetLastError();
+  const int stages = (p.K + 127) / 128;
+  const int pad_a = (int)round_up(p.M, c->bm), pad_w = (int)round_up(p.N, c->bn);
+  const int64_t threads = (int64_t)(pad_a + pad_w) * stages;
+  mx4_scale_kernel<<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(p.sa, p.M, p.s, p.N, p.K / 32, stages, pad_a,
+                                                                          pad_w, (uint16_t*)ws);
+  return c->launch(p, (const uint16_t*)ws, stages, pad_a, st);
 }
 
 }  // namespace swq

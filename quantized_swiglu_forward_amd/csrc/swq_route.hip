@@ -127,21 +127,55 @@ __global__ __launch_bounds__(1024) void plan_kernel(RoutePlan p) {
   }
 }
 
+// One thread per V neighbours of an output row: the k partial rows are read four slots
+// at a time, each slot's id and weight first.
+template <int V>
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
                                                       const float* __restrict__ weights,
                                                       const uint16_t* __restrict__ res, int64_t T, int k, int E, int N,
                                                       int type, int out_type, void* __restrict__ out) {
+  const int per = N / V;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = i / N;
-  const int n = (int)(i - t * N);
+  const int64_t t = i / per;
+  const int n = (int)(i - t * per) * V;
   if (t >= T) return;
-  float y = res ? from_16(res[i], type) : 0.0f;
-  for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j];
-    if (e >= 0 && e < E) y = fmaf(weights[t * k + j], part[(t * k + j) * N + n], y);
+  const int64_t at = t * N + n;
+  float y[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) y[v] = res ? from_16(res[at + v], type) : 0.0f;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    float p[4][V], w[4];
+    bool on[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t slot = t * k + j0 + j;
+      const int e = j0 + j < k ? ids[slot] : -1;
+      on[j] = e >= 0 && e < E;
+      w[j] = on[j] ? weights[slot] : 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[j][v] = 0.0f;
+      if (on[j]) {
+        if constexpr (V == 4) {
+          const f32x4 q = *(const f32x4*)(part + slot * N + n);
+#pragma unroll
+          for (int v = 0; v < V; ++v) p[j][v] = q[v];
+        } else {
+          p[j][0] = part[slot * N + n];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = on[j] ? fmaf(w[j], p[j][v], y[v]) : y[v];
   }
-  if (out_type == kTypeF32) ((float*)out)[i] = y;
-  else ((uint16_t*)out)[i] = to_16(y, out_type);
+  if constexpr (V == 4) {
+    store4(out, at - n, n, N, true, (f32x4){y[0], y[1], y[2], y[3]}, out_type);
+  } else if (out_type == kTypeF32) {
+    ((float*)out)[at] = y[0];
+  } else {
+    ((uint16_t*)out)[at] = to_16(y[0], out_type);
+  }
 }
 
 }  // namespace
@@ -159,8 +193,12 @@ hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {
 
 hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
                           int k, int E, int N, int type, int out_type, void* out, hipStream_t st) {
-  combine_kernel<<<dim3((unsigned)((T * N + 255) / 256)), 256, 0, st>>>(part, ids, weights, res, T, k, E, N, type,
-                                                                        out_type, out);
+  const bool wide = N % 4 == 0 && (uintptr_t)out % (4 * type_bytes(out_type)) == 0;
+  const int64_t threads = T * (wide ? N / 4 : N);
+  if ((threads + 255) / 256 >= (1LL << 31)) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((threads + 255) / 256));
+  if (wide) combine_kernel<4><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, type, out_type, out);
+  else combine_kernel<1><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, type, out_type, out);
   return hipGetLastError();
 }
 
