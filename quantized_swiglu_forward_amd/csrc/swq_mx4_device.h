@@ -13,6 +13,10 @@
 
 #include "swq_device.h"
 
+// A lambda that is not inlined would take its captures, buffer descriptors among
+// them, from memory.
+#define SWQ_INLINE __attribute__((always_inline))
+
 namespace swq {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

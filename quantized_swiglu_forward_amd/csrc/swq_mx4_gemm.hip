@@ -33,6 +33,19 @@ namespace {
 // A buffer offset past every buffer's end: the load returns zeros and touches no memory.
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
+// Loads through a buffer descriptor.  What is out of range is asked for at
+// kNowhere instead of being branched around: a branch around a load makes the
+// compiler wait for every load in flight where the paths meet.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+}
+__device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b8(b, off, 0, 0);
+}
+
 
 // XCD-aware order of the tiles: the hardware deals consecutive blocks to the
 // eight XCDs in turn, so block b takes tile b / 8 of a contiguous eighth of the
@@ -180,8 +193,7 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
     const uint32_t xbytes = (uint32_t)((int64_t)(gather ? p.xrows : rows) * p.K * 2);
     __amdgpu_buffer_rsrc_t xr[NL];
 #pragma unroll
-    for (int q = 0; q < NL; ++q)
-      xr[q] = __builtin_amdgcn_make_buffer_rsrc((void*)(xb + q * p.plane), 0, (int)xbytes, 0x00020000);
+    for (int q = 0; q < NL; ++q) xr[q] = buffer(xb + q * p.plane, xbytes);
     uint32_t xoff[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -193,10 +205,10 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
     const int64_t wrow = (int64_t)expert * p.N + n0;
     const int cols = p.N - n0;
     const int wbytes = min(cols, 16 * CT) * (p.K / 2);
-    const __amdgpu_buffer_rsrc_t wr[2] = {
-        __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + wrow * (p.K / 8)), 0, wbytes, 0x00020000),
-        __builtin_amdgcn_make_buffer_rsrc((void*)((FUSED ? p.w2 : p.w) + wrow * (p.K / 8)), 0, wbytes, 0x00020000)};
-    const uint8_t* sb[2] = {p.s + wrow * kb, (FUSED ? p.s2 : p.s) + wrow * kb};
+    const __amdgpu_buffer_rsrc_t wr[2] = {buffer(p.w + wrow * (p.K / 8), wbytes),
+                                          buffer((FUSED ? p.w2 : p.w) + wrow * (p.K / 8), wbytes)};
+    const __amdgpu_buffer_rsrc_t sr[2] = {buffer(p.s + wrow * kb, wbytes / 16),
+                                          buffer((FUSED ? p.s2 : p.s) + wrow * kb, wbytes / 16)};
 
     for (int c0 = wave; c0 < chunks; c0 += W * U) {
       u32x4 w[U][NW], x[U][NL][RT][4];
@@ -208,10 +220,8 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
 #pragma unroll
         for (int j = 0; j < NW; ++j) {
           const int col = 16 * (j % CT) + r;
-          w[u][j] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                         wr[j / CT], in ? (uint32_t)col * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere, 0, 0));
-          s[u][j] = in ? sb[j / CT][(int64_t)min(col, cols - 1) * kb + 4 * c + h] : 0u;
+          w[u][j] = load16(wr[j / CT], in ? (uint32_t)col * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere);
+          s[u][j] = load1(sr[j / CT], in ? (uint32_t)(col * kb + 4 * c + h) : kNowhere);
         }
 #pragma unroll
         for (int q = 0; q < NL; ++q)
@@ -219,9 +229,7 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
           for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              x[u][q][i][k] = __builtin_bit_cast(
-                  u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                             xr[q], in && xoff[i] != kNowhere ? xoff[i] + c * 256 + k * 16 : kNowhere, 0, 0));
+              x[u][q][i][k] = load16(xr[q], in && xoff[i] != kNowhere ? xoff[i] + c * 256 + k * 16 : kNowhere);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -335,13 +343,11 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
     if (expert < 0 || expert >= p.E) continue;
     const float wt = weights[slot];
     const int64_t wrow = (int64_t)expert * p.N + n0;
-    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.w + wrow * (p.K / 8)), 0, min(cols, 16) * (p.K / 2), 0x00020000);
-    const uint8_t* sb = p.s + (wrow + min(r, cols - 1)) * kb;
+    const __amdgpu_buffer_rsrc_t wr = buffer(p.w + wrow * (p.K / 8), min(cols, 16) * (p.K / 2));
+    const __amdgpu_buffer_rsrc_t sr = buffer(p.s + wrow * kb, min(cols, 16) * kb);
     __amdgpu_buffer_rsrc_t xr[NL];
 #pragma unroll
-    for (int q = 0; q < NL; ++q)
-      xr[q] = __builtin_amdgcn_make_buffer_rsrc((void*)(p.x + q * p.plane + (int64_t)slot * p.K), 0, p.K * 2, 0x00020000);
+    for (int q = 0; q < NL; ++q) xr[q] = buffer(p.x + q * p.plane + (int64_t)slot * p.K, p.K * 2);
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     constexpr int U = 2;
     for (int c0 = wave % share; c0 < chunks; c0 += share * U) {
@@ -351,15 +357,13 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
       for (int u = 0; u < U; ++u) {
         const int c = c0 + u * share;
         const bool in = 4 * c + h < kb;
-        w[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             wr, in ? (uint32_t)r * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere, 0, 0));
-        s[u] = in ? sb[4 * c + h] : 0u;
+        w[u] = load16(wr, in ? (uint32_t)r * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere);
+        s[u] = load1(sr, in ? (uint32_t)(r * kb + 4 * c + h) : kNowhere);
 #pragma unroll
         for (int q = 0; q < NL; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[u][q][e] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       xr[q], in && r == 0 ? c * 256 + h * 64 + e * 16 : kNowhere, 0, 0));
+            x[u][q][e] = load16(xr[q], in && r == 0 ? c * 256 + h * 64 + e * 16 : kNowhere);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -457,21 +461,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
     const int kb = p.K / 32;
     const int64_t wrow = (int64_t)expert * p.N + n0;
     const int wn_rows = p.N - n0;
-    uint32_t woff[NF];
-    int scol[NF];
+    uint32_t woff[NF], soff[NF];
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
       const int col = FUSED ? 16 * (wn * (NF / 2) + j % (NF / 2)) + r : 16 * (wn * NF + j) + r;
       woff[j] = (uint32_t)col * (uint32_t)(p.K / 2) + h * 16;
-      scol[j] = min(col, wn_rows - 1);
+      soff[j] = (uint32_t)col * (uint32_t)kb + h;
     }
-    const __amdgpu_buffer_rsrc_t wr0 = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.w + wrow * (p.K / 8)), 0, (int)min((int64_t)wn_rows, (int64_t)BNO) * (p.K / 2), 0x00020000);
-    const __amdgpu_buffer_rsrc_t wr1 = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)((FUSED ? p.w2 : p.w) + wrow * (p.K / 8)), 0, (int)min((int64_t)wn_rows, (int64_t)BNO) * (p.K / 2),
-        0x00020000);
-    const uint8_t* s0 = p.s + wrow * kb;
-    const uint8_t* s1 = (FUSED ? p.s2 : p.s) + wrow * kb;
+    const __amdgpu_buffer_rsrc_t wr0 = buffer(p.w + wrow * (p.K / 8), min(wn_rows, BNO) * (p.K / 2));
+    const __amdgpu_buffer_rsrc_t wr1 =
+        buffer((FUSED ? p.w2 : p.w) + wrow * (p.K / 8), min(wn_rows, BNO) * (p.K / 2));
+    const __amdgpu_buffer_rsrc_t sr0 = buffer(p.s + wrow * kb, min(wn_rows, BNO) * kb);
+    const __amdgpu_buffer_rsrc_t sr1 = buffer((FUSED ? p.s2 : p.s) + wrow * kb, min(wn_rows, BNO) * kb);
     u32x4 wc[NF];
     uint32_t sc[NF];
     const auto load_w = [&](int c, u32x4* w, uint32_t* s) {
@@ -479,9 +480,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
         const bool up = FUSED && j >= NF / 2;
-        w[j] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(up ? wr1 : wr0, in ? woff[j] + c * 64 : kNowhere, 0, 0));
-        s[j] = in ? (up ? s1 : s0)[(int64_t)scol[j] * kb + 4 * c + h] : 0u;
+        w[j] = load16(up ? wr1 : wr0, in ? woff[j] + c * 64 : kNowhere);
+        s[j] = load1(up ? sr1 : sr0, in ? soff[j] + 4 * c : kNowhere);
       }
     };
 
@@ -493,34 +493,40 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
     for (int c = 0; c < chunks; ++c) {
       u32x4 wnext[NF];
       uint32_t snext[NF];
-      const bool more = c + 1 < chunks;
-      if (more) {
-        stage(c + 1, buf ^ 1);
-        load_w(c + 1, wnext, snext);
-      }
+      stage(c + 1, buf ^ 1);                    // past the last chunk: loads of nothing
+      load_w(c + 1, wnext, snext);
+      __builtin_amdgcn_sched_barrier(0);        // the loads are under way before the sums
+      // The chunk's operands of x one after another (step, plane, row tile), each read two ahead of
+      // its MFMAs; the next step's weights are converted in between.
+      constexpr int PER = MF * NP, ALL = 4 * PER;
       const char* xt = lds[buf] + (wm * MF * 16 + r) * 256;
+      const auto read_x = [&](int n) SWQ_INLINE {
+        const int step = n / PER, q = n % PER / MF, i = n % MF;
+        return *(const bf16x8*)(xt + (((4 * h + step) ^ r) * 16) + (q * BM + 16 * i) * 256);
+      };
+      bf16x8 x[3], w[2][NF];
+      x[0] = read_x(0);
+      x[1] = read_x(1);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        bf16x8 a[NF];
+      for (int j = 0; j < NF; ++j) w[0][j] = mx4_word(wc[j][0], e8m0_operand(sc[j]));
 #pragma unroll
-        for (int j = 0; j < NF; ++j) a[j] = mx4_word(wc[j][s], e8m0_operand(sc[j]));
-        const char* xu = xt + (((4 * h + s) ^ r) * 16);
+      for (int n = 0; n < ALL; ++n) {
+        const int step = n / PER, k = n % PER, i = n % MF;
+        if (n + 2 < ALL) x[(n + 2) % 3] = read_x(n + 2);
+        if (step < 3) {
 #pragma unroll
-        for (int q = 0; q < NP; ++q)
+          for (int j = 0; j < NF; ++j)
+            if (j * PER / NF == k) w[(step + 1) & 1][j] = mx4_word(wc[j][(step + 1) & 3], e8m0_operand(sc[j]));
+        }
 #pragma unroll
-          for (int i = 0; i < MF; ++i) {
-            const bf16x8 b = *(const bf16x8*)(xu + (q * BM + 16 * i) * 256);
-#pragma unroll
-            for (int j = 0; j < NF; ++j) acc[i][j] = mfma_bf16(a[j], b, acc[i][j]);
-          }
+        for (int j = 0; j < NF; ++j) acc[i][j] = mfma_bf16(w[step & 1][j], x[n % 3], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) {
 #pragma unroll
-        for (int j = 0; j < NF; ++j) wc[j] = wnext[j], sc[j] = snext[j];
-        wait_vmcnt<0>();
-        __syncthreads();
-        buf ^= 1;
-      }
+      for (int j = 0; j < NF; ++j) wc[j] = wnext[j], sc[j] = snext[j];
+      wait_vmcnt<0>();
+      __syncthreads();
+      buf ^= 1;
     }
   }
 
@@ -585,9 +591,6 @@ __device__ __forceinline__ f32x16 mfma_mx4_wide(u32x4 a, uint32_t sa, u32x4 b, u
   const i32x8 B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, E, (int)sa, E, (int)sb);
 }
-
-// (a lambda that is not inlined would take its captures, buffer descriptors among them, from memory)
-#define SWQ_INLINE __attribute__((always_inline))
 
 // f.operator()<0>(), f.operator()<1>(), ...
 template <int N, int I = 0, class F>
@@ -842,15 +845,13 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
   const int m0 = (blockIdx.x / ntn) * 16, n0 = (blockIdx.x % ntn) * 16;
   const int rows = min(16, p.M - m0), cols = min(16, p.N - n0);
   const int blocks = p.K / 32, steps = (blocks + 3) / 4;
-  const int64_t m = m0 + min(r, rows - 1), n = n0 + min(r, cols - 1);
   // rows past the end read zeros and touch no memory
-  const __amdgpu_buffer_rsrc_t ra =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (int64_t)m0 * (p.K / 8)), 0, rows * (p.K / 2), 0x00020000);
-  const __amdgpu_buffer_rsrc_t rw =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (int64_t)n0 * (p.K / 8)), 0, cols * (p.K / 2), 0x00020000);
+  const __amdgpu_buffer_rsrc_t ra = buffer(p.a + (int64_t)m0 * (p.K / 8), rows * (p.K / 2));
+  const __amdgpu_buffer_rsrc_t rw = buffer(p.w + (int64_t)n0 * (p.K / 8), cols * (p.K / 2));
+  const __amdgpu_buffer_rsrc_t sra = buffer(p.sa + (int64_t)m0 * blocks, rows * blocks);
+  const __amdgpu_buffer_rsrc_t srw = buffer(p.s + (int64_t)n0 * blocks, cols * blocks);
   const uint32_t off = r * (p.K / 2) + h * 16;
-  const uint8_t* sa = p.sa + m * blocks;
-  const uint8_t* sw = p.s + n * blocks;
+  const uint32_t soff = r * blocks + h;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int t0 = wave; t0 < steps; t0 += W * U) {
     u32x4 a[U], w[U];
@@ -859,10 +860,10 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
     for (int u = 0; u < U; ++u) {
       const int t = t0 + u * W;
       const bool in = 4 * t + h < blocks;
-      a[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? off + t * 64 : kNowhere, 0, 0));
-      w[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? off + t * 64 : kNowhere, 0, 0));
-      fa[u] = in ? sa[4 * t + h] : 0u;
-      fw[u] = in ? sw[4 * t + h] : 0u;
+      a[u] = load16(ra, in ? off + t * 64 : kNowhere);
+      w[u] = load16(rw, in ? off + t * 64 : kNowhere);
+      fa[u] = load1(sra, in ? soff + 4 * t : kNowhere);
+      fw[u] = load1(srw, in ? soff + 4 * t : kNowhere);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) acc = mfma_mx4(w[u], fw[u], a[u], fa[u], acc);
@@ -873,7 +874,7 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
   f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int v = 0; v < W; ++v) y += lds[v * 64 + lane];
-  store4(p.out, m * p.N, n0 + 4 * h, p.N, p.vec, y, p.out_type);
+  store4(p.out, (int64_t)(m0 + r) * p.N, n0 + 4 * h, p.N, p.vec, y, p.out_type);
 }
 
 }  // namespace
