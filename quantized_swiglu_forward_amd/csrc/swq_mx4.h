@@ -17,6 +17,9 @@ inline int type_bytes(int t) { return t == kTypeF32 ? 4 : 2; }
 //   kXPlanes two bf16 rows (hi, lo), `plane` elements apart
 enum : int { kXBf16 = 0, kXF16 = 1, kXPlanes = 2 };
 
+// Kernels of a product with MXFP4 weights.
+enum : int { kFew, kSmallTiles, kLargeTiles };
+
 // One tile of rows of a grouped product.
 struct RowTile {
   int expert;   // -1: rows of no expert, written as zeros
@@ -50,6 +53,7 @@ struct MxGemm {
   const int* ntiles;
   const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
+  int kind;                 // kFew, kSmallTiles or kLargeTiles (mx4_gemm_kind)
   const int* ids;           // without tiles: the expert of every row (few rows, taken one by one), or null
 
 #ifdef __HIPCC__
@@ -96,8 +100,10 @@ hipError_t launch_mx4_dequantize(const uint32_t* codes, const uint8_t* scales, i
 // binary16 rows [n] to two bf16 planes, n a multiple of 8
 hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int64_t plane, hipStream_t st);
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st);
-int mx4_gemm_tile(const MxGemm& p);           // row tile height that the launch takes, for the plan
-bool mx4_gemm_takes_planes(const MxGemm& p);  // binary16 x has to come as planes
+// The kernel for a product (MxGemm::kind); one choice for products that share a plan.
+int mx4_gemm_kind(const MxGemm& p);
+int mx4_gemm_tile(const MxGemm& p);           // row tile height of its kind, for the plan
+bool mx4_gemm_takes_planes(const MxGemm& p);  // its kind wants binary16 x as planes
 // out[t] = res[t] + sum_j weights[t, j] x[t k + j] W[ids[t k + j]]^T for few tokens (p.rows = tokens k)
 hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st);
 // bytes of workspace that the product of two MXFP4 matrices takes (0: none)

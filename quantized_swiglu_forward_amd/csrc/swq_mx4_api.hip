@@ -137,6 +137,7 @@ int swiglu_q_mx4_linear(const void* x, const uint32_t* W, const void* s, const v
   g.type = type;
   g.out_type = out_mode;
   g.vec = vec_ok(N, out, residual, out_mode);
+  g.kind = mx4_gemm_kind(g);
   if (const int64_t need = planes_bytes(g, M)) {
     void* ws = nullptr;
     rc = stream_workspace((hipStream_t)stream, (size_t)need, &ws, kWsSlot);
@@ -196,6 +197,7 @@ int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uin
   g.type = type;
   g.out_type = out_mode;
   g.vec = vec_ok(N, out, nullptr, out_mode);
+  g.kind = mx4_gemm_kind(g);
   const int tile = mx4_gemm_tile(g);
   const PlanLayout l = plan_layout(P, E, tile, false);
   void* ws = nullptr;
@@ -263,6 +265,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   // tensor in the plan's order (two planes for binary16), the experts' outputs
   // in the slots' order, and x as planes.
   const bool direct = T <= kDirectTokens;
+  g.kind = direct ? (int)kFew : mx4_gemm_kind(g);
   const int tile = mx4_gemm_tile(g);
   const PlanLayout l = direct ? PlanLayout{0, 0, 0} : plan_layout(P, E, tile, true);
   const int64_t hidden = align256(P * I * 2) * (f16 ? 2 : 1);

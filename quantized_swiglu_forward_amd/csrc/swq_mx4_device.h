@@ -35,6 +35,12 @@ __device__ __forceinline__ bf16x8 mx4_word(uint32_t w, float scale) {
   return (bf16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Codes 2 E and 2 E + 1 of a word, likewise.
+template <int E>
+__device__ __forceinline__ uint32_t mx4_pair(uint32_t w, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, E));
+}
+
 // A binary16 value as the sum of two bf16 values: hi rounds it to 8
 // significant bits, lo is the rest (at most 3 bits; both exact: bf16's
 // exponent range holds binary16's).  An infinity or NaN is hi alone.

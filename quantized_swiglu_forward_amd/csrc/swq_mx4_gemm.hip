@@ -47,6 +47,15 @@ __device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t b, uint32_t off
 }
 
 
+// f.operator()<0>(), f.operator()<1>(), ...
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f.template operator()<I>();
+    each<N, I + 1>(f);
+  }
+}
+
 // XCD-aware order of the tiles: the hardware deals consecutive blocks to the
 // eight XCDs in turn, so block b takes tile b / 8 of a contiguous eighth of the
 // order, and an XCD's own L2 sees neighbours.  In the order, bands of eight row
@@ -73,9 +82,9 @@ __device__ __forceinline__ void drain16(const Spec& p, const float* buf, int row
   const int lane = threadIdx.x & 63;
   if (p.vec == 2) {
 #pragma unroll
-    for (int i = 0; i < 16 * UNITS / 64; ++i) {
+    for (int i = 0; i < (16 * UNITS + 63) / 64; ++i) {
       const int u = i * 64 + lane, lr = u / UNITS, c = (u % UNITS) * 8, col = col0 + c;
-      if (lr >= rows || col >= p.N) continue;
+      if (u >= 16 * UNITS || lr >= rows || col >= p.N) continue;
       const f32x4 a = *(const f32x4*)(buf + lr * LD + c), b = *(const f32x4*)(buf + lr * LD + c + 4);
       float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
       const int64_t at = row_at(lr) * p.N + col;
@@ -175,6 +184,17 @@ __device__ __forceinline__ void finish4(const MxGemm& p, int64_t at, int col, f3
 // 128 inputs c = wave, wave + W, ... on its own, weights and x straight to
 // registers, U chunks of loads in flight, and the waves' sums meet in LDS at the
 // end.  No barrier stands between the loads.
+// Row tiles whose partial sums meet in LDS at once, and the f32x4 of LDS that this takes.
+constexpr int few_pass(int rt, int nw, int w) {
+  int rp = rt;
+  while (rp > 1 && w * rp * nw > 32) rp /= 2;
+  return rp;
+}
+constexpr int few_lds(int rt, int nw, int w) {
+  const int rp = few_pass(rt, nw, w);
+  return (rp < rt ? 2 : 1) * w * rp * nw * 64;
+}
+
 template <int RT, int CT, int XS, bool FUSED, int W, int U>
 __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first, int rows, int n0, f32x4* lds) {
   constexpr int NW = FUSED ? 2 * CT : CT, NP = XS == kXBf16 ? 1 : 2, NL = XS == kXPlanes ? 2 : 1;
@@ -256,28 +276,33 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
     }
   }
 
-  // the waves' sums: [wave][i][j][lane], added in wave order
+  // the waves' sums, RP row tiles at a time: [wave][i][j][lane], added in wave order
+  constexpr int RP = few_pass(RT, NW, W), PASS = W * RP * NW * 64;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int i0 = 0; i0 < RT; i0 += RP) {
+    f32x4* part = lds + (i0 / RP & 1) * PASS;   // two stretches in turn: one barrier a pass
 #pragma unroll
-    for (int j = 0; j < NW; ++j) lds[((wave * RT + i) * NW + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  for (int f = wave; f < RT * CT; f += W) {
-    const int i = f / CT, j = f % CT;
-    f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+    for (int i = 0; i < RP; ++i)
 #pragma unroll
-    for (int v = 0; v < W; ++v) {
-      g += lds[((v * RT + i) * NW + j) * 64 + lane];
-      if constexpr (FUSED) u += lds[((v * RT + i) * NW + j + CT) * 64 + lane];
-    }
-    if constexpr (FUSED) {
+      for (int j = 0; j < NW; ++j) part[((wave * RP + i) * NW + j) * 64 + lane] = acc[i0 + i][j];
+    __syncthreads();
+    for (int f = wave; f < RP * CT; f += W) {
+      const int i = f / CT, j = f % CT;
+      f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) g[e] = silu_times(g[e], u[e]);
-    }
-    const int lr = 16 * i + r;
-    if (lr < rows) {
-      const int row = p.perm ? p.perm[first + lr] : first + lr;
-      finish4(p, (int64_t)row * p.N, n0 + 16 * j + 4 * h, g);
+      for (int v = 0; v < W; ++v) {
+        g += part[((v * RP + i) * NW + j) * 64 + lane];
+        if constexpr (FUSED) u += part[((v * RP + i) * NW + j + CT) * 64 + lane];
+      }
+      if constexpr (FUSED) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = silu_times(g[e], u[e]);
+      }
+      const int lr = 16 * (i0 + i) + r;
+      if (lr < rows) {
+        const int row = p.perm ? p.perm[first + lr] : first + lr;
+        finish4(p, (int64_t)row * p.N, n0 + 16 * j + 4 * h, g);
+      }
     }
   }
 }
@@ -285,9 +310,8 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
 // Rows of the block: a tile of the table, of a dense product, or the one row
 // (slot) of p.ids.
 template <int RT, int CT, int XS, bool FUSED, int W, int U>
-__global__ __launch_bounds__(64 * W) void mx4_few_kernel(MxGemm p) {
-  constexpr int F = RT * CT * (FUSED ? 2 : 1);
-  __shared__ f32x4 lds[W * F * 64];
+__global__ __launch_bounds__(64 * W, 2) void mx4_few_kernel(MxGemm p) {
+  __shared__ f32x4 lds[few_lds(RT, FUSED ? 2 * CT : CT, W)];
 #ifdef SWQ_LDS_POISON
   lds_poison(lds, sizeof(lds), kPoisonFloat);
   __syncthreads();
@@ -307,12 +331,6 @@ __global__ __launch_bounds__(64 * W) void mx4_few_kernel(MxGemm p) {
   expert = __builtin_amdgcn_readfirstlane(expert);
   first = __builtin_amdgcn_readfirstlane(first);
   rows = __builtin_amdgcn_readfirstlane(rows);
-  if constexpr (RT > 1) {
-    if (rows <= 16) return few_rows<1, CT, XS, FUSED, W, 2>(p, expert, first, rows, tn * 16 * CT, lds);
-  }
-  if constexpr (RT > 2) {
-    if (rows <= 32) return few_rows<2, CT, XS, FUSED, W, 1>(p, expert, first, rows, tn * 16 * CT, lds);
-  }
   few_rows<RT, CT, XS, FUSED, W, U>(p, expert, first, rows, tn * 16 * CT, lds);
 }
 
@@ -397,12 +415,12 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
 // by WM waves only).  x goes through LDS, [BM * NP][128] bf16, two buffers, by
 // loads that write LDS; 16-byte unit u of a row sits at u ^ (row & 15), so the
 // sixteen rows that a read touches lie in different banks.
-template <int MF, int NF, int WM, int WN, int NP, bool FUSED>
+template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   constexpr int W = WM * WN, BM = 16 * MF * WM, ROWS = BM * NP, BN = 16 * NF * WN, BNO = FUSED ? BN / 2 : BN;
   constexpr int DMA = ROWS / (4 * W);           // loads per lane and chunk, four rows each per wave
   static_assert(ROWS % (4 * W) == 0 && (!FUSED || NF % 2 == 0));
-  __shared__ __attribute__((aligned(1024))) char lds[2][ROWS * 256];
+  __shared__ __attribute__((aligned(1024))) char lds[S * ROWS * 256];
 #ifdef SWQ_LDS_POISON
   lds_poison(lds, sizeof(lds), kPoisonFloat);
   __syncthreads();
@@ -447,14 +465,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
       const int xrow = p.xperm ? p.xperm[first + slot] / p.xdiv : slot;
       xoff[i] = (uint32_t)xrow * (uint32_t)p.K * 2u + du * 16;
     }
-    const auto stage = [&](int c, int buf) {
-      const bool in = c * 128 + du * 8 < p.K;   // past K: zeros
-#pragma unroll
-      for (int i = 0; i < DMA; ++i) {
-        const uint32_t base = lds_addr(&lds[buf][(i * 4 * W + wave * 4) * 256]);
-        dma16(xr[(i * 4 * W) / BM], __builtin_amdgcn_readfirstlane(base),
-              in ? xoff[i] + (uint32_t)c * 256u : kNowhere);
-      }
+    // load i of chunk c (past K: zeros)
+    const auto load_x = [&]<int i>(int c, int buf) SWQ_INLINE {
+      dma16(xr[(i * 4 * W) / BM],
+            __builtin_amdgcn_readfirstlane(lds_addr(lds) + buf * (ROWS * 256) + (i * 4 * W + wave * 4) * 256),
+            c * 128 + du * 8 < p.K ? xoff[i] + (uint32_t)c * 256u : kNowhere);
     };
 
     // W: the columns of this wave; rows past N read zeros
@@ -473,61 +488,61 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
         buffer((FUSED ? p.w2 : p.w) + wrow * (p.K / 8), min(wn_rows, BNO) * (p.K / 2));
     const __amdgpu_buffer_rsrc_t sr0 = buffer(p.s + wrow * kb, min(wn_rows, BNO) * kb);
     const __amdgpu_buffer_rsrc_t sr1 = buffer((FUSED ? p.s2 : p.s) + wrow * kb, min(wn_rows, BNO) * kb);
-    u32x4 wc[NF];
-    uint32_t sc[NF];
-    const auto load_w = [&](int c, u32x4* w, uint32_t* s) {
+    // S stages: a chunk's x in LDS, its codes and scales in registers, loaded S - 1 chunks ahead
+    u32x4 wc[S][NF];
+    uint32_t sc[S][NF];
+    const auto load_w = [&]<int b, int j>(int c) SWQ_INLINE {
+      constexpr bool up = FUSED && j >= NF / 2;
       const bool in = 4 * c + h < kb;
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        const bool up = FUSED && j >= NF / 2;
-        w[j] = load16(up ? wr1 : wr0, in ? woff[j] + c * 64 : kNowhere);
-        s[j] = load1(up ? sr1 : sr0, in ? soff[j] + 4 * c : kNowhere);
-      }
+      wc[b][j] = load16(up ? wr1 : wr0, in ? woff[j] + c * 64 : kNowhere);
+      sc[b][j] = load1(up ? sr1 : sr0, in ? soff[j] + 4 * c : kNowhere);
     };
+    constexpr int LOADS = 2 * NF + DMA;
+    each<S - 1>([&]<int b>() SWQ_INLINE {
+      each<NF>([&]<int j>() SWQ_INLINE { load_w.template operator()<b, j>(b); });
+      each<DMA>([&]<int i>() SWQ_INLINE { load_x.template operator()<i>(b, b); });
+      __builtin_amdgcn_sched_barrier(0);        // the waits below count on the loads' order
+    });
 
-    stage(0, 0);
-    load_w(0, wc, sc);
-    wait_vmcnt<0>();
-    __syncthreads();
-    int buf = 0;
-    for (int c = 0; c < chunks; ++c) {
-      u32x4 wnext[NF];
-      uint32_t snext[NF];
-      stage(c + 1, buf ^ 1);                    // past the last chunk: loads of nothing
-      load_w(c + 1, wnext, snext);
-      __builtin_amdgcn_sched_barrier(0);        // the loads are under way before the sums
-      // The chunk's operands of x one after another (step, plane, row tile), each read two ahead of
-      // its MFMAs; the next step's weights are converted in between.
-      constexpr int PER = MF * NP, ALL = 4 * PER;
-      const char* xt = lds[buf] + (wm * MF * 16 + r) * 256;
-      const auto read_x = [&](int n) SWQ_INLINE {
-        const int step = n / PER, q = n % PER / MF, i = n % MF;
-        return *(const bf16x8*)(xt + (((4 * h + step) ^ r) * 16) + (q * BM + 16 * i) * 256);
+    // Chunk c, in stage b; loads past the last chunk read nothing, chunks past it add zeros.
+    const auto chunk = [&]<int b>(int c) SWQ_INLINE {
+      wait_vmcnt<(S - 2) * LOADS>();            // the later chunks' loads may still be out
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      // The chunk's operands of x one after another (step, plane, row tile), each read two ahead of its
+      // MFMAs.  What else there is to do -- the loads of chunk c + S - 1, the conversion of the
+      // next step's weights -- stands one piece at a time between MFMAs, in whose
+      // cycles it hides.
+      constexpr int PER = MF * NP, ALL = 4 * PER, GAP = PER / 4, ahead = (b + S - 1) % S;
+      const char* xt = lds + b * (ROWS * 256) + (wm * MF * 16 + r) * 256;
+      bf16x8 x[3];
+      u32x4 w[2][NF];
+      const auto read_x = [&]<int n>() SWQ_INLINE {
+        constexpr int step = n / PER, q = n % PER / MF, i = n % MF;
+        x[n % 3] = *(const bf16x8*)(xt + (((4 * h + step) ^ r) * 16) + (q * BM + 16 * i) * 256);
       };
-      bf16x8 x[3], w[2][NF];
-      x[0] = read_x(0);
-      x[1] = read_x(1);
+      read_x.template operator()<0>();
+      read_x.template operator()<1>();
 #pragma unroll
-      for (int j = 0; j < NF; ++j) w[0][j] = mx4_word(wc[j][0], e8m0_operand(sc[j]));
-#pragma unroll
-      for (int n = 0; n < ALL; ++n) {
-        const int step = n / PER, k = n % PER, i = n % MF;
-        if (n + 2 < ALL) x[(n + 2) % 3] = read_x(n + 2);
-        if (step < 3) {
-#pragma unroll
-          for (int j = 0; j < NF; ++j)
-            if (j * PER / NF == k) w[(step + 1) & 1][j] = mx4_word(wc[j][(step + 1) & 3], e8m0_operand(sc[j]));
+      for (int j = 0; j < NF; ++j) w[0][j] = __builtin_bit_cast(u32x4, mx4_word(wc[b][j][0], e8m0_operand(sc[b][j])));
+      each<ALL * NF>([&]<int m>() SWQ_INLINE {
+        constexpr int n = m / NF, j = m % NF, step = n / PER, i = n % MF, l = m % (PER * NF);
+        if constexpr (j == 0 && n + 2 < ALL) read_x.template operator()<n + 2>();
+        if constexpr (m % 2 == 1 && m / 2 < NF) load_w.template operator()<ahead, m / 2>(c + S - 1);
+        if constexpr (m % 2 == 1 && m / 2 >= NF && m / 2 < NF + DMA)
+          load_x.template operator()<m / 2 - NF>(c + S - 1, ahead);
+        if constexpr (step < 3 && l % GAP == GAP - 1) {
+          constexpr int k = l / GAP, jj = k / 4, e = k % 4;
+          w[(step + 1) & 1][jj][e] = mx4_pair<e>(wc[b][jj][step + 1], e8m0_operand(sc[b][jj]));
         }
-#pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = mfma_bf16(w[step & 1][j], x[n % 3], acc[i][j]);
+        acc[i][j] = mfma_bf16(__builtin_bit_cast(bf16x8, w[step & 1][j]), x[n % 3], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int j = 0; j < NF; ++j) wc[j] = wnext[j], sc[j] = snext[j];
-      wait_vmcnt<0>();
-      __syncthreads();
-      buf ^= 1;
-    }
+      });
+    };
+    for (int c = 0; c < chunks; c += S)
+      each<S>([&]<int b>() SWQ_INLINE { chunk.template operator()<b>(c + b); });
+    wait_vmcnt<0>();           // no load past the end may still write LDS
   }
 
   // the stretches of the waves overlay the x buffers
@@ -590,15 +605,6 @@ __device__ __forceinline__ f32x16 mfma_mx4_wide(u32x4 a, uint32_t sa, u32x4 b, u
   const i32x8 A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
   const i32x8 B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, E, (int)sa, E, (int)sb);
-}
-
-// f.operator()<0>(), f.operator()<1>(), ...
-template <int N, int I = 0, class F>
-__device__ __forceinline__ void each(F f) {
-  if constexpr (I < N) {
-    f.template operator()<I>();
-    each<N, I + 1>(f);
-  }
 }
 
 // As dma16, four bytes per lane.
@@ -879,32 +885,43 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 
 }  // namespace
 
-// Kernel of a product: the few-row kernel below a row count, else the tiled one.
-// A grouped product goes by its rows per expert.
-static bool few(const MxGemm& p) {
-  if (const char* e = getenv("SWQ_MX4_FEW")) return p.rows / p.E < atoi(e);
-  return p.rows / p.E < 64;
+// What a product runs on.  Measured on one MI355X (x bf16, us; K x N = 4096 x 14336):
+//   rows          1     16    32    64    128   256   1024  2048
+//   few-row       12    14    16    26    50    96    -     -
+//   64 x 128      -     -     -     24    24    40    150   278
+//   128 x 256     55    57    57    58    62    64    115   215
+// and for 1024 rows of 5632 x 2048 62, 30 and 84: the few-row kernel up to 48 rows (a grouped
+// product: of an average expert), the 128 x 256 tiles once they fill three quarters of
+// the CUs (one such tile takes 1.9 us per chunk, a 64 x 128 tile 0.62), else 64 x 128.
+int mx4_gemm_kind(const MxGemm& p) {
+  const int64_t each = p.rows / p.E;
+  if (each <= 48) return kFew;
+  const int64_t rows128 = p.E == 1 ? (p.rows + 127) / 128 : p.rows / 128 + p.E / 2;
+  const int64_t n = p.w2 ? 128 : 256;
+  return 4 * rows128 * ((p.N + n - 1) / n) >= 3 * device_cus() ? kLargeTiles : kSmallTiles;
 }
 
-static int few_tiles(const MxGemm& p) {       // row tiles of 16 of the few-row kernel
+// Row tiles of 16 of the few-row kernel, by the rows of an average expert.
+static int few_tiles(const MxGemm& p) {
   if (p.ids && !p.tiles) return 1;
-  return p.tiles ? 4 : p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+  const int64_t each = p.rows / p.E;
+  return p.E == 1 ? (p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4) : each <= 8 ? 1 : each <= 20 ? 2 : 4;
 }
 
 int mx4_gemm_tile(const MxGemm& p) {
-  if (few(p)) return 64;
-  return p.xsrc != kXBf16 ? 64 : 128;
+  const int k = p.kind;
+  return k == kFew ? 16 * few_tiles(p) : k == kSmallTiles || p.xsrc != kXBf16 ? 64 : 128;
 }
 
-bool mx4_gemm_takes_planes(const MxGemm& p) { return !few(p); }
+bool mx4_gemm_takes_planes(const MxGemm& p) { return p.kind != kFew; }
 
-template <int MF, int NF, int WM, int WN, int NP, bool FUSED>
+template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED>
 static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
   constexpr int BM = 16 * MF * WM, BNO = 16 * NF * WN / (FUSED ? 2 : 1);
   const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + BM - 1) / BM, ntn = (p.N + BNO - 1) / BNO;
   const int64_t blocks = (ntm * ntn + 7) / 8 * 8;
   if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-  mx4_gemm_kernel<MF, NF, WM, WN, NP, FUSED><<<dim3((unsigned)blocks), 64 * WM * WN, 0, st>>>(p);
+  mx4_gemm_kernel<MF, NF, WM, WN, NP, S, FUSED><<<dim3((unsigned)blocks), 64 * WM * WN, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -917,23 +934,40 @@ static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Column tiles per block: as many as leave seven eighths of the CUs a block (more columns
+// read x less often).
+template <int RT, int XS, bool FUSED>
+static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
+  constexpr int D = FUSED ? 2 : 1;
+  const int64_t tiles = p.tiles ? std::min<int64_t>(p.max_tiles, p.rows) : p.ids ? p.rows : (p.rows + 16 * RT - 1) / (16 * RT);
+  const int64_t need = device_cus() * 7 / 8;
+  if (p.N / (16 * 4 / D) * tiles >= need) return launch_few_as<RT, 4 / D, XS, FUSED, 8, 1>(p, st);
+  if (p.N / (16 * 2 / D) * tiles >= need || FUSED) return launch_few_as<RT, 2 / D, XS, FUSED, 8, RT == 1 ? 2 : 1>(p, st);
+  if constexpr (!FUSED) return launch_few_as<RT, 1, XS, FUSED, 8, RT <= 2 ? 2 : 1>(p, st);
+  return hipErrorInvalidValue;
+}
+
 template <int XS, bool FUSED>
 static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
   const int rt = few_tiles(p);
-  if (rt == 1) return launch_few_as<1, 1, XS, FUSED, 8, 2>(p, st);
-  if (rt == 2) return launch_few_as<2, FUSED ? 1 : 2, XS, FUSED, 8, 1>(p, st);
-  return launch_few_as<4, FUSED ? 1 : 2, XS, FUSED, 8, 1>(p, st);
+  return rt == 1 ? launch_few_rt<1, XS, FUSED>(p, st) : rt == 2 ? launch_few_rt<2, XS, FUSED>(p, st)
+                                                                : launch_few_rt<4, XS, FUSED>(p, st);
+}
+
+template <bool FUSED>
+static hipError_t launch_gemm(const MxGemm& p, hipStream_t st) {
+  const int k = p.kind;
+  if (k == kFew)
+    return p.xsrc == kXBf16  ? launch_few<kXBf16, FUSED>(p, st)
+           : p.xsrc == kXF16 ? launch_few<kXF16, FUSED>(p, st)
+                             : launch_few<kXPlanes, FUSED>(p, st);
+  if (p.xsrc != kXBf16)
+    return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 2, 2, FUSED>(p, st) : launch_tiled<4, 4, 1, 4, 2, 2, FUSED>(p, st);
+  return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 1, 4, FUSED>(p, st) : launch_tiled<8, 4, 1, 4, 1, 2, FUSED>(p, st);
 }
 
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st) {
-  const bool fused = p.w2;
-  if ((p.ids && !p.tiles) || few(p)) {
-    if (p.xsrc == kXBf16) return fused ? launch_few<kXBf16, true>(p, st) : launch_few<kXBf16, false>(p, st);
-    if (p.xsrc == kXF16) return fused ? launch_few<kXF16, true>(p, st) : launch_few<kXF16, false>(p, st);
-    return fused ? launch_few<kXPlanes, true>(p, st) : launch_few<kXPlanes, false>(p, st);
-  }
-  if (p.xsrc != kXBf16) return fused ? launch_tiled<4, 4, 1, 4, 2, true>(p, st) : launch_tiled<4, 4, 1, 4, 2, false>(p, st);
-  return fused ? launch_tiled<8, 4, 1, 4, 1, true>(p, st) : launch_tiled<8, 4, 1, 4, 1, false>(p, st);
+  return p.w2 ? launch_gemm<true>(p, st) : launch_gemm<false>(p, st);
 }
 
 hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st) {

@@ -80,50 +80,74 @@ __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ log
 // no result: every output row depends on its own input row alone).  With
 // offsets: the groups as given, made non-decreasing and cut at P; the rows
 // before the first and after the last group become tiles of no expert.
-__global__ __launch_bounds__(1024) void plan_kernel(RoutePlan p) {
-  __shared__ int count[kMaxExperts + 2], first[kMaxExperts + 2], tile0[kMaxExperts + 2];
-  const int t = threadIdx.x;
-  if (t < p.E) count[t] = 0;
+// Thread t holds expert t.
+constexpr int kPlanThreads = 1024, kPlanAhead = 8;
+
+// Inclusive sum (or maximum) over the threads of a block.
+template <bool MAX>
+__device__ __forceinline__ int block_scan(int v, int* wave_total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v = MAX ? max(v, o) : v + o;
+  }
+  if (lane == 63) wave_total[wave] = v;
   __syncthreads();
-  const int groups = p.ids ? p.E : p.E + 2;
+  int before = MAX ? INT32_MIN : 0;
+  for (int w = 0; w < wave; ++w) before = MAX ? max(before, wave_total[w]) : before + wave_total[w];
+  __syncthreads();
+  return MAX ? max(v, before) : v + before;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(RoutePlan p) {
+  __shared__ int count[kMaxExperts], next[kMaxExperts], total[kPlanThreads / 64];
+  const int t = threadIdx.x;
+  int rows = 0, first = 0, last = 0;           // of expert t; the end of the last expert's rows
   if (p.ids) {
-    for (int i = t; i < p.P; i += 1024) {
-      const int e = p.ids[i];
-      if (e >= 0 && e < p.E) atomicAdd(&count[e], 1);
+    if (t < p.E) count[t] = 0;
+    __syncthreads();
+    for (int i0 = t; i0 < p.P; i0 += kPlanThreads * kPlanAhead) {
+      int e[kPlanAhead];
+#pragma unroll
+      for (int j = 0; j < kPlanAhead; ++j) e[j] = i0 + j * kPlanThreads < p.P ? p.ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+      for (int j = 0; j < kPlanAhead; ++j)
+        if (e[j] >= 0 && e[j] < p.E) atomicAdd(&count[e[j]], 1);
     }
     __syncthreads();
+    rows = t < p.E ? count[t] : 0;
+  } else {
+    const int start = block_scan<true>(t < p.E ? min(max(p.offsets[t], 0), p.P) : 0, total);
+    if (t < p.E) next[t] = start;
+    if (t == p.E - 1) count[0] = max(start, min(max(p.offsets[p.E], 0), p.P));
+    __syncthreads();
+    last = count[0];
+    first = start;
+    rows = t < p.E ? (t + 1 < p.E ? next[t + 1] : last) - start : 0;
   }
-  if (t == 0) {                                // scan over the experts
-    int at = 0, tiles = 0;
-    if (!p.ids) {
-      at = min(max(p.offsets[0], 0), p.P);
-      first[0] = 0, count[0] = at, tile0[0] = 0;
-      tiles = (at + p.tile - 1) / p.tile;
-    }
-    for (int e = 0; e < p.E; ++e) {
-      const int g = p.ids ? e : e + 1;
-      const int c = p.ids ? count[e] : min(max(p.offsets[e + 1], at), p.P) - at;
-      first[g] = at, count[g] = c, tile0[g] = tiles;
-      at += c;
-      tiles += (c + p.tile - 1) / p.tile;
-    }
-    if (!p.ids) {
-      first[p.E + 1] = at, count[p.E + 1] = p.P - at, tile0[p.E + 1] = tiles;
-      tiles += (p.P - at + p.tile - 1) / p.tile;
-    }
-    *p.ntiles = tiles;
-  }
-  __syncthreads();
-  for (int g = t; g < groups; g += 1024)
-    for (int i = 0; i * p.tile < count[g]; ++i)
-      p.tiles[tile0[g] + i] = RowTile{p.ids ? g : (g == 0 || g == p.E + 1 ? -1 : g - 1), first[g] + i * p.tile,
-                                      min(p.tile, count[g] - i * p.tile), 0};
-  __syncthreads();
+  const int tiles = (rows + p.tile - 1) / p.tile;
+  if (p.ids) first = block_scan<false>(rows, total) - rows;
+  const int tile_end = block_scan<false>(tiles, total);
+  for (int i = 0; i < tiles; ++i)
+    p.tiles[tile_end - tiles + i] = RowTile{t, first + i * p.tile, min(p.tile, rows - i * p.tile), 0};
   if (p.ids) {
-    for (int i = t; i < p.P; i += 1024) {
-      const int e = p.ids[i];
-      if (e >= 0 && e < p.E) p.perm[atomicAdd(&first[e], 1)] = i;
+    if (t == kPlanThreads - 1) *p.ntiles = tile_end;
+    if (t < p.E) next[t] = first;
+    __syncthreads();
+    for (int i0 = t; i0 < p.P; i0 += kPlanThreads * kPlanAhead) {
+      int e[kPlanAhead];
+#pragma unroll
+      for (int j = 0; j < kPlanAhead; ++j) e[j] = i0 + j * kPlanThreads < p.P ? p.ids[i0 + j * kPlanThreads] : -1;
+#pragma unroll
+      for (int j = 0; j < kPlanAhead; ++j)
+        if (e[j] >= 0 && e[j] < p.E) p.perm[atomicAdd(&next[e[j]], 1)] = i0 + j * kPlanThreads;
     }
+  } else if (t == kPlanThreads - 1) {          // rows of no expert, before and after the groups
+    int n = tile_end;
+    for (int i = 0; i < next[0]; i += p.tile) p.tiles[n++] = RowTile{-1, i, min(p.tile, next[0] - i), 0};
+    for (int i = last; i < p.P; i += p.tile) p.tiles[n++] = RowTile{-1, i, min(p.tile, p.P - i), 0};
+    *p.ntiles = n;
   }
 }
 
@@ -187,7 +211,7 @@ hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, i
 }
 
 hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {
-  plan_kernel<<<1, 1024, 0, st>>>(p);
+  plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 

@@ -235,6 +235,42 @@ def test_grouped_odd_offsets(P, offsets, taken):
             ref.close(out[a:b], v, ref.rounded(v, err, BF16), "odd offsets")
 
 
+def test_most_experts():
+    """1024 experts, most of them without a row, the first and the last with some."""
+    E, N, K, P = 1024, 40, 64, 50
+    w, s = matrix(3, E, N, K)
+    expert = torch.cat([torch.zeros(3, dtype=torch.long), torch.randint(0, E, (P - 7,), generator=gen(1)),
+                        torch.full((4,), E - 1)]).sort().values
+    off = torch.searchsorted(expert, torch.arange(E + 1)).to(torch.int32)
+    x = acts(2, P, K)
+    say("most experts")
+    got = swq.mx4_grouped_linear(x, off.cuda(), w, s, out_mode=swq.SWQ_LINEAR_F32)
+    wv = ref.values(w, s)
+    y, err = (np.concatenate([ref.dot(ref.to64(x[p:p + 1]), wv[int(expert[p])])[i] for p in range(P)]) for i in (0, 1))
+    ref.close(got, y, ref.rounded(y, err, F32), "most experts")
+    wd, sd = matrix(4, E, 48, 32)
+    h = [matrix(5 + i, E, 32, K) for i in (0, 1)]
+    ids = torch.stack([expert[torch.randperm(P, generator=gen(9))], expert], 1).to(torch.int32).cuda()
+    weights = torch.rand(P, 2, generator=gen(8)).cuda()
+    got = swq.moe_mlp(x, ids, weights, *h[0], *h[1], wd, sd)
+    y, err = ref.experts(ref.to64(x), ids.cpu().numpy(), ref.to64(weights), ref.values(*h[0]), ref.values(*h[1]),
+                         ref.values(wd, sd), None, HIDDEN[BF16])
+    ref.close(got, y, ref.rounded(y, err, BF16), "most experts, MLP")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,E,k,H,I,Ho", [(700, 3, 1, 64, 4096, 40), (700, 3, 1, 2048, 32, 4100), (400, 2, 2, 96, 96, 2052)])
+def test_moe_unlike_widths(T, E, k, H, I, Ho, dtype):
+    """Wide and narrow hidden tensors: both products take the tiles of one plan."""
+    x, ids, weights, ((wg, sg), (wu, su), (wd, sd)) = moe_case(T + I, T, k, E, H, I, Ho, dtype)
+    say("moe unlike widths", T, E, k, H, I, Ho, dtype)
+    got = swq.moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, out_mode=swq.SWQ_LINEAR_F32)
+    pick = torch.cat([torch.arange(0, T, 37), torch.tensor([T - 1])])
+    y, err = ref.experts(ref.to64(x)[pick], ids.cpu().numpy()[pick], ref.to64(weights)[pick],
+                         *(ref.values(w, s) for w, s in ((wg, sg), (wu, su), (wd, sd))), None, HIDDEN[dtype])
+    ref.close(got[pick.cuda()], y, ref.rounded(y, err, F32), "moe unlike widths")
+
+
 def test_grouped_weights_past_4_gib():
     """The last expert of a set of more than 2^32 bytes of codes."""
     E, N, K = 66, 16384, 8192
