@@ -11,12 +11,6 @@ enum : int { kRouteSoftmax = 0, kRouteSoftmaxChosen = 1, kRouteSigmoid = 2, kRou
 
 constexpr int kMaxExperts = 1024;
 
-__device__ __forceinline__ float load_logit(const void* p, int64_t at, int type) {
-  const float v = type == kTypeF32 ? ((const float*)p)[at] : from_16(((const uint16_t*)p)[at], type);
-  // NaN ranks below everything; +inf counts as the largest float32
-  return v != v ? -__builtin_inff() : fminf(v, 3.402823466e38f);
-}
-
 // A chosen logit's weight before the division by the sum: e^(v - top), or the sigmoid
 // e^min(v, 0) / (1 + e^-|v|), over the chosen ones times e^-min(top, 0), so that
 // very low logits do not make it 0 / 0.
@@ -26,52 +20,167 @@ __device__ __forceinline__ float routing_term(float v, float top, int scoring) {
   return expf(fminf(v, 0.0f) - from) / (1.0f + expf(-fabsf(v)));
 }
 
-// One wave per token.  A logit and its index make one 64-bit key that orders
-// by value, then by the lower index: k rounds of a maximum over the wave.
-__global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ logits, int64_t T, int E, int k, int type,
-                                                    int scoring, int* __restrict__ ids, float* __restrict__ weights) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= T) return;
-  constexpr int R = kMaxExperts / 64;
-  float v[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) v[i] = 64 * i + lane < E ? load_logit(logits, t * E + 64 * i + lane, type) : -__builtin_inff();
-  float top = -__builtin_inff(), sum = 0.0f;
-  const bool over_all = scoring == kRouteSoftmax;
-  if (over_all) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) top = fmaxf(top, v[i]);
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-#pragma unroll
-    for (int i = 0; i < R; ++i) sum += v[i] > -__builtin_inff() ? expf(v[i] - top) : 0.0f;
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+constexpr float kMaxFloat = 3.402823466e38f;
+
+// A logit as an unsigned number that orders like it: 0 for -inf and NaN (never
+// chosen), equal for both zeros, +inf above everything.
+template <int TYPE>
+struct LogitKey {             // float32: the value's 32 bits
+  static __device__ __forceinline__ uint32_t of(uint32_t bits) {
+    if (bits == 0x80000000u) bits = 0;
+    if (bits == 0x7F800000u) bits = 0x7F7FFFFFu;       // +inf counts as the largest float32
+    const bool out = (bits & 0x7FFFFFFFu) > 0x7F800000u || bits == 0xFF800000u;
+    return out ? 0u : bits ^ ((bits >> 31) ? 0xFFFFFFFFu : 0x80000000u);
   }
-  int my_id = -1;
-  float my_w = 0.0f, chosen = 0.0f;
-  uint32_t used = 0;
-  for (int j = 0; j < k; ++j) {
-    float bv = -__builtin_inff();
-    int bi = kMaxExperts;
+  static __device__ __forceinline__ float value(uint32_t key) {
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+  }
+};
+template <int TYPE>
+struct LogitKey16 {           // bf16, binary16: the 16 bits
+  static constexpr uint32_t kInf = TYPE == kTypeF16 ? 0x7C00u : 0x7F80u;
+  static __device__ __forceinline__ uint32_t of(uint32_t bits) {
+    if (bits == 0x8000u) bits = 0;
+    const bool out = (bits & 0x7FFFu) > kInf || bits == (kInf | 0x8000u);
+    return out ? 0u : (bits ^ ((bits >> 15) ? 0xFFFFu : 0x8000u));
+  }
+  static __device__ __forceinline__ float value(uint32_t key) {
+    return fminf(from_16((uint16_t)(key ^ ((key >> 15) ? 0x8000u : 0xFFFFu)), TYPE), kMaxFloat);
+  }
+};
+
+// op over a group of G lanes (16 neighbours, or the wave); every lane gets the result.
+template <int ROT>
+__device__ __forceinline__ uint32_t rotate16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROT, 0xF, 0xF, true);
+}
+template <int G, class Op>
+__device__ __forceinline__ uint32_t over_group(uint32_t v, Op op) {
+  v = op(v, rotate16<8>(v));
+  v = op(v, rotate16<4>(v));
+  v = op(v, rotate16<2>(v));
+  v = op(v, rotate16<1>(v));
+  if constexpr (G == 64) {
+    v = op(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = op(v, (uint32_t)__shfl_xor((int)v, 32));
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t min_u32(uint32_t a, uint32_t b) { return min(a, b); }
+__device__ __forceinline__ uint32_t add_f32(uint32_t a, uint32_t b) {
+  return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+
+// G lanes per token, R logits per lane, k rounds of a maximum over the group.  A
+// 16-bit logit and its index make one 32-bit key that orders by value, then by
+// the lower index; float32 takes a second reduction, over the indices of the
+// largest.  VEC: a lane's logits are neighbours, loaded 16 bytes at a time; else lane l has
+// l, l + G, ...  KR: chosen experts per lane (k <= 16 KR).
+template <int TYPE, int G, int R, int KR, bool VEC>
+__global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ logits, int64_t T, int E, int k,
+                                                    int scoring, int* __restrict__ ids, float* __restrict__ weights) {
+  constexpr bool F32 = TYPE == kTypeF32;
+  const int lane = threadIdx.x & (G - 1), l16 = threadIdx.x & 15;
+  const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;
+  const bool live = t < T;
+  const int64_t row = (live ? t : T - 1) * E;
+  // (no lane leaves early: the reductions take every lane of their group)
+  const auto index = [&](int i) { return VEC ? lane * R + i : i * G + lane; };
+  uint32_t key[R];
+  if constexpr (VEC) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < R; i += 4) {
+        u32x4 q = {0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u};
+        if (lane * R + i < E) q = *(const u32x4*)((const uint32_t*)logits + row + lane * R + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key[i + j] = LogitKey<TYPE>::of(q[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; i += 8) {
+        u32x4 q = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (lane * R + i < E) q = *(const u32x4*)((const uint16_t*)logits + row + lane * R + i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) key[i + j] = LogitKey16<TYPE>::of((q[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const bool in = index(i) < E;
+      if constexpr (F32) key[i] = LogitKey<TYPE>::of(in ? ((const uint32_t*)logits)[row + index(i)] : 0xFF800000u);
+      else key[i] = LogitKey16<TYPE>::of(in ? ((const uint16_t*)logits)[row + index(i)] : 0xFFFFu);
+    }
+  }
+  const auto value = [&](uint32_t v) {
+    if constexpr (F32) return LogitKey<TYPE>::value(v);
+    else return LogitKey16<TYPE>::value(v);
+  };
+
+  float top = 0.0f, sum = 0.0f;
+  if (scoring == kRouteSoftmax) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) m = max(m, key[i]);
+    m = over_group<G>(m, max_u32);
+    top = value(m);
+    // (small terms need no more than the hardware's exp2 gives: their error is below the sum's own rounding)
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (!(used >> i & 1) && v[i] > bv) bv = v[i], bi = 64 * i + lane;
-    for (int d = 32; d; d >>= 1) {
-      const float ov = __shfl_xor(bv, d);
-      const int oi = __shfl_xor(bi, d);
-      if (ov > bv || (ov == bv && oi < bi)) bv = ov, bi = oi;
-    }
-    if (bi == kMaxExperts) break;              // only -inf is left
-    if ((bi & 63) == lane) used |= 1u << (bi >> 6);
-    if (j == 0) top = bv;
-    const float w = routing_term(bv, top, scoring);
-    chosen += w;
-    if (lane == j) my_id = bi, my_w = w;
+      sum += key[i] ? __builtin_amdgcn_exp2f((value(key[i]) - top) * 1.4426950408889634f) : 0.0f;
+    sum = __uint_as_float(over_group<G>(__float_as_uint(sum), add_f32));
   }
-  if (lane < k) {
-    const float by = over_all ? sum : scoring == kRouteSigmoid ? 1.0f : chosen;
-    ids[t * k + lane] = my_id;
-    weights[t * k + lane] = my_id < 0 ? 0.0f : my_w / by;
+  if constexpr (!F32) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) key[i] = key[i] ? key[i] << 16 | (0xFFFFu - (uint32_t)index(i)) : 0u;
+  }
+
+  int id[KR];
+  float w[KR], chosen = 0.0f;
+#pragma unroll
+  for (int s = 0; s < KR; ++s) {
+    id[s] = -1;
+    w[s] = 0.0f;
+    for (int j = 16 * s; j < 16 * s + 16 && j < k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) best = max(best, key[i]);
+      best = over_group<G>(best, max_u32);
+      uint32_t at;
+      float v;
+      if constexpr (F32) {
+        at = 0xFFFFu;
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)index(i) : at;
+        at = over_group<G>(at, min_u32);
+        v = value(best);
+#pragma unroll
+        for (int i = 0; i < R; ++i) key[i] = (uint32_t)index(i) == at ? 0u : key[i];
+      } else {
+        at = 0xFFFFu - (best & 0xFFFFu);
+        v = value(best >> 16);
+#pragma unroll
+        for (int i = 0; i < R; ++i) key[i] = key[i] == best ? 0u : key[i];
+      }
+      if (best != 0) {                         // else only -inf is left
+        if (j == 0) top = v;
+        const float term = routing_term(v, top, scoring);
+        chosen += term;
+        if (l16 == (j & 15)) id[s] = (int)at, w[s] = term;
+      }
+    }
+  }
+  if (!live || lane >= 16) return;
+  const float by = scoring == kRouteSoftmax ? sum : scoring == kRouteSigmoid ? 1.0f : chosen;
+#pragma unroll
+  for (int s = 0; s < KR; ++s) {
+    const int j = 16 * s + l16;
+    if (j < k) {
+      ids[t * k + j] = id[s];
+      weights[t * k + j] = id[s] < 0 ? 0.0f : w[s] / by;
+    }
   }
 }
 
@@ -204,10 +313,44 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
 
 }  // namespace
 
+template <int TYPE, int G, int R, int KR>
+static hipError_t launch_route_as(const void* logits, int64_t T, int E, int k, int scoring, int* ids, float* weights,
+                                  hipStream_t st) {
+  constexpr int WIDE = TYPE == kTypeF32 ? 4 : 8;
+  const dim3 grid((unsigned)((T * G + 255) / 256));
+  if constexpr (R % WIDE == 0) {
+    if (E % WIDE == 0 && (uintptr_t)logits % 16 == 0) {
+      route_kernel<TYPE, G, R, KR, true><<<grid, 256, 0, st>>>(logits, T, E, k, scoring, ids, weights);
+      return hipGetLastError();
+    }
+  }
+  route_kernel<TYPE, G, R, KR, false><<<grid, 256, 0, st>>>(logits, T, E, k, scoring, ids, weights);
+  return hipGetLastError();
+}
+
+template <int TYPE, int KR>
+static hipError_t launch_route_type(const void* logits, int64_t T, int E, int k, int scoring, int* ids, float* weights,
+                                    hipStream_t st) {
+  if (E <= 64) return launch_route_as<TYPE, 16, 4, KR>(logits, T, E, k, scoring, ids, weights, st);
+  if (E <= 128) return launch_route_as<TYPE, 16, 8, KR>(logits, T, E, k, scoring, ids, weights, st);
+  if (E <= 256) return launch_route_as<TYPE, 16, 16, KR>(logits, T, E, k, scoring, ids, weights, st);
+  if (E <= 512) return launch_route_as<TYPE, 64, 8, KR>(logits, T, E, k, scoring, ids, weights, st);
+  return launch_route_as<TYPE, 64, 16, KR>(logits, T, E, k, scoring, ids, weights, st);
+}
+
+template <int TYPE>
+static hipError_t launch_route_k(const void* logits, int64_t T, int E, int k, int scoring, int* ids, float* weights,
+                                 hipStream_t st) {
+  return k <= 16 ? launch_route_type<TYPE, 1>(logits, T, E, k, scoring, ids, weights, st)
+                 : launch_route_type<TYPE, 4>(logits, T, E, k, scoring, ids, weights, st);
+}
+
 hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
                         hipStream_t st) {
-  route_kernel<<<dim3((unsigned)((T + 3) / 4)), 256, 0, st>>>(logits, T, E, k, type, scoring, ids, weights);
-  return hipGetLastError();
+  if (T * 64 >= (int64_t(1) << 39)) return hipErrorInvalidValue;
+  return type == kTypeF32   ? launch_route_k<kTypeF32>(logits, T, E, k, scoring, ids, weights, st)
+         : type == kTypeF16 ? launch_route_k<kTypeF16>(logits, T, E, k, scoring, ids, weights, st)
+                            : launch_route_k<kTypeBf16>(logits, T, E, k, scoring, ids, weights, st);
 }
 
 hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {

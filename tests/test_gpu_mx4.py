@@ -317,7 +317,7 @@ def test_route_masks_and_nonfinite():
     low = torch.finfo(F32).min
     lo = torch.tensor([[-inf, 1.0, -inf, -inf, -inf], [-inf] * 5, [nan, 2.0, nan, 1.0, 3.0], [0.0, inf, 1.0, inf, -1.0],
                        [0.5] * 5, [low, low, 1.0, low, low], [nan] * 5, [low] * 5, [-0.0, 0.0, -0.0, 0.0, 0.0],
-                       [-200.0, -300.0, -400.0, -inf, -1000.0]])
+                       [-200.0, -300.0, -400.0, -inf, -1000.0], [inf, -low, inf, -low, 0.0], [-inf, nan, inf, nan, -inf]])
     for scoring in range(4):
         say("route masks", scoring)
         ids, w = swq.route(lo.cuda(), 3, scoring)
