@@ -54,6 +54,9 @@ struct MxGemm {
   const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
   int kind;                 // kFew, kSmallTiles or kLargeTiles (mx4_gemm_kind)
+  int splits;               // K splits (mx4_gemm_splits; 0 and 1: none) and their partial sums [splits][rows][N]
+  float* parts;
+  int split_chunks;         // chunks of 128 inputs per split (set by the launch)
   const int* ids;           // without tiles: the expert of every row (few rows, taken one by one), or null
 
 #ifdef __HIPCC__
@@ -102,6 +105,7 @@ hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int6
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st);
 // The kernel for a product (MxGemm::kind); one choice for products that share a plan.
 int mx4_gemm_kind(const MxGemm& p);
+int mx4_gemm_splits(const MxGemm& p);
 int mx4_gemm_tile(const MxGemm& p);           // row tile height of its kind, for the plan
 bool mx4_gemm_takes_planes(const MxGemm& p);  // its kind wants binary16 x as planes
 // out[t] = res[t] + sum_j weights[t, j] x[t k + j] W[ids[t k + j]]^T for few tokens (p.rows = tokens k)

@@ -208,7 +208,7 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
 
   if (expert >= 0) {
     // x: rows past the tile's read zeros and touch no memory
-    const bool gather = p.xperm || p.ids;
+    const bool gather = p.xperm;
     const uint16_t* xb = gather ? p.x : p.x + (int64_t)first * p.K;
     const uint32_t xbytes = (uint32_t)((int64_t)(gather ? p.xrows : rows) * p.K * 2);
     __amdgpu_buffer_rsrc_t xr[NL];
@@ -218,7 +218,7 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const int lr = 16 * i + r;
-      const int xrow = lr >= rows ? 0 : p.xperm ? p.xperm[first + lr] / p.xdiv : p.ids ? (first + lr) / p.xdiv : lr;
+      const int xrow = lr >= rows ? 0 : p.xperm ? p.xperm[first + lr] / p.xdiv : lr;
       xoff[i] = lr >= rows ? kNowhere : (uint32_t)xrow * (uint32_t)p.K * 2u + h * 64;
     }
     const int kb = p.K / 32, chunks = (kb + 3) / 4;
@@ -307,8 +307,7 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
   }
 }
 
-// Rows of the block: a tile of the table, of a dense product, or the one row
-// (slot) of p.ids.
+// Rows of the block: a tile of the table, or of a dense product.
 template <int RT, int CT, int XS, bool FUSED, int W, int U>
 __global__ __launch_bounds__(64 * W, 2) void mx4_few_kernel(MxGemm p) {
   __shared__ f32x4 lds[few_lds(RT, FUSED ? 2 * CT : CT, W)];
@@ -324,9 +323,6 @@ __global__ __launch_bounds__(64 * W, 2) void mx4_few_kernel(MxGemm p) {
     if (tm >= *p.ntiles) return;
     const RowTile t = p.tiles[tm];
     expert = t.expert, first = t.first, rows = t.rows;
-  } else if (p.ids) {
-    expert = p.ids[tm], first = tm, rows = 1;
-    if (expert < 0 || expert >= p.E) return;       // a skipped slot: nothing reads its row
   }
   expert = __builtin_amdgcn_readfirstlane(expert);
   first = __builtin_amdgcn_readfirstlane(first);
@@ -334,26 +330,145 @@ __global__ __launch_bounds__(64 * W, 2) void mx4_few_kernel(MxGemm p) {
   few_rows<RT, CT, XS, FUSED, W, U>(p, expert, first, rows, tn * 16 * CT, lds);
 }
 
-// The experts' down projection of few tokens, one row each, with the weighted
-// sum: block (token, 16 columns), wave v takes the token's slot v % k' and a share
-// of its inputs, and the waves' sums, times the slots' weights, are added in
-// wave order.  k' = k rounded up to a divisor or multiple of the W waves.
-template <int XS, int W>
-__global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float* __restrict__ weights, int k) {
-  constexpr int NL = XS == kXPlanes ? 2 : 1;
-  __shared__ f32x4 lds[W * 64];
+// ----------------------------------------------------------- one-row kernels ----
+//
+// One row of x: the weights' bytes are all there is.  A wave takes U chunks at once; its
+// part of x is one load of 16 bytes per lane, put into the wave's own stretch of
+// LDS and read back by every column of the operand (all 16 rows of the MFMA's second operand hold the
+// same row; row 0's result counts).
+
+constexpr int kRowU = 4, kRowStretch = kRowU * 16;       // chunks in flight; u32x4 of LDS per wave and plane
+
+// Sums of a wave over the chunks 4 i .. 4 i + 3, i = first, first + step, ..., for the 16 columns of each of NW matrices
+// (four neighbours: 256 bytes of each row).
+template <int XS, int NW>
+__device__ __forceinline__ void row_sums(const __amdgpu_buffer_rsrc_t (&wr)[NW], const __amdgpu_buffer_rsrc_t (&sr)[NW],
+                                         const uint16_t* x, int64_t plane, int K, int first, int step, u32x4* own,
+                                         f32x4 (&acc)[NW]) {
+  constexpr int NP = XS == kXBf16 ? 1 : 2, NL = XS == kXPlanes ? 2 : 1;
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  const int kb = K / 32, chunks = (kb + 3) / 4;
+  __amdgpu_buffer_rsrc_t xr[NL];
+#pragma unroll
+  for (int q = 0; q < NL; ++q) xr[q] = buffer(x + q * plane, K * 2);
+  const uint32_t woff = (uint32_t)r * (uint32_t)(K / 2) + h * 16, soff = (uint32_t)(r * kb + h);
+  for (int c0 = first * kRowU; c0 < chunks; c0 += step * kRowU) {
+    u32x4 w[kRowU][NW], xv[NL];
+    uint32_t s[kRowU][NW];
+#pragma unroll
+    for (int u = 0; u < kRowU; ++u) {
+      const int c = c0 + u;
+      const bool in = 4 * c + h < kb;
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        w[u][j] = load16(wr[j], in ? woff + c * 64 : kNowhere);
+        s[u][j] = load1(sr[j], in ? soff + 4 * c : kNowhere);
+      }
+    }
+    // lane 16 u + p: the 16 bytes p of chunk u (past K: zeros, by the descriptor's end)
+#pragma unroll
+    for (int q = 0; q < NL; ++q) xv[q] = load16(xr[q], (uint32_t)c0 * 256u + lane * 16);
+    __builtin_amdgcn_sched_barrier(0);         // every load is out before the first is waited for
+    asm volatile("" ::: "memory");             // a wave's LDS accesses keep their order
+    if constexpr (XS == kXF16) {
+      bf16x8 hi, lo;
+      split_f16x8(__builtin_bit_cast(f16x8, xv[0]), hi, lo);
+      own[lane] = __builtin_bit_cast(u32x4, hi);
+      own[kRowStretch + lane] = __builtin_bit_cast(u32x4, lo);
+    } else {
+#pragma unroll
+      for (int q = 0; q < NL; ++q) own[q * kRowStretch + lane] = xv[q];
+    }
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < kRowU; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        bf16x8 b[NP];
+#pragma unroll
+        for (int q = 0; q < NP; ++q) b[q] = __builtin_bit_cast(bf16x8, own[q * kRowStretch + 16 * u + 4 * h + k]);
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+          const bf16x8 a = mx4_word(w[u][j][k], e8m0_operand(s[u][j]));
+#pragma unroll
+          for (int q = 0; q < NP; ++q) acc[j] = mfma_bf16(a, b[q], acc[j]);
+        }
+      }
+  }
+}
+
+// 16 columns (SwiGLU: of both matrices) of one row per block: a dense product's row, or the slot
+// of p.ids.  The W waves' sums are added in wave order.
+template <int XS, bool FUSED, int W>
+__global__ __launch_bounds__(64 * W) void mx4_row_kernel(MxGemm p) {
+  constexpr int NW = FUSED ? 2 : 1, NP = XS == kXBf16 ? 1 : 2;
+  __shared__ u32x4 xs[W * NP * kRowStretch];
+  __shared__ f32x4 part[W * NW * 4];
 #ifdef SWQ_LDS_POISON
-  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  lds_poison(xs, sizeof(xs), kPoisonFloat);
+  lds_poison(part, sizeof(part), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h = lane >> 4;
+  const int ntn = (p.N + 15) / 16;
+  const int slot = blockIdx.x / ntn, n0 = (blockIdx.x - slot * ntn) * 16;
+  const int expert = p.ids ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : 0;
+  if (expert < 0 || expert >= p.E) return;     // a skipped slot: nothing reads its row
+  const int kb = p.K / 32, cols = min(16, p.N - n0);
+  const int64_t wrow = (int64_t)expert * p.N + n0;
+  __amdgpu_buffer_rsrc_t wr[NW], sr[NW];
+#pragma unroll
+  for (int j = 0; j < NW; ++j) {
+    wr[j] = buffer((j ? p.w2 : p.w) + wrow * (p.K / 8), cols * (p.K / 2));
+    sr[j] = buffer((j ? p.s2 : p.s) + wrow * kb, cols * kb);
+  }
+  f32x4 acc[NW];
+#pragma unroll
+  for (int j = 0; j < NW; ++j) acc[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  row_sums<XS, NW>(wr, sr, p.x + (int64_t)(slot / p.xdiv) * p.K, p.plane, p.K, wave, W, xs + wave * NP * kRowStretch,
+                   acc);
+  if (r == 0) {
+#pragma unroll
+    for (int j = 0; j < NW; ++j) part[(wave * NW + j) * 4 + h] = acc[j];
+  }
+  __syncthreads();
+  if (wave == 0 && r == 0) {
+    f32x4 g[NW];
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+      g[j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int v = 0; v < W; ++v) g[j] += part[(v * NW + j) * 4 + h];
+    }
+    if constexpr (FUSED) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[0][e] = silu_times(g[0][e], g[1][e]);
+    }
+    finish4(p, (int64_t)slot * p.N, n0 + 4 * h, g[0]);
+  }
+}
+
+// The experts' down projection of few tokens with the weighted sum: block (token, 16
+// columns).  `share` waves (a power of two) take a slot together, the W / share
+// teams take the token's slots in turn, and the waves' sums, times the slots' weights,
+// are added in wave order.
+template <int XS, int W>
+__global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float* __restrict__ weights, int k,
+                                                          int share) {
+  constexpr int NP = XS == kXBf16 ? 1 : 2;
+  __shared__ u32x4 xs[W * NP * kRowStretch];
+  __shared__ f32x4 part[W * 4];
+#ifdef SWQ_LDS_POISON
+  lds_poison(xs, sizeof(xs), kPoisonFloat);
+  lds_poison(part, sizeof(part), kPoisonFloat);
   __syncthreads();
 #endif
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, h = lane >> 4;
   const int ntn = (p.N + 15) / 16;
   const int t = blockIdx.x / ntn, n0 = (blockIdx.x - t * ntn) * 16;
-  const int kb = p.K / 32, chunks = (kb + 3) / 4, cols = p.N - n0;
-  // waves per slot: the largest power of two that leaves no slot waiting
-  int share = W;
-  while (share > 1 && share * k > W) share >>= 1;
+  const int kb = p.K / 32, cols = min(16, p.N - n0);
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int j = wave / share; j < k; j += W / share) {
     const int slot = t * k + j;
@@ -361,46 +476,20 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
     if (expert < 0 || expert >= p.E) continue;
     const float wt = weights[slot];
     const int64_t wrow = (int64_t)expert * p.N + n0;
-    const __amdgpu_buffer_rsrc_t wr = buffer(p.w + wrow * (p.K / 8), min(cols, 16) * (p.K / 2));
-    const __amdgpu_buffer_rsrc_t sr = buffer(p.s + wrow * kb, min(cols, 16) * kb);
-    __amdgpu_buffer_rsrc_t xr[NL];
+    const __amdgpu_buffer_rsrc_t wr[1] = {buffer(p.w + wrow * (p.K / 8), cols * (p.K / 2))};
+    const __amdgpu_buffer_rsrc_t sr[1] = {buffer(p.s + wrow * kb, cols * kb)};
+    f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    row_sums<XS, 1>(wr, sr, p.x + (int64_t)slot * p.K, p.plane, p.K, wave % share, share, xs + wave * NP * kRowStretch,
+                    acc);
 #pragma unroll
-    for (int q = 0; q < NL; ++q) xr[q] = buffer(p.x + q * p.plane + (int64_t)slot * p.K, p.K * 2);
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int U = 2;
-    for (int c0 = wave % share; c0 < chunks; c0 += share * U) {
-      u32x4 w[U], x[U][NL][4];
-      uint32_t s[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * share;
-        const bool in = 4 * c + h < kb;
-        w[u] = load16(wr, in ? (uint32_t)r * (uint32_t)(p.K / 2) + c * 64 + h * 16 : kNowhere);
-        s[u] = load1(sr, in ? (uint32_t)(r * kb + 4 * c + h) : kNowhere);
-#pragma unroll
-        for (int q = 0; q < NL; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[u][q][e] = load16(xr[q], in && r == 0 ? c * 256 + h * 64 + e * 16 : kNowhere);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bf16x8 a = mx4_word(w[u][e], e8m0_operand(s[u]));
-#pragma unroll
-          for (int q = 0; q < NL; ++q) acc = mfma_bf16(a, __builtin_bit_cast(bf16x8, x[u][q][e]), acc);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = fmaf(wt, acc[e], sum[e]);
+    for (int e = 0; e < 4; ++e) sum[e] = fmaf(wt, acc[0][e], sum[e]);
   }
-  lds[wave * 64 + lane] = sum;
+  if (r == 0) part[wave * 4 + h] = sum;
   __syncthreads();
   if (wave == 0 && r == 0) {
     f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int v = 0; v < W; ++v) y += lds[v * 64 + lane];
+    for (int v = 0; v < W; ++v) y += part[v * 4 + h];
     finish4(p, (int64_t)t * p.N, n0 + 4 * h, y);
   }
 }
@@ -415,7 +504,7 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
 // by WM waves only).  x goes through LDS, [BM * NP][128] bf16, two buffers, by
 // loads that write LDS; 16-byte unit u of a row sits at u ^ (row & 15), so the
 // sixteen rows that a read touches lie in different banks.
-template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED>
+template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   constexpr int W = WM * WN, BM = 16 * MF * WM, ROWS = BM * NP, BN = 16 * NF * WN, BNO = FUSED ? BN / 2 : BN;
   constexpr int DMA = ROWS / (4 * W);           // loads per lane and chunk, four rows each per wave
@@ -432,6 +521,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   const int ntn = (p.N + BNO - 1) / BNO;
   int tm, tn;
   if (!tile_of(blockIdx.x, p.tiles ? *p.ntiles : (p.rows + BM - 1) / BM, ntn, tm, tn)) return;
+  const int split = SPLIT ? blockIdx.y : 0;     // of K: its share of the chunks, its part of the partial sums
   int expert = 0, first = tm * BM, rows = min(BM, p.rows - first);
   if (p.tiles) {
     const RowTile t = p.tiles[tm];
@@ -447,7 +537,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
-  const int chunks = (p.K + 127) / 128;
+  const int c_begin = SPLIT ? split * p.split_chunks : 0;
+  const int chunks = SPLIT ? min((p.K + 127) / 128, c_begin + p.split_chunks) : (p.K + 127) / 128;
   if (expert >= 0) {
     // x: rows of the tile from its first (contiguous rows) or from row 0 (gathered)
     const uint16_t* xb = p.xperm ? p.x : p.x + (int64_t)first * p.K;
@@ -469,7 +560,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
     const auto load_x = [&]<int i>(int c, int buf) SWQ_INLINE {
       dma16(xr[(i * 4 * W) / BM],
             __builtin_amdgcn_readfirstlane(lds_addr(lds) + buf * (ROWS * 256) + (i * 4 * W + wave * 4) * 256),
-            c * 128 + du * 8 < p.K ? xoff[i] + (uint32_t)c * 256u : kNowhere);
+            (!SPLIT || c < chunks) && c * 128 + du * 8 < p.K ? xoff[i] + (uint32_t)c * 256u : kNowhere);
     };
 
     // W: the columns of this wave; rows past N read zeros
@@ -493,14 +584,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
     uint32_t sc[S][NF];
     const auto load_w = [&]<int b, int j>(int c) SWQ_INLINE {
       constexpr bool up = FUSED && j >= NF / 2;
-      const bool in = 4 * c + h < kb;
+      const bool in = (!SPLIT || c < chunks) && 4 * c + h < kb;
       wc[b][j] = load16(up ? wr1 : wr0, in ? woff[j] + c * 64 : kNowhere);
       sc[b][j] = load1(up ? sr1 : sr0, in ? soff[j] + 4 * c : kNowhere);
     };
     constexpr int LOADS = 2 * NF + DMA;
     each<S - 1>([&]<int b>() SWQ_INLINE {
-      each<NF>([&]<int j>() SWQ_INLINE { load_w.template operator()<b, j>(b); });
-      each<DMA>([&]<int i>() SWQ_INLINE { load_x.template operator()<i>(b, b); });
+      each<NF>([&]<int j>() SWQ_INLINE { load_w.template operator()<b, j>(c_begin + b); });
+      each<DMA>([&]<int i>() SWQ_INLINE { load_x.template operator()<i>(c_begin + b, b); });
       __builtin_amdgcn_sched_barrier(0);        // the waits below count on the loads' order
     });
 
@@ -540,7 +631,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
         __builtin_amdgcn_sched_barrier(0);
       });
     };
-    for (int c = 0; c < chunks; c += S)
+    for (int c = c_begin; c < chunks; c += S)
       each<S>([&]<int b>() SWQ_INLINE { chunk.template operator()<b>(c + b); });
     wait_vmcnt<0>();           // no load past the end may still write LDS
   }
@@ -564,9 +655,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
     }
     flush16<NT>(p, buf, v, rows - r0, n0 + 16 * NT * wn, [&](int lr) {
       const int slot = first + r0 + lr;
-      return (int64_t)(p.perm ? p.perm[slot] : slot);
+      return (int64_t)(p.perm ? p.perm[slot] : slot) + (int64_t)split * p.rows;
     });
   }
+}
+
+// The sums of a K split: four neighbouring outputs per thread.
+__global__ __launch_bounds__(256) void mx4_join_kernel(MxGemm p) {
+  const int per = (p.N + 3) / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / per;
+  const int n = (int)(i - row * per) * 4;
+  if (row >= p.rows) return;
+  const float* part = (const float*)p.parts + row * p.N + n;
+  const int64_t step = (int64_t)p.rows * p.N;
+  f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.N % 4 == 0) {
+    for (int s = 0; s < p.splits; ++s) y += *(const f32x4*)(part + s * step);
+  } else {
+    for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) y[e] += part[s * step + e];
+  }
+  finish4(p, row * p.N, n, y);
 }
 
 // ----------------------------------------------------- two MXFP4 operands ----
@@ -888,22 +999,39 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 // What a product runs on.  Measured on one MI355X (x bf16, us; K x N = 4096 x 14336):
 //   rows          1     16    32    64    128   256   1024  2048
 //   few-row       12    14    16    26    50    96    -     -
-//   64 x 128      -     -     -     24    24    40    150   278
+//   64 x 128      -     -     -     24    24    47    150   278
 //   128 x 256     55    57    57    58    62    64    115   215
-// and for 1024 rows of 5632 x 2048 62, 30 and 84: the few-row kernel up to 48 rows (a grouped
-// product: of an average expert), the 128 x 256 tiles once they fill three quarters of
-// the CUs (one such tile takes 1.9 us per chunk, a 64 x 128 tile 0.62), else 64 x 128.
+// and for 1024 rows of 5632 x 2048 62, 30 and 84.  Where their tiles leave CUs idle the 64 x 128 kernel splits
+// K (K x N = 5632 x 2048, 32 / 64 / 256 rows: few-row 15 / 26 / 27, split 13 / 15 / 19; 8192 x 512 20 / 35 / 35
+// against 14 / 15 / 18; on small weights, K N <= 2^20, the second launch costs more than it
+// gives: 1024 x 1024, 256 rows, 8 against 11).  A CU takes 1.9 us per chunk of a 128 x 256
+// tile and 0.62 per chunk of a 64 x 128 one, whether it holds one or two blocks: the
+// shapes are compared by the tiles of the fullest CU.
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 int mx4_gemm_kind(const MxGemm& p) {
   const int64_t each = p.rows / p.E;
-  if (each <= 48) return kFew;
-  const int64_t rows128 = p.E == 1 ? (p.rows + 127) / 128 : p.rows / 128 + p.E / 2;
-  const int64_t n = p.w2 ? 128 : 256;
-  return 4 * rows128 * ((p.N + n - 1) / n) >= 3 * device_cus() ? kLargeTiles : kSmallTiles;
+  if (const char* e = getenv("SWQ_MX4_KIND")) return atoi(e);
+  if (each <= (p.E > 1 ? 48 : 24) || (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20))) return kFew;
+  const int64_t part = p.E == 1 ? 0 : p.E / 2;           // half a tile per expert for its last, partial one
+  const int64_t n = p.w2 ? 2 * (int64_t)p.N : p.N, cus = device_cus();
+  const int64_t large = ceil_div((ceil_div(p.rows, 128) + part) * ceil_div(n, 256), cus);
+  const int64_t small = ceil_div((ceil_div(p.rows, 64) + part) * ceil_div(n, 128), cus);
+  return 190 * large < 62 * small ? kLargeTiles : kSmallTiles;
+}
+
+// K split of 64 x 128 tiles that leave half the CUs without one: at least four chunks each, at most 16 ways.
+int mx4_gemm_splits(const MxGemm& p) {
+  if (p.kind != kSmallTiles || p.tiles || p.w2) return 1;
+  const int64_t tiles = ceil_div(p.rows, 64) * ceil_div(p.N, 128), chunks = ceil_div(p.K, 128);
+  if (const char* e = getenv("SWQ_MX4_SPLIT")) return atoi(e);
+  int64_t n = std::min<int64_t>(std::min<int64_t>(device_cus() / tiles, chunks / 4), 16);
+  if (n < 2) return 1;
+  return (int)ceil_div(chunks, ceil_div(chunks, n));     // no empty split
 }
 
 // Row tiles of 16 of the few-row kernel, by the rows of an average expert.
 static int few_tiles(const MxGemm& p) {
-  if (p.ids && !p.tiles) return 1;
   const int64_t each = p.rows / p.E;
   return p.E == 1 ? (p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4) : each <= 8 ? 1 : each <= 20 ? 2 : 4;
 }
@@ -921,14 +1049,30 @@ static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
   const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + BM - 1) / BM, ntn = (p.N + BNO - 1) / BNO;
   const int64_t blocks = (ntm * ntn + 7) / 8 * 8;
   if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-  mx4_gemm_kernel<MF, NF, WM, WN, NP, S, FUSED><<<dim3((unsigned)blocks), 64 * WM * WN, 0, st>>>(p);
+  if constexpr (!FUSED && NF == 2) {
+    if (p.splits > 1) {
+      // K split: float32 partial sums [split][row][column] in the workspace, added in split order
+      MxGemm q = p;
+      q.split_chunks = ((p.K + 127) / 128 + p.splits - 1) / p.splits;
+      q.out = p.parts;
+      q.out_type = kTypeF32;
+      q.res = nullptr;
+      q.vec = p.N % 8 == 0 ? 2 : 0;
+      mx4_gemm_kernel<MF, NF, WM, WN, NP, S, FUSED, true>
+          <<<dim3((unsigned)blocks, (unsigned)p.splits), 64 * WM * WN, 0, st>>>(q);
+      const int64_t threads = (int64_t)p.rows * ((p.N + 3) / 4);
+      mx4_join_kernel<<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(p);
+      return hipGetLastError();
+    }
+  }
+  mx4_gemm_kernel<MF, NF, WM, WN, NP, S, FUSED, false><<<dim3((unsigned)blocks), 64 * WM * WN, 0, st>>>(p);
   return hipGetLastError();
 }
 
 template <int RT, int CT, int XS, bool FUSED, int W, int U>
 static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
   const int64_t ntn = (p.N + 16 * CT - 1) / (16 * CT);
-  const int64_t ntm = p.tiles ? p.max_tiles : p.ids ? p.rows : (p.rows + 16 * RT - 1) / (16 * RT);
+  const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + 16 * RT - 1) / (16 * RT);
   if (ntm * ntn >= (1LL << 31)) return hipErrorInvalidValue;
   mx4_few_kernel<RT, CT, XS, FUSED, W, U><<<dim3((unsigned)(ntm * ntn)), 64 * W, 0, st>>>(p);
   return hipGetLastError();
@@ -939,7 +1083,7 @@ static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
 template <int RT, int XS, bool FUSED>
 static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
   constexpr int D = FUSED ? 2 : 1;
-  const int64_t tiles = p.tiles ? std::min<int64_t>(p.max_tiles, p.rows) : p.ids ? p.rows : (p.rows + 16 * RT - 1) / (16 * RT);
+  const int64_t tiles = p.tiles ? std::min<int64_t>(p.max_tiles, p.rows) : (p.rows + 16 * RT - 1) / (16 * RT);
   const int64_t need = device_cus() * 7 / 8;
   if (p.N / (16 * 4 / D) * tiles >= need) return launch_few_as<RT, 4 / D, XS, FUSED, 8, 1>(p, st);
   if (p.N / (16 * 2 / D) * tiles >= need || FUSED) return launch_few_as<RT, 2 / D, XS, FUSED, 8, RT == 1 ? 2 : 1>(p, st);
@@ -947,8 +1091,18 @@ static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
   return hipErrorInvalidValue;
 }
 
+template <int XS, bool FUSED, int W>
+static hipError_t launch_row(const MxGemm& p, hipStream_t st) {
+  const int64_t blocks = (int64_t)p.rows * ((p.N + 15) / 16);
+  if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+  mx4_row_kernel<XS, FUSED, W><<<dim3((unsigned)blocks), 64 * W, 0, st>>>(p);
+  return hipGetLastError();
+}
+
 template <int XS, bool FUSED>
 static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
+  if (!p.tiles && (p.ids || p.rows == 1))      // rows one by one; four waves cover 2048 inputs at once
+    return p.K <= 4 * kRowU * 128 ? launch_row<XS, FUSED, 4>(p, st) : launch_row<XS, FUSED, 8>(p, st);
   const int rt = few_tiles(p);
   return rt == 1 ? launch_few_rt<1, XS, FUSED>(p, st) : rt == 2 ? launch_few_rt<2, XS, FUSED>(p, st)
                                                                 : launch_few_rt<4, XS, FUSED>(p, st);
@@ -971,10 +1125,15 @@ hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st) {
 }
 
 hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st) {
+  constexpr int W = 16;
   const int64_t blocks = (int64_t)(p.rows / k) * ((p.N + 15) / 16);
   if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-  if (p.xsrc == kXPlanes) mx4_down_kernel<kXPlanes, 16><<<dim3((unsigned)blocks), 1024, 0, st>>>(p, weights, k);
-  else mx4_down_kernel<kXBf16, 16><<<dim3((unsigned)blocks), 1024, 0, st>>>(p, weights, k);
+  // as many waves per slot as leave no slot waiting, and no more than it has chunks for
+  int share = W;
+  while (share > 1 && (share * k > W || (share - 1) * kRowU * 128 >= p.K)) share >>= 1;
+  const dim3 grid((unsigned)blocks);
+  if (p.xsrc == kXPlanes) mx4_down_kernel<kXPlanes, W><<<grid, 64 * W, 0, st>>>(p, weights, k, share);
+  else mx4_down_kernel<kXBf16, W><<<grid, 64 * W, 0, st>>>(p, weights, k, share);
   return hipGetLastError();
 }
 
