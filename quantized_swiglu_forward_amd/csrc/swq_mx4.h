@@ -18,7 +18,7 @@ inline int type_bytes(int t) { return t == kTypeF32 ? 4 : 2; }
 enum : int { kXBf16 = 0, kXF16 = 1, kXPlanes = 2 };
 
 // Kernels of a product with MXFP4 weights.
-enum : int { kFew, kSmallTiles, kLargeTiles };
+enum : int { kFew, kSmallTiles, kMidTiles, kLargeTiles };
 
 // One tile of rows of a grouped product.
 struct RowTile {
@@ -53,7 +53,7 @@ struct MxGemm {
   const int* ntiles;
   const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
-  int kind;                 // kFew, kSmallTiles or kLargeTiles (mx4_gemm_kind)
+  int kind;                 // kFew .. kLargeTiles (mx4_gemm_kind)
   int splits;               // K splits (mx4_gemm_splits; 0 and 1: none) and their partial sums [splits][rows][N]
   float* parts;
   int split_chunks;         // chunks of 128 inputs per split (set by the launch)

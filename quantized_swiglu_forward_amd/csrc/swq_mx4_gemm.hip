@@ -508,7 +508,7 @@ template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   constexpr int W = WM * WN, BM = 16 * MF * WM, ROWS = BM * NP, BN = 16 * NF * WN, BNO = FUSED ? BN / 2 : BN;
   constexpr int DMA = ROWS / (4 * W);           // loads per lane and chunk, four rows each per wave
-  static_assert(ROWS % (4 * W) == 0 && (!FUSED || NF % 2 == 0));
+  static_assert(ROWS % (4 * W) == 0 && W % 4 == 0 && (!FUSED || NF % 2 == 0));
   __shared__ __attribute__((aligned(1024))) char lds[S * ROWS * 256];
 #ifdef SWQ_LDS_POISON
   lds_poison(lds, sizeof(lds), kPoisonFloat);
@@ -996,28 +996,33 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 
 }  // namespace
 
-// What a product runs on.  Measured on one MI355X (x bf16, us; K x N = 4096 x 14336):
-//   rows          1     16    32    64    128   256   1024  2048
-//   few-row       12    14    16    26    50    96    -     -
-//   64 x 128      -     -     -     24    24    47    150   278
-//   128 x 256     55    57    57    58    62    64    115   215
-// and for 1024 rows of 5632 x 2048 62, 30 and 84.  Where their tiles leave CUs idle the 64 x 128 kernel splits
-// K (K x N = 5632 x 2048, 32 / 64 / 256 rows: few-row 15 / 26 / 27, split 13 / 15 / 19; 8192 x 512 20 / 35 / 35
-// against 14 / 15 / 18; on small weights, K N <= 2^20, the second launch costs more than it
-// gives: 1024 x 1024, 256 rows, 8 against 11).  A CU takes 1.9 us per chunk of a 128 x 256
-// tile and 0.62 per chunk of a 64 x 128 one, whether it holds one or two blocks: the
-// shapes are compared by the tiles of the fullest CU.
+// What a product runs on: the few-row kernel up to 24 rows (a grouped product: 48 of an average
+// expert), else the tile shape whose fullest CU is done first.  Measured on one
+// MI355X, a CU takes 1.77 us per chunk of a 128 x 256 tile, 0.98 of a 128 x 128 and
+// 0.62 of a 64 x 128 one, however many blocks it holds (bf16 x; us):
+//   rows x K x N          64 x 128   128 x 128   128 x 256
+//   1024 x 5632 x 2048        34         48          82
+//   512 x 2048 x 5632         24         21          36
+//   6144 x 2048 x 1408        54         49          56
+//   2048 x 4096 x 14336      286        217         218
+//   8192 x 2560 x 10240      471        391         353
+// Where their tiles leave CUs idle the 64 x 128 kernel splits K (K x N = 5632 x 2048,
+// 32 / 64 / 256 rows: few-row kernel 15 / 26 / 27, split 13 / 15 / 19; 8192 x 512 20 / 35 / 35 against
+// 14 / 15 / 18).  On small weights, K N <= 2^20, the second launch costs more than
+// it gives: 1024 x 1024, 256 rows, few-row 8, split 11.
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int mx4_gemm_kind(const MxGemm& p) {
   const int64_t each = p.rows / p.E;
-  if (const char* e = getenv("SWQ_MX4_KIND")) return atoi(e);
   if (each <= (p.E > 1 ? 48 : 24) || (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20))) return kFew;
   const int64_t part = p.E == 1 ? 0 : p.E / 2;           // half a tile per expert for its last, partial one
   const int64_t n = p.w2 ? 2 * (int64_t)p.N : p.N, cus = device_cus();
-  const int64_t large = ceil_div((ceil_div(p.rows, 128) + part) * ceil_div(n, 256), cus);
-  const int64_t small = ceil_div((ceil_div(p.rows, 64) + part) * ceil_div(n, 128), cus);
-  return 190 * large < 62 * small ? kLargeTiles : kSmallTiles;
+  const auto cost = [&](int bm, int bn, int us) {
+    return us * ceil_div((ceil_div(p.rows, bm) + part) * ceil_div(n, bn), cus);
+  };
+  const int64_t large = cost(128, 256, 177), mid = cost(128, 128, 98), small = cost(64, 128, 62);
+  if (small <= mid && small <= large) return kSmallTiles;
+  return mid < large ? kMidTiles : kLargeTiles;
 }
 
 // K split of 64 x 128 tiles that leave half the CUs without one: at least four chunks each, at most 16 ways.
@@ -1049,7 +1054,7 @@ static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
   const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + BM - 1) / BM, ntn = (p.N + BNO - 1) / BNO;
   const int64_t blocks = (ntm * ntn + 7) / 8 * 8;
   if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
-  if constexpr (!FUSED && NF == 2) {
+  if constexpr (!FUSED && MF == 4 && NF == 2) {
     if (p.splits > 1) {
       // K split: float32 partial sums [split][row][column] in the workspace, added in split order
       MxGemm q = p;
@@ -1117,7 +1122,9 @@ static hipError_t launch_gemm(const MxGemm& p, hipStream_t st) {
                              : launch_few<kXPlanes, FUSED>(p, st);
   if (p.xsrc != kXBf16)
     return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 2, 2, FUSED>(p, st) : launch_tiled<4, 4, 1, 4, 2, 2, FUSED>(p, st);
-  return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 1, 4, FUSED>(p, st) : launch_tiled<8, 4, 1, 4, 1, 2, FUSED>(p, st);
+  return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 1, 4, FUSED>(p, st)
+         : k == kMidTiles ? launch_tiled<8, 2, 1, 4, 1, 2, FUSED>(p, st)
+                          : launch_tiled<8, 4, 1, 4, 1, 2, FUSED>(p, st);
 }
 
 hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st) {
