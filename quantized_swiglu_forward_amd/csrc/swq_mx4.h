@@ -41,6 +41,7 @@ struct MxGemm {
   void* out;                // [rows, N] in out_type; SwiGLU with hidden_planes: bf16 planes
   int64_t out_plane;        // elements between the planes of a split hidden tensor
   int rows, K, N, E;
+  int64_t wrows;            // rows of W from one expert to the next (N, or more where the product takes some columns)
   int xsrc;                 // kXBf16, kXF16, kXPlanes
   const int* xperm;         // slot -> row (x row: that / xdiv), or null: slot s reads x row s
   int xdiv;
@@ -117,8 +118,9 @@ hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, i
                         hipStream_t st);
 hipError_t launch_plan(const RoutePlan& p, hipStream_t st);
 // out[t] = residual[t] + sum_j weights[t, j] part[t k + j] over the slots whose id is an expert
+// (part has rows of N; res and out rows of ld, from their first column on)
 hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
-                          int k, int E, int N, int type, int out_type, void* out, hipStream_t st);
+                          int k, int E, int N, int64_t ld, int type, int out_type, void* out, hipStream_t st);
 
 // Compute units of the current device (swq_api.hip).
 int device_cus();

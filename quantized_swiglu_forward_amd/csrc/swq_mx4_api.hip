@@ -10,6 +10,9 @@ namespace {
 
 constexpr int kWsSlot = 2;            // the experts' workspace beside the MLP's two
 constexpr int64_t kDirectTokens = 4;  // most tokens whose slots are taken one by one
+// The experts' float32 outputs that wait for their sum: what the 256 MB last-level cache still holds when the
+// sum reads them (4096 tokens, 8 of 64 experts, 2048 columns, 268 MB: in one piece 529 us, in two 515, in three 558).
+constexpr int64_t kPartBytes = int64_t(160) << 20;
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 20;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
@@ -33,6 +36,12 @@ int check_codes(const uint32_t* W, const void* s) {
 }
 
 int check_status(hipError_t e) { return e == hipSuccess ? SWQ_OK : SWQ_ERR_HIP; }
+
+// Columns of the experts' outputs that are computed and summed at once.
+int64_t part_columns(int64_t P, int64_t Ho) {
+  const int64_t parts = (P * Ho * 4 + kPartBytes - 1) / kPartBytes;
+  return ((Ho + parts - 1) / parts + 255) / 256 * 256;
+}
 
 // Bytes of a plan in the workspace: the tile count, the tile table, the order.
 struct PlanLayout {
@@ -132,6 +141,7 @@ int swiglu_q_mx4_linear(const void* x, const uint32_t* W, const void* s, const v
   g.K = (int)K;
   g.N = (int)N;
   g.E = 1;
+  g.wrows = N;
   g.xsrc = type == SWQ_TYPE_F16 ? kXF16 : kXBf16;
   g.xdiv = 1;
   g.type = type;
@@ -195,6 +205,7 @@ int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uin
   g.K = (int)K;
   g.N = (int)N;
   g.E = (int)E;
+  g.wrows = N;
   g.xsrc = type == SWQ_TYPE_F16 ? kXF16 : kXBf16;
   g.xdiv = 1;
   g.type = type;
@@ -256,6 +267,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   g.K = (int)H;
   g.N = (int)I;
   g.E = (int)E;
+  g.wrows = I;
   g.xsrc = f16 ? kXF16 : kXBf16;
   g.xdiv = (int)k;
   g.type = type;
@@ -272,7 +284,8 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   const int tile = mx4_gemm_tile(g);
   const PlanLayout l = direct ? PlanLayout{0, 0, 0} : plan_layout(P, E, tile, true);
   const int64_t hidden = align256(P * I * 2) * (f16 ? 2 : 1);
-  const int64_t part = l.total + hidden, xplanes = part + (direct ? 0 : align256(P * Ho * 4));
+  const int64_t part = l.total + hidden, cols = part_columns(P, Ho);
+  const int64_t xplanes = part + (direct ? 0 : align256(P * cols * 4));
   void* ws_v = nullptr;
   rc = stream_workspace(stream, (size_t)(xplanes + (direct ? 0 : planes_bytes(g, T))), &ws_v, kWsSlot);
   if (rc != SWQ_OK) return rc;
@@ -303,10 +316,10 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   d.perm = perm;
   d.K = (int)I;
   d.N = (int)Ho;
+  d.wrows = Ho;
   d.xsrc = f16 ? kXPlanes : kXBf16;
   d.out_type = SWQ_TYPE_F32;
   d.hidden_planes = 0;
-  d.vec = vec_ok(Ho, d.out, nullptr, SWQ_TYPE_F32);
   if (direct) {
     d.res = (const uint16_t*)residual;
     d.out = out;
@@ -314,10 +327,19 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
     d.vec = vec_ok(Ho, out, residual, out_mode);
     return check_status(launch_mx4_down(d, weights, (int)k, stream));
   }
-  rc = check_status(launch_mx4_gemm(d, stream));
-  if (rc != SWQ_OK) return rc;
-  return check_status(launch_combine((const float*)(ws + part), ids, weights, (const uint16_t*)residual, T, (int)k,
-                                     (int)E, (int)Ho, type, out_mode, out, stream));
+  for (int64_t n = 0; n < Ho; n += cols) {
+    d.N = (int)(Ho - n < cols ? Ho - n : cols);
+    d.w = Wd + n * (I / 8);
+    d.s = (const uint8_t*)sd + n * (I / 32);
+    d.vec = vec_ok(d.N, d.out, nullptr, SWQ_TYPE_F32);
+    rc = check_status(launch_mx4_gemm(d, stream));
+    if (rc != SWQ_OK) return rc;
+    rc = check_status(launch_combine((const float*)(ws + part), ids, weights,
+                                     residual ? (const uint16_t*)residual + n : nullptr, T, (int)k, (int)E, d.N, Ho, type,
+                                     out_mode, (char*)out + n * type_bytes(out_mode), stream));
+    if (rc != SWQ_OK) return rc;
+  }
+  return SWQ_OK;
 }
 
 }  // extern "C"

@@ -9,8 +9,6 @@
 // row r, four neighbours for one store.  The products are exact (8 by 2
 // significant bits); only the float32 sums and the last rounding are not.
 // binary16 rows are split into two bf16 operands (split_f16), exact too.
-#include <stdlib.h>
-
 #include <algorithm>
 
 #include "swq_mx4.h"
@@ -222,7 +220,7 @@ __device__ __forceinline__ void few_rows(const MxGemm& p, int expert, int first,
       xoff[i] = lr >= rows ? kNowhere : (uint32_t)xrow * (uint32_t)p.K * 2u + h * 64;
     }
     const int kb = p.K / 32, chunks = (kb + 3) / 4;
-    const int64_t wrow = (int64_t)expert * p.N + n0;
+    const int64_t wrow = (int64_t)expert * p.wrows + n0;
     const int cols = p.N - n0;
     const int wbytes = min(cols, 16 * CT) * (p.K / 2);
     const __amdgpu_buffer_rsrc_t wr[2] = {buffer(p.w + wrow * (p.K / 8), wbytes),
@@ -416,7 +414,7 @@ __global__ __launch_bounds__(64 * W) void mx4_row_kernel(MxGemm p) {
   const int expert = p.ids ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : 0;
   if (expert < 0 || expert >= p.E) return;     // a skipped slot: nothing reads its row
   const int kb = p.K / 32, cols = min(16, p.N - n0);
-  const int64_t wrow = (int64_t)expert * p.N + n0;
+  const int64_t wrow = (int64_t)expert * p.wrows + n0;
   __amdgpu_buffer_rsrc_t wr[NW], sr[NW];
 #pragma unroll
   for (int j = 0; j < NW; ++j) {
@@ -475,7 +473,7 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
     const int expert = __builtin_amdgcn_readfirstlane(p.ids[slot]);
     if (expert < 0 || expert >= p.E) continue;
     const float wt = weights[slot];
-    const int64_t wrow = (int64_t)expert * p.N + n0;
+    const int64_t wrow = (int64_t)expert * p.wrows + n0;
     const __amdgpu_buffer_rsrc_t wr[1] = {buffer(p.w + wrow * (p.K / 8), cols * (p.K / 2))};
     const __amdgpu_buffer_rsrc_t sr[1] = {buffer(p.s + wrow * kb, cols * kb)};
     f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
@@ -565,7 +563,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
 
     // W: the columns of this wave; rows past N read zeros
     const int kb = p.K / 32;
-    const int64_t wrow = (int64_t)expert * p.N + n0;
+    const int64_t wrow = (int64_t)expert * p.wrows + n0;
     const int wn_rows = p.N - n0;
     uint32_t woff[NF], soff[NF];
 #pragma unroll
@@ -696,8 +694,9 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(MxGemm p) {
 __global__ __launch_bounds__(256) void mx4_scale_kernel(const uint8_t* __restrict__ sa, int M,
                                                         const uint8_t* __restrict__ sw, int N, int kb, int stages,
                                                         int pad_a, int pad_w, uint16_t* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [row][stage]
-  const int row = (int)(i / stages), t = (int)(i - (int64_t)row * stages);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [32 rows][stage][row]
+  const int64_t group = i / (32 * stages);
+  const int t = (int)((i - group * 32 * stages) >> 5), row = (int)group * 32 + (int)(i & 31);
   if (row >= pad_a + pad_w) return;
   const bool is_a = row < pad_a;
   const int at = is_a ? row : row - pad_a;
@@ -706,7 +705,7 @@ __global__ __launch_bounds__(256) void mx4_scale_kernel(const uint8_t* __restric
   uint32_t b[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) b[e] = live && 4 * t + e < kb ? s[4 * t + e] : 0u;
-  uint16_t* o = out + ((int64_t)(row / 32) * stages + t) * 64 + (row & 31);
+  uint16_t* o = out + (group * stages + t) * 64 + (row & 31);
   o[0] = (uint16_t)(b[0] | b[2] << 8);
   o[32] = (uint16_t)(b[1] | b[3] << 8);
 }
@@ -767,23 +766,25 @@ __device__ __forceinline__ void store_wide(const Mx4Matmul& p, const f32x16 (&ac
   }
 }
 
-// 64 AF x 64 WF outputs per tile, 2 x 2 waves of 32 AF x 32 WF.  A stage is 128 inputs, 64
-// bytes a row of each operand and its scales, S stages in LDS; a k-step reads
-// its successor's operands into registers while its MFMAs run, and a stage that
-// has been read makes room for the loads of the one S ahead.  16-byte unit u of a row sits at
-// u ^ (row / 4 & 3): the rows that a read touches lie in different banks.
-template <int AF, int WF, int S>
+// WM x WN waves of 32 AF x 32 WF outputs.  A stage is 128 inputs, 64 bytes a row
+// of each operand and its scales, S stages in LDS; a k-step reads its successor's
+// operands into registers while its MFMAs run, and a stage that has been read makes
+// room for the loads of the one S ahead.  16-byte unit u of a row sits at u ^ (row / 4 & 3):
+// the rows that a read touches lie in different banks.
+template <int AF, int WF, int WM, int WN, int S>
 struct MmShape {
-  static constexpr int BM = 64 * AF, BN = 64 * WF, ROWS = BM + BN;
-  static constexpr int CODES = ROWS * 64, STAGE = CODES + 2048, LDS = S * STAGE;
-  static constexpr int LOADS = ROWS / 64, PER = LOADS + 2;     // of one wave: codes, with the scales
+  static constexpr int W = WM * WN, BM = 32 * AF * WM, BN = 32 * WF * WN, ROWS = BM + BN;
+  // of one wave and stage: loads of 16 rows of codes, loads of the scales of 64 rows
+  static constexpr int LOADS = ROWS / (16 * W), SCALES = (ROWS / 64 + W - 1) / W, PER = LOADS + SCALES;
+  static constexpr int CODES = ROWS * 64, STAGE = CODES + SCALES * W * 256, LDS = S * STAGE;
+  static_assert(ROWS % (16 * W) == 0 && BM % (16 * W) == 0 && BM % 64 == 0);
 };
 
-template <int AF, int WF, int S, int OCC>
-__global__ __launch_bounds__(256, OCC) void mx4_matmul_kernel(Mx4Matmul p, const uint16_t* __restrict__ scales,
-                                                              int stages, int pad_a) {
-  using Sh = MmShape<AF, WF, S>;
-  constexpr int BM = Sh::BM, BN = Sh::BN;
+template <int AF, int WF, int WM, int WN, int S, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void mx4_matmul_kernel(
+    Mx4Matmul p, const uint16_t* __restrict__ scales, int stages, int pad_a) {
+  using Sh = MmShape<AF, WF, WM, WN, S>;
+  constexpr int BM = Sh::BM, BN = Sh::BN, W = Sh::W;
   __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
 #ifdef SWQ_LDS_POISON
   lds_poison(lds, sizeof(lds), kPoisonFloat);
@@ -791,35 +792,36 @@ __global__ __launch_bounds__(256, OCC) void mx4_matmul_kernel(Mx4Matmul p, const
 #endif
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const int ntm = (p.M + BM - 1) / BM, ntn = (p.N + BN - 1) / BN, row_bytes = p.K / 2;
   const int unit = (lane & 3) ^ (lane >> 4);           // (row / 4 & 3) == lane / 16
 
-  // One tile's loads.  Codes: load i of wave w takes rows 16 (4 i + w) + lane / 4 of the two operands put
+  // One tile's loads.  Codes: load i of wave w takes rows 16 (W i + w) + lane / 4 of the two operands put
   // together, a row past the end repeating the tile's first.  Scales: load i of wave w
-  // takes the 128 bytes of row groups 8 i + 2 w and the next (the operands put together).
+  // takes the 128 bytes of row groups 2 (W i + w) and the next (the operands put together).
+  constexpr int OF_A = BM / (16 * W);                  // the loads that are of A
+  // The descriptors cover the whole operands (under 4 GiB each): they stay in scalar
+  // registers whatever the tile.
+  const i32x4 ra = make_srsrc(p.a, (uint32_t)p.M * (uint32_t)row_bytes);
+  const i32x4 rw = make_srsrc(p.w, (uint32_t)p.N * (uint32_t)row_bytes);
+  const i32x4 rs = make_srsrc(scales, (uint32_t)(pad_a + ntn * BN) * (uint32_t)stages * 4u);
   int m0 = 0, n0 = 0;
-  i32x4 ra, rw, rs[2];
-  uint32_t off[Sh::LOADS], soff[2];
+  uint32_t off[Sh::LOADS], soff[Sh::SCALES];
   const auto aim = [&](int block) SWQ_INLINE {
     int tm, tn;
     if (!tile_of(block, ntm, ntn, tm, tn)) return false;
     m0 = tm * BM, n0 = tn * BN;
-    const int rows_a = min(BM, p.M - m0), rows_w = min(BN, p.N - n0);
-    ra = make_srsrc((const char*)p.a + (int64_t)m0 * row_bytes, (uint32_t)rows_a * row_bytes);
-    rw = make_srsrc((const char*)p.w + (int64_t)n0 * row_bytes, (uint32_t)rows_w * row_bytes);
 #pragma unroll
     for (int i = 0; i < Sh::LOADS; ++i) {
-      const int row = 64 * i + wave * 16 + (lane >> 2), of = i < AF ? row : row - BM, n = i < AF ? rows_a : rows_w;
-      off[i] = (uint32_t)(of < n ? of : 0) * row_bytes + unit * 16;
+      const int row = 16 * (W * i + wave) + (lane >> 2);
+      const int at = i < OF_A ? (m0 + row < p.M ? m0 + row : m0) : (n0 + row - BM < p.N ? n0 + row - BM : n0);
+      off[i] = (uint32_t)at * (uint32_t)row_bytes + unit * 16;
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int grp = 8 * i + 2 * wave;
-      const bool of_a = grp < BM / 32;
-      rs[i] = make_srsrc(scales + (int64_t)(of_a ? m0 : pad_a + n0) / 32 * stages * 64,
-                         (uint32_t)(of_a ? BM : BN) / 32 * stages * 128);
-      soff[i] = grp < Sh::ROWS / 32 ? (uint32_t)(grp + h - (of_a ? 0 : BM / 32)) * stages * 128 + r * 4 : 0x80000000u;
+    for (int i = 0; i < Sh::SCALES; ++i) {
+      const int grp = 2 * (W * i + wave) + h;
+      const int at = grp < BM / 32 ? m0 / 32 + grp : (pad_a + n0) / 32 + grp - BM / 32;
+      soff[i] = grp < Sh::ROWS / 32 ? (uint32_t)at * (uint32_t)stages * 128u + r * 4 : kNowhere;
     }
     return true;
   };
@@ -828,11 +830,11 @@ __global__ __launch_bounds__(256, OCC) void mx4_matmul_kernel(Mx4Matmul p, const
   const auto load = [&]<int i>(int t, int slot) SWQ_INLINE {
     const uint32_t base = lds0 + slot * Sh::STAGE;
     if constexpr (i < Sh::LOADS)
-      dma16(i < AF ? ra : rw, __builtin_amdgcn_readfirstlane(base + wave * 1024 + i * 4096),
+      dma16(i < OF_A ? ra : rw, __builtin_amdgcn_readfirstlane(base + (W * i + wave) * 1024),
             t * 128 + unit * 32 < p.K ? off[i] + (uint32_t)t * 64u : kNowhere);
     else
-      dma4(rs[i - Sh::LOADS], __builtin_amdgcn_readfirstlane(base + Sh::CODES + wave * 256 + (i - Sh::LOADS) * 1024),
-           t < stages ? soff[i - Sh::LOADS] + (uint32_t)t * 128u : kNowhere);
+      dma4(rs, __builtin_amdgcn_readfirstlane(base + Sh::CODES + (W * (i - Sh::LOADS) + wave) * 256),
+           t < stages && soff[i - Sh::LOADS] != kNowhere ? soff[i - Sh::LOADS] + (uint32_t)t * 128u : kNowhere);
   };
 
   f32x16 acc[AF][WF];
@@ -847,7 +849,7 @@ __global__ __launch_bounds__(256, OCC) void mx4_matmul_kernel(Mx4Matmul p, const
   const auto read_scale = [&]<int set, int i>(int slot) SWQ_INLINE {
     const char* s = lds + slot * Sh::STAGE + Sh::CODES + lane * 2;
     if constexpr (i < AF) sa[set][i] = *(const uint16_t*)(s + (wm * AF + i) * 128);
-    else sw[set][i - AF] = *(const uint16_t*)(s + (2 * AF + wn * WF + i - AF) * 128);
+    else sw[set][i - AF] = *(const uint16_t*)(s + (BM / 32 + wn * WF + i - AF) * 128);
   };
   const auto meet = [&]() SWQ_INLINE {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -924,7 +926,7 @@ __global__ __launch_bounds__(256, OCC) void mx4_matmul_kernel(Mx4Matmul p, const
     const int mw = m0 + wm * 32 * AF, nw = n0 + wn * 32 * WF;
     if (p.vec != 2) {          // rows out of line: through LDS, one output per lane
       constexpr int NT = 2 * WF;
-      static_assert(4 * flush_floats(NT) * 4 <= Sh::LDS);
+      static_assert(W * flush_floats(NT) * 4 <= Sh::LDS);
       float* buf = (float*)lds + wave * flush_floats(NT);
 #pragma unroll
       for (int i = 0; i < AF; ++i)
@@ -996,8 +998,9 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 
 }  // namespace
 
-// What a product runs on: the few-row kernel up to 24 rows (a grouped product: 48 of an average
-// expert), else the tile shape whose fullest CU is done first.  Measured on one
+// What a product runs on: the few-row kernel up to 24 rows (a grouped product: 10 of an average
+// expert, 20 of binary16 x; 32 experts, K x N = 2048 x 1408, 8 / 16 / 32 rows each: few-row kernel 22 / 28 / 45 us,
+// tiles 28 / 35 / 29), else the tile shape whose fullest CU is done first.  Measured on one
 // MI355X, a CU takes 1.77 us per chunk of a 128 x 256 tile, 0.98 of a 128 x 128 and
 // 0.62 of a 64 x 128 one, however many blocks it holds (bf16 x; us):
 //   rows x K x N          64 x 128   128 x 128   128 x 256
@@ -1014,7 +1017,7 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int mx4_gemm_kind(const MxGemm& p) {
   const int64_t each = p.rows / p.E;
-  if (each <= (p.E > 1 ? 48 : 24) || (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20))) return kFew;
+  if (each <= (p.E == 1 ? 24 : p.xsrc == kXBf16 ? 10 : 20) || (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20))) return kFew;
   const int64_t part = p.E == 1 ? 0 : p.E / 2;           // half a tile per expert for its last, partial one
   const int64_t n = p.w2 ? 2 * (int64_t)p.N : p.N, cus = device_cus();
   const auto cost = [&](int bm, int bn, int us) {
@@ -1029,7 +1032,6 @@ int mx4_gemm_kind(const MxGemm& p) {
 int mx4_gemm_splits(const MxGemm& p) {
   if (p.kind != kSmallTiles || p.tiles || p.w2) return 1;
   const int64_t tiles = ceil_div(p.rows, 64) * ceil_div(p.N, 128), chunks = ceil_div(p.K, 128);
-  if (const char* e = getenv("SWQ_MX4_SPLIT")) return atoi(e);
   int64_t n = std::min<int64_t>(std::min<int64_t>(device_cus() / tiles, chunks / 4), 16);
   if (n < 2) return 1;
   return (int)ceil_div(chunks, ceil_div(chunks, n));     // no empty split
@@ -1169,27 +1171,38 @@ struct MatmulConfig {
   hipError_t (*launch)(const Mx4Matmul&, const uint16_t*, int, int, hipStream_t);
 };
 
-template <int AF, int WF, int S, int OCC>
+template <int AF, int WF, int WM, int WN, int S, int OCC>
 static hipError_t launch_matmul_as(const Mx4Matmul& p, const uint16_t* ws, int stages, int pad_a, hipStream_t st) {
-  using Sh = MmShape<AF, WF, S>;
+  using Sh = MmShape<AF, WF, WM, WN, S>;
   const int64_t tiles = (int64_t)((p.M + Sh::BM - 1) / Sh::BM) * ((p.N + Sh::BN - 1) / Sh::BN);
   if (tiles >= (1LL << 30)) return hipErrorInvalidValue;
   const int64_t blocks = std::min<int64_t>(round_up(tiles, 8), (int64_t)device_cus() / 8 * 8 * OCC);
-  mx4_matmul_kernel<AF, WF, S, OCC><<<dim3((unsigned)blocks), 256, 0, st>>>(p, ws, stages, pad_a);
+  mx4_matmul_kernel<AF, WF, WM, WN, S, OCC>
+      <<<dim3((unsigned)blocks), 64 * WM * WN, 0, st>>>(p, ws, stages, pad_a);
   return hipGetLastError();
 }
 
+// Tile shapes.  Measured (us; 8192 x 2560 x 10240, 2048 x 4096 x 14336, 200 x 2080 x 1001):
+//   256 x 256   149   77   27     eight waves; the others four, and two blocks a CU
+//   128 x 128   197   90   16
+//    64 x  64   299  140    9     seven stages deep
+// (a CU takes about 10 TB/s / 256 from its L2, so the larger tile's fewer bytes count;
+// 128 x 256 took 179, 87 and 23).  The largest shape that gives three fifths of the CUs a tile,
+// the 64 x 64 one below half of them.
 static const MatmulConfig kMatmul[] = {
-    {128, 256, launch_matmul_as<2, 4, 3, 2>},
-    {128, 128, launch_matmul_as<2, 2, 4, 2>},
-    {64, 64, launch_matmul_as<1, 1, 7, 2>},
+    {256, 256, launch_matmul_as<4, 2, 2, 4, 4, 1>},
+    {128, 128, launch_matmul_as<2, 2, 2, 2, 4, 2>},
+    {64, 64, launch_matmul_as<1, 1, 2, 2, 7, 2>},
 };
 
 static const MatmulConfig* matmul_config(const Mx4Matmul& p) {
-  if (const char* e = getenv("SWQ_MX4_MM")) return atoi(e) < 0 ? nullptr : &kMatmul[atoi(e)];
-  if (p.M <= 32) return nullptr;
-  const auto tiles = [&](const MatmulConfig& c) { return round_up(p.M, c.bm) / c.bm * (round_up(p.N, c.bn) / c.bn); };
-  return tiles(kMatmul[0]) >= device_cus() ? &kMatmul[0] : tiles(kMatmul[1]) >= device_cus() / 2 ? &kMatmul[1] : &kMatmul[2];
+  // few rows, or more than the kernels' 32-bit offsets reach
+  if (p.M <= 32 || std::max<int64_t>(p.M, p.N) * (p.K / 2) >= (int64_t(1) << 32) - 16) return nullptr;
+  const auto tiles = [&](const MatmulConfig& c) { return ceil_div(p.M, c.bm) * ceil_div(p.N, c.bn); };
+  const int64_t cus = device_cus();
+  return 5 * tiles(kMatmul[0]) >= 3 * cus   ? &kMatmul[0]
+         : 2 * tiles(kMatmul[1]) >= cus ? &kMatmul[1]
+                                          : &kMatmul[2];
 }
 
 int64_t mx4_matmul_workspace(const Mx4Matmul& p) {

@@ -266,13 +266,13 @@ template <int V>
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part, const int* __restrict__ ids,
                                                       const float* __restrict__ weights,
                                                       const uint16_t* __restrict__ res, int64_t T, int k, int E, int N,
-                                                      int type, int out_type, void* __restrict__ out) {
+                                                      int64_t ld, int type, int out_type, void* __restrict__ out) {
   const int per = N / V;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = i / per;
   const int n = (int)(i - t * per) * V;
   if (t >= T) return;
-  const int64_t at = t * N + n;
+  const int64_t at = t * ld + n;
   float y[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) y[v] = res ? from_16(res[at + v], type) : 0.0f;
@@ -359,13 +359,13 @@ hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {
 }
 
 hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
-                          int k, int E, int N, int type, int out_type, void* out, hipStream_t st) {
-  const bool wide = N % 4 == 0 && (uintptr_t)out % (4 * type_bytes(out_type)) == 0;
+                          int k, int E, int N, int64_t ld, int type, int out_type, void* out, hipStream_t st) {
+  const bool wide = N % 4 == 0 && ld % 4 == 0 && (uintptr_t)out % (4 * type_bytes(out_type)) == 0;
   const int64_t threads = T * (wide ? N / 4 : N);
   if ((threads + 255) / 256 >= (1LL << 31)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((threads + 255) / 256));
-  if (wide) combine_kernel<4><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, type, out_type, out);
-  else combine_kernel<1><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, type, out_type, out);
+  if (wide) combine_kernel<4><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, ld, type, out_type, out);
+  else combine_kernel<1><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, ld, type, out_type, out);
   return hipGetLastError();
 }
 

@@ -259,13 +259,15 @@ def test_most_experts():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("T,E,k,H,I,Ho", [(700, 3, 1, 64, 4096, 40), (700, 3, 1, 2048, 32, 4100), (400, 2, 2, 96, 96, 2052)])
+@pytest.mark.parametrize("T,E,k,H,I,Ho", [(700, 3, 1, 64, 4096, 40), (700, 3, 1, 2048, 32, 4100), (400, 2, 2, 96, 96, 2052),
+                                            (10300, 3, 2, 64, 32, 2056), (20500, 2, 1, 32, 32, 2050)])
 def test_moe_unlike_widths(T, E, k, H, I, Ho, dtype):
-    """Wide and narrow hidden tensors: both products take the tiles of one plan."""
+    """Wide and narrow hidden tensors, where both products take the tiles of one plan, and outputs so large
+    that they are computed and summed some columns at a time."""
     x, ids, weights, ((wg, sg), (wu, su), (wd, sd)) = moe_case(T + I, T, k, E, H, I, Ho, dtype)
     say("moe unlike widths", T, E, k, H, I, Ho, dtype)
     got = swq.moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, out_mode=swq.SWQ_LINEAR_F32)
-    pick = torch.cat([torch.arange(0, T, 37), torch.tensor([T - 1])])
+    pick = torch.cat([torch.arange(0, T, max(37, T // 30)), torch.tensor([T - 1])])
     y, err = ref.experts(ref.to64(x)[pick], ids.cpu().numpy()[pick], ref.to64(weights)[pick],
                          *(ref.values(w, s) for w, s in ((wg, sg), (wu, su), (wd, sd))), None, HIDDEN[dtype])
     ref.close(got[pick.cuda()], y, ref.rounded(y, err, F32), "moe unlike widths")
