@@ -244,12 +244,15 @@ int swiglu_q_mlp(const void *x,
  * formats (MX)" specification's MXFP4.
  *
  * As above: device pointers, contiguous row-major, work enqueued on `stream`,
- * arguments checked on the host before any HIP call, deterministic results, no
- * clearing needed between graph replays.  Codes, x and dequantized output need
- * 16-byte alignment, scales none, everything else its element size.  The
- * grouped linear and the experts' MLP take a workspace of the
- * (device, stream) as described at the top, with the same rules for graphs and
- * concurrent calls; the others take none.
+ * arguments checked on the host before any HIP call, nothing launched on error,
+ * deterministic results, no clearing needed between graph replays.  Codes, x and
+ * dequantized output need 16-byte alignment, scales none, everything else its
+ * element size.  Quantize, dequantize and the router take no workspace; the
+ * products and the experts' MLP take one of the (device, stream) for the shapes that
+ * need it (partial sums of a K split, binary16 rows as two bf16 planes, the scales
+ * of two MXFP4 operands in the matrix instructions' order, the experts' order, hidden
+ * tensor and outputs), with the rules for graphs and concurrent calls given at the
+ * top.
  */
 
 /* Element types (and the out_mode values beyond the affine linear's two). */
@@ -331,7 +334,8 @@ int swiglu_q_route(const void *logits, int64_t T, int64_t E, int k, int type, in
  *   out        [T, Ho] in x's type (out_mode = type) or float32
  * gate, up, silu and their product are float32; the hidden tensor is rounded
  * once (bf16; for binary16 x to 16 significant bits), everything after it is
- * float32 up to the one rounding of out.
+ * float32 up to the one rounding of out.  x below 4 GiB (SWQ_ERR_SHAPE otherwise:
+ * gathered rows are addressed with 32-bit byte offsets).
  */
 int swiglu_q_moe_mlp(const void *x, const int32_t *ids, const float *weights,
                      const uint32_t *Wg, const void *sg, const uint32_t *Wu, const void *su,

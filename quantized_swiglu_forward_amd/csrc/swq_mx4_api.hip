@@ -9,7 +9,9 @@ using namespace swq;
 namespace {
 
 constexpr int kWsSlot = 2;            // the experts' workspace beside the MLP's two
-constexpr int64_t kDirectTokens = 4;  // most tokens whose slots are taken one by one
+// Most tokens whose slots are taken one by one (8 of 64 experts, 2048 x 1024; us, by expert / one by one: 5 tokens 44 / 40, 6 45 / 45,
+// 8 51 / 57, 16 62 / 106).
+constexpr int64_t kDirectTokens = 6;
 // The experts' float32 outputs that wait for their sum: what the 256 MB last-level cache still holds when the
 // sum reads them (4096 tokens, 8 of 64 experts, 2048 columns, 268 MB: in one piece 529 us, in two 515, in three 558).
 constexpr int64_t kPartBytes = int64_t(160) << 20;

@@ -137,6 +137,31 @@ def test_matmul(M, K, N):
         ref.close(got, y, ref.rounded(y, err, out), f"matmul M{M} K{K} N{N} {out}")
 
 
+# (M, K, N) that take the 128 x 128 and the 128 x 256 tiles: aligned rows, rows of 4, odd rows
+@pytest.mark.parametrize("M,K,N", [(513, 160, 5700), (600, 96, 5632), (2047, 288, 4090), (1900, 544, 4096)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_linear_large_tiles(M, K, N, dtype):
+    x, (w, s) = acts(M, M, K, dtype=dtype), matrix(N, N, K)
+    res = acts(N, M, N, dtype=dtype)
+    y, err = ref.dot(ref.to64(x), ref.values(w, s))
+    for out, r in ((dtype, res), (F32, None)):
+        say("linear large", M, K, N, dtype, out)
+        got = swq.mx4_linear(x, w, s, residual=r, out_mode=MODE[out])
+        yy, ee = (y, err) if r is None else (y + ref.to64(r), err + 2.0 ** -23 * (np.abs(y) + np.abs(ref.to64(r))))
+        ref.close(got, yy, ref.rounded(yy, ee, out), f"linear large {out}")
+
+
+# the 128 x 128 and the 256 x 256 tiles of two MXFP4 operands
+@pytest.mark.parametrize("M,K,N", [(1500, 160, 1530), (1500, 1056, 1544), (3100, 288, 3300), (3100, 416, 3336)])
+def test_matmul_large_tiles(M, K, N):
+    (a, sa), (w, s) = matrix(M + 1, M, K, lo=120, hi=134), matrix(K + N, N, K)
+    y, err = ref.dot(ref.values(a, sa), ref.values(w, s))
+    for out in (BF16, F16, F32):
+        say("matmul large", M, K, N, out)
+        got = swq.mx4_matmul(a, sa, w, s, out_mode=MODE[out])
+        ref.close(got, y, ref.rounded(y, err, out), f"matmul large {out}")
+
+
 def test_leading_dimensions_and_empty():
     x, (w, s) = acts(1, 2, 3, 64), matrix(2, 40, 64)
     say("leading dimensions")
