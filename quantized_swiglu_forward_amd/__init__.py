@@ -357,18 +357,23 @@ def mlp(x, wg, sg, bg, wu, su, bu, wd, sd, bd, spec_g, spec_u, spec_d, residual=
 # goes to the current stream of x's GPU unless it is given one.  Small calls
 # cost as much here as on the GPU, so the checks are kept short.
 
-_types = {}      # torch type -> SWQ_TYPE_*
+_types = {}      # torch type -> SWQ_TYPE_*; the rest is set with it
 _dtypes = ()     # SWQ_TYPE_* -> torch type
 _words = ()      # types of codes
-_bytes = None    # type of scales
+_bytes = _int32 = _float32 = None
+_raw_stream = _device_now = _on_device = None   # torch's current stream of a GPU, current GPU, GPU guard
 
 
 def _load_types():
-    global _types, _dtypes, _words, _bytes
+    global _types, _dtypes, _words, _bytes, _int32, _float32, _raw_stream, _device_now, _on_device
     import torch
     _dtypes = (torch.bfloat16, torch.float32, torch.float16)
     _words = (torch.int32, torch.uint32)
-    _bytes = torch.uint8
+    _bytes, _int32, _float32 = torch.uint8, torch.int32, torch.float32
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _on_device = torch.cuda.device
     _types = {t: i for i, t in enumerate(_dtypes)}
     return _types
 
@@ -437,15 +442,14 @@ def _residual(residual, x, shape, what):
 
 def _call(fn, dev, stream, *args):
     """The entry point on the stream (by default the current one) of GPU dev."""
-    import torch
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev == torch._C._cuda_getDevice():
+    if dev == _device_now():
         rc = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with _on_device(dev):
             rc = fn(*args, stream)
     if rc != SWQ_OK:
         raise SwigluQError(rc, fn.__name__)
@@ -454,15 +458,16 @@ def _call(fn, dev, stream, *args):
 def mx4_quantize(x, codes=None, scales=None, stream=None):
     """(codes int32 [..., K/8], scales uint8 [..., K/32]) of x [..., K] (bf16,
     float16 or float32; K a multiple of 32)."""
-    import torch
     t = _type(x, "mx4_quantize")
     shape = x.shape
     if len(shape) < 1 or shape[-1] % 32 or shape[-1] == 0:
         raise ValueError("mx4_quantize: the last dimension must be a positive multiple of 32")
     dev = _same_place("mx4_quantize", x)
     K, n, lead = shape[-1], x.numel(), shape[:-1]
-    codes = _out(codes, lead + (K // 8,), torch.int32, x, "mx4_quantize codes")
-    scales = _out(scales, lead + (K // 32,), torch.uint8, x, "mx4_quantize scales")
+    codes = (x.new_empty(lead + (K // 8,), dtype=_int32) if codes is None
+             else _out(codes, lead + (K // 8,), _int32, x, "mx4_quantize codes"))
+    scales = (x.new_empty(lead + (K // 32,), dtype=_bytes) if scales is None
+              else _out(scales, lead + (K // 32,), _bytes, x, "mx4_quantize scales"))
     if n:
         _call((_lib or lib()).swiglu_q_mx4_quantize, dev, stream, x.data_ptr(), n // K, K, t, codes.data_ptr(),
               scales.data_ptr())
@@ -475,7 +480,8 @@ def mx4_dequantize(codes, scales, dtype=None, out=None, stream=None):
     dtype = _dtypes[0] if dtype is None else dtype
     dev = _same_place("mx4_dequantize", codes, scales)
     K = codes.shape[-1] * 8
-    out = _out(out, lead + (K,), dtype, codes, "mx4_dequantize")
+    shape = lead + (K,)
+    out = codes.new_empty(shape, dtype=dtype) if out is None else _out(out, shape, dtype, codes, "mx4_dequantize")
     t, n = _type(out, "mx4_dequantize"), out.numel()
     if n:
         _call((_lib or lib()).swiglu_q_mx4_dequantize, dev, stream, codes.data_ptr(), scales.data_ptr(), n // K, K, t,
@@ -493,11 +499,11 @@ def mx4_linear(x, w, s, residual=None, out_mode=None, out=None, stream=None):
     shape = x.shape[:-1] + (N,)
     res = _residual(residual, x, shape, "mx4_linear")
     dev = _same_place("mx4_linear", x, w, s, residual)
-    out = _out(out, shape, _dtypes[mode], x, "mx4_linear")
+    out = x.new_empty(shape, dtype=_dtypes[mode]) if out is None else _out(out, shape, _dtypes[mode], x, "mx4_linear")
     n = x.numel()
     if n and N:
-        _call((_lib or lib()).swiglu_q_mx4_linear, dev, stream, x.data_ptr(), w.data_ptr(), s.data_ptr(), res, n // K, K,
-              N, t, mode, out.data_ptr())
+        _call((_lib or lib()).swiglu_q_mx4_linear, dev, stream, x.data_ptr(), w.data_ptr(), s.data_ptr(), res, n // K,
+              K, N, t, mode, out.data_ptr())
     return out
 
 
@@ -510,11 +516,12 @@ def mx4_matmul(a, sa, w, sw, out_mode=SWQ_LINEAR_BF16, out=None, stream=None):
     if out_mode not in (SWQ_LINEAR_BF16, SWQ_LINEAR_F32, SWQ_LINEAR_F16):
         raise ValueError("mx4_matmul: unknown out_mode")
     dev = _same_place("mx4_matmul", a, sa, w, sw)
-    out = _out(out, lead + (N,), _dtypes[out_mode], a, "mx4_matmul")
+    shape, dtype = lead + (N,), _dtypes[out_mode]
+    out = a.new_empty(shape, dtype=dtype) if out is None else _out(out, shape, dtype, a, "mx4_matmul")
     n = a.numel()
     if n and N:
-        _call((_lib or lib()).swiglu_q_mx4_matmul, dev, stream, a.data_ptr(), sa.data_ptr(), w.data_ptr(), sw.data_ptr(),
-              n * 8 // K, K, N, out_mode, out.data_ptr())
+        _call((_lib or lib()).swiglu_q_mx4_matmul, dev, stream, a.data_ptr(), sa.data_ptr(), w.data_ptr(),
+              sw.data_ptr(), n * 8 // K, K, N, out_mode, out.data_ptr())
     return out
 
 
@@ -522,17 +529,17 @@ def mx4_grouped_linear(x, offsets, w, s, out_mode=None, out=None, stream=None):
     """``x[p] W[e]^T`` for rows sorted by expert: x [P, K] bf16 or float16, offsets
     int32 [E + 1] on the device (expert e has rows offsets[e] .. offsets[e+1]),
     W [E, N, K].  Returns ``out`` [P, N]; rows of no expert are zero."""
-    import torch
     t = _type(x, "mx4_grouped_linear", wide=False)
     if x.dim() != 2:
         raise ValueError("mx4_grouped_linear: x must be [rows, K]")
     P, K = x.shape
     E, N = _mx4_shape(w, s, "mx4_grouped_linear", K, dims=3)
-    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,):
+    if offsets.dtype != _int32 or offsets.shape != (E + 1,):
         raise ValueError(f"mx4_grouped_linear: offsets must be int32 [{E + 1}]")
     mode = _out_mode(out_mode, t, "mx4_grouped_linear")
     dev = _same_place("mx4_grouped_linear", x, offsets, w, s)
-    out = _out(out, (P, N), _dtypes[mode], x, "mx4_grouped_linear")
+    dtype = _dtypes[mode]
+    out = x.new_empty((P, N), dtype=dtype) if out is None else _out(out, (P, N), dtype, x, "mx4_grouped_linear")
     if P and N:
         _call((_lib or lib()).swiglu_q_mx4_grouped_linear, dev, stream, x.data_ptr(), offsets.data_ptr(), w.data_ptr(),
               s.data_ptr(), P, E, K, N, t, mode, out.data_ptr())
@@ -543,15 +550,16 @@ def route(logits, k, scoring=SWQ_ROUTE_SOFTMAX, ids=None, weights=None, stream=N
     """(ids int32 [..., k], weights float32 [..., k]): the k largest of each row
     of logits [..., E] and their routing weights (SWQ_ROUTE_*); -1 and 0 where
     fewer than k logits are above -inf."""
-    import torch
     t = _type(logits, "route")
     shape = logits.shape
     if len(shape) < 1:
         raise ValueError("route: logits need at least one dimension")
     dev = _same_place("route", logits)
     E, lead, n = shape[-1], shape[:-1], logits.numel()
-    ids = _out(ids, lead + (k,), torch.int32, logits, "route ids")
-    weights = _out(weights, lead + (k,), torch.float32, logits, "route weights")
+    each = lead + (k,)
+    ids = logits.new_empty(each, dtype=_int32) if ids is None else _out(ids, each, _int32, logits, "route ids")
+    weights = (logits.new_empty(each, dtype=_float32) if weights is None
+               else _out(weights, each, _float32, logits, "route weights"))
     if ids.numel() or n:
         _call((_lib or lib()).swiglu_q_route, dev, stream, logits.data_ptr(), n // max(E, 1), E, k, t, scoring,
               ids.data_ptr(), weights.data_ptr())
@@ -565,7 +573,6 @@ def moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual=None, out_mode=Non
     weights float32 [..., k] (``route``'s output; an id outside the experts is
     skipped).  Returns ``out`` [..., Ho] in x's type, or float32 with
     SWQ_LINEAR_F32."""
-    import torch
     t = _type(x, "moe_mlp", wide=False)
     H, lead = x.shape[-1], x.shape[:-1]
     E, I = _mx4_shape(wg, sg, "moe_mlp gate", H, dims=3)
@@ -574,14 +581,14 @@ def moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual=None, out_mode=Non
     Ed, Ho = _mx4_shape(wd, sd, "moe_mlp down", I, dims=3)
     if Ed != E:
         raise ValueError(f"moe_mlp: {E} experts in the gate, {Ed} in the down projection")
-    if ids.dtype != torch.int32 or weights.dtype != torch.float32 or ids.shape != weights.shape \
+    if ids.dtype != _int32 or weights.dtype != _float32 or ids.shape != weights.shape \
             or ids.dim() < 1 or ids.shape[:-1] != lead:
         raise ValueError(f"moe_mlp: ids must be int32 and weights float32 of shape {tuple(lead) + ('k',)}")
     mode = _out_mode(out_mode, t, "moe_mlp")
     shape = lead + (Ho,)
     res = _residual(residual, x, shape, "moe_mlp")
     dev = _same_place("moe_mlp", x, ids, weights, wg, sg, wu, su, wd, sd, residual)
-    out = _out(out, shape, _dtypes[mode], x, "moe_mlp")
+    out = x.new_empty(shape, dtype=_dtypes[mode]) if out is None else _out(out, shape, _dtypes[mode], x, "moe_mlp")
     n = x.numel()
     if n and Ho:
         _call((_lib or lib()).swiglu_q_moe_mlp, dev, stream, x.data_ptr(), ids.data_ptr(), weights.data_ptr(),

@@ -20,6 +20,9 @@ enum : int { kXBf16 = 0, kXF16 = 1, kXPlanes = 2 };
 // Kernels of a product with MXFP4 weights.
 enum : int { kFew, kSmallTiles, kMidTiles, kLargeTiles };
 
+// Most experts whose offsets the products read themselves (one per lane of a wave).
+constexpr int kOffsetExperts = 64;
+
 // One tile of rows of a grouped product.
 struct RowTile {
   int expert;   // -1: rows of no expert, written as zeros
@@ -52,6 +55,7 @@ struct MxGemm {
   int hidden_planes;        // 1: write the hidden tensor as two bf16 planes
   const RowTile* tiles;     // tile table, or null
   const int* ntiles;
+  const int* offsets;       // without tiles: [E + 1] the experts' first rows, E <= 64, or null
   const int* perm;          // slot -> row of out, or null (the same)
   int max_tiles;
   int kind;                 // kFew .. kLargeTiles (mx4_gemm_kind)

@@ -215,12 +215,18 @@ int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uin
   g.vec = vec_ok(N, out, nullptr, out_mode);
   g.kind = mx4_gemm_kind(g);
   const int tile = mx4_gemm_tile(g);
-  const PlanLayout l = plan_layout(P, E, tile, false);
+  const bool planned = E > kOffsetExperts;
+  const PlanLayout l = planned ? plan_layout(P, E, tile, false) : PlanLayout{0, 0, 0};
   void* ws = nullptr;
-  rc = stream_workspace(stream, (size_t)(l.total + planes_bytes(g, P)), &ws, kWsSlot);
+  if (const int64_t need = l.total + planes_bytes(g, P)) rc = stream_workspace(stream, (size_t)need, &ws, kWsSlot);
   if (rc != SWQ_OK) return rc;
   (void)hipGetLastError();
-  rc = run_plan(g, (char*)ws, l, nullptr, offsets, tile, stream);
+  if (planned) {
+    rc = run_plan(g, (char*)ws, l, nullptr, offsets, tile, stream);
+  } else {
+    g.offsets = offsets;
+    g.max_tiles = (int)max_row_tiles(P, E, tile);
+  }
   if (rc == SWQ_OK) rc = to_planes(g, P, (char*)ws + l.total, stream);
   if (rc != SWQ_OK) return rc;
   return check_status(launch_mx4_gemm(g, stream));

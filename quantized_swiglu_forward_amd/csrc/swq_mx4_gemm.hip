@@ -68,6 +68,49 @@ __device__ __forceinline__ bool tile_of(int b, int ntm, int ntn, int& tm, int& t
   return true;
 }
 
+// The tiles of a product grouped by at most 64 experts, found by every wave on its own from
+// the offsets: lane e holds expert e's rows (offsets made non-decreasing and cut at
+// the rows) and the tiles up to its last.  The tiles of the rows before the first and after the last
+// group, of no expert, follow.  (A plan kernel of its own would cost a launch, 4 to 5 us.)
+struct OffsetTiles {
+  int start, end, upto, experts;
+  int before, after;           // rows of no expert: [0, before), [after, rows)
+  int total;
+};
+__device__ __forceinline__ OffsetTiles scan_offsets(const MxGemm& p, int tile) {
+  const int lane = threadIdx.x & 63;
+  OffsetTiles s;
+  s.start = lane < p.E ? min(max(p.offsets[lane], 0), p.rows) : 0;
+  s.end = lane < p.E ? min(max(p.offsets[lane + 1], 0), p.rows) : 0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s.start = max(s.start, __shfl_up(s.start, d));   // (lanes below d: their own)
+  s.end = lane < p.E ? max(s.end, s.start) : s.start;
+  s.upto = lane < p.E ? (s.end - s.start + tile - 1) / tile : 0;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s.upto, d);
+    s.upto += lane >= d ? o : 0;
+  }
+  s.experts = __builtin_amdgcn_readlane(s.upto, 63);
+  s.before = __builtin_amdgcn_readlane(s.start, 0);
+  s.after = __builtin_amdgcn_readlane(s.end, p.E - 1);
+  s.total = s.experts + (s.before + tile - 1) / tile + (p.rows - s.after + tile - 1) / tile;
+  return s;
+}
+__device__ __forceinline__ RowTile offset_tile(const OffsetTiles& s, int rows, int tile, int tm) {
+  if (tm < s.experts) {
+    const int e = __builtin_ctzll(__ballot(s.upto > tm));
+    const int start = __builtin_amdgcn_readlane(s.start, e), end = __builtin_amdgcn_readlane(s.end, e);
+    const int own = (end - start + tile - 1) / tile, in = tm - (__builtin_amdgcn_readlane(s.upto, e) - own);
+    return RowTile{e, start + in * tile, min(tile, end - start - in * tile), 0};
+  }
+  tm -= s.experts;
+  const int before = (s.before + tile - 1) / tile;
+  if (tm < before) return RowTile{-1, tm * tile, min(tile, s.before - tm * tile), 0};
+  const int first = s.after + (tm - before) * tile;
+  return RowTile{-1, first, min(tile, rows - first), 0};
+}
+
 // Sixteen rows of NT column tiles from a wave's accumulators (v[j]: lane 16 h + r has
 // columns 16 j + 4 h .. + 3 of row r) to memory, through the wave's own stretch
 // of LDS, so that a row leaves as whole lines: 16-byte stores of eight outputs (float32: two
@@ -317,7 +360,12 @@ __global__ __launch_bounds__(64 * W, 2) void mx4_few_kernel(MxGemm p) {
   int tm = blockIdx.x / ntn;
   const int tn = blockIdx.x - tm * ntn;
   int expert = 0, first = tm * 16 * RT, rows = min(16 * RT, p.rows - first);
-  if (p.tiles) {
+  if (p.offsets) {
+    const OffsetTiles s = scan_offsets(p, 16 * RT);
+    if (tm >= s.total) return;
+    const RowTile t = offset_tile(s, p.rows, 16 * RT, tm);
+    expert = t.expert, first = t.first, rows = t.rows;
+  } else if (p.tiles) {
     if (tm >= *p.ntiles) return;
     const RowTile t = p.tiles[tm];
     expert = t.expert, first = t.first, rows = t.rows;
@@ -517,12 +565,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   const int wm = wave / WN, wn = wave % WN;
 
   const int ntn = (p.N + BNO - 1) / BNO;
-  int tm, tn;
-  if (!tile_of(blockIdx.x, p.tiles ? *p.ntiles : (p.rows + BM - 1) / BM, ntn, tm, tn)) return;
+  int tm, tn, ntm = (p.rows + BM - 1) / BM;
+  OffsetTiles ot;
+  if (p.offsets) {
+    ot = scan_offsets(p, BM);
+    ntm = ot.total;
+  } else if (p.tiles) {
+    ntm = *p.ntiles;
+  }
+  if (!tile_of(blockIdx.x, ntm, ntn, tm, tn)) return;
   const int split = SPLIT ? blockIdx.y : 0;     // of K: its share of the chunks, its part of the partial sums
   int expert = 0, first = tm * BM, rows = min(BM, p.rows - first);
-  if (p.tiles) {
-    const RowTile t = p.tiles[tm];
+  if (p.offsets || p.tiles) {
+    const RowTile t = p.offsets ? offset_tile(ot, p.rows, BM, tm) : p.tiles[tm];
     expert = __builtin_amdgcn_readfirstlane(t.expert);
     first = __builtin_amdgcn_readfirstlane(t.first);
     rows = __builtin_amdgcn_readfirstlane(t.rows);
@@ -1030,7 +1085,7 @@ int mx4_gemm_kind(const MxGemm& p) {
 
 // K split of 64 x 128 tiles that leave half the CUs without one: at least four chunks each, at most 16 ways.
 int mx4_gemm_splits(const MxGemm& p) {
-  if (p.kind != kSmallTiles || p.tiles || p.w2) return 1;
+  if (p.kind != kSmallTiles || p.tiles || p.offsets || p.w2) return 1;
   const int64_t tiles = ceil_div(p.rows, 64) * ceil_div(p.N, 128), chunks = ceil_div(p.K, 128);
   int64_t n = std::min<int64_t>(std::min<int64_t>(device_cus() / tiles, chunks / 4), 16);
   if (n < 2) return 1;
@@ -1053,7 +1108,7 @@ bool mx4_gemm_takes_planes(const MxGemm& p) { return p.kind != kFew; }
 template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED>
 static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
   constexpr int BM = 16 * MF * WM, BNO = 16 * NF * WN / (FUSED ? 2 : 1);
-  const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + BM - 1) / BM, ntn = (p.N + BNO - 1) / BNO;
+  const int64_t ntm = p.tiles || p.offsets ? p.max_tiles : (p.rows + BM - 1) / BM, ntn = (p.N + BNO - 1) / BNO;
   const int64_t blocks = (ntm * ntn + 7) / 8 * 8;
   if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
   if constexpr (!FUSED && MF == 4 && NF == 2) {
@@ -1079,7 +1134,7 @@ static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
 template <int RT, int CT, int XS, bool FUSED, int W, int U>
 static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
   const int64_t ntn = (p.N + 16 * CT - 1) / (16 * CT);
-  const int64_t ntm = p.tiles ? p.max_tiles : (p.rows + 16 * RT - 1) / (16 * RT);
+  const int64_t ntm = p.tiles || p.offsets ? p.max_tiles : (p.rows + 16 * RT - 1) / (16 * RT);
   if (ntm * ntn >= (1LL << 31)) return hipErrorInvalidValue;
   mx4_few_kernel<RT, CT, XS, FUSED, W, U><<<dim3((unsigned)(ntm * ntn)), 64 * W, 0, st>>>(p);
   return hipGetLastError();
@@ -1090,7 +1145,7 @@ static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
 template <int RT, int XS, bool FUSED>
 static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
   constexpr int D = FUSED ? 2 : 1;
-  const int64_t tiles = p.tiles ? std::min<int64_t>(p.max_tiles, p.rows) : (p.rows + 16 * RT - 1) / (16 * RT);
+  const int64_t tiles = p.tiles || p.offsets ? std::min<int64_t>(p.max_tiles, p.rows) : (p.rows + 16 * RT - 1) / (16 * RT);
   const int64_t need = device_cus() * 7 / 8;
   if (p.N / (16 * 4 / D) * tiles >= need) return launch_few_as<RT, 4 / D, XS, FUSED, 8, 1>(p, st);
   if (p.N / (16 * 2 / D) * tiles >= need || FUSED) return launch_few_as<RT, 2 / D, XS, FUSED, 8, RT == 1 ? 2 : 1>(p, st);
@@ -1108,7 +1163,7 @@ static hipError_t launch_row(const MxGemm& p, hipStream_t st) {
 
 template <int XS, bool FUSED>
 static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
-  if (!p.tiles && (p.ids || p.rows == 1))      // rows one by one; four waves cover 2048 inputs at once
+  if (!p.tiles && !p.offsets && (p.ids || p.rows == 1))      // rows one by one; four waves cover 2048 inputs at once
     return p.K <= 4 * kRowU * 128 ? launch_row<XS, FUSED, 4>(p, st) : launch_row<XS, FUSED, 8>(p, st);
   const int rt = few_tiles(p);
   return rt == 1 ? launch_few_rt<1, XS, FUSED>(p, st) : rt == 2 ? launch_few_rt<2, XS, FUSED>(p, st)
