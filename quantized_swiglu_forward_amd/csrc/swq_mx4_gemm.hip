@@ -1003,7 +1003,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void mx4_matmul_ke
   }
 }
 
-// Few rows of x: 16 x 16 outputs per block, everything straight to registers; the W
+// Few outputs: 16 x 16 per block, everything straight to registers; the W
 // waves take steps of 128 inputs in turn, U of them in flight, and add their
 // sums in wave order.  (16 x 16 x 128 MFMA: lane 16 h + r holds row r's block h.)
 template <int W, int U>
@@ -1237,13 +1237,14 @@ static hipError_t launch_matmul_as(const Mx4Matmul& p, const uint16_t* ws, int s
   return hipGetLastError();
 }
 
-// Tile shapes.  Measured (us; 8192 x 2560 x 10240, 2048 x 4096 x 14336, 200 x 2080 x 1001):
+// Tile shapes.  Measured (us; 8192 x 2560 x 10240, 2048 x 4096 x 14336, 200 x 2080 x 1001
+// with its scale layout):
 //   256 x 256   149   77   27     eight waves; the others four, and two blocks a CU
 //   128 x 128   197   90   16
-//    64 x  64   299  140    9     seven stages deep
+//    64 x  64   299  140    8.9   seven stages deep
 // (a CU takes about 10 TB/s / 256 from its L2, so the larger tile's fewer bytes count;
-// 128 x 256 took 179, 87 and 23).  The largest shape that gives three fifths of the CUs a tile,
-// the 64 x 64 one below half of them.
+// 128 x 256 took 179, 87 and 23).  256 x 256 where it gives three fifths of the CUs a tile, 128 x 128
+// where it gives half of them one, else 64 x 64.
 static const MatmulConfig kMatmul[] = {
     {256, 256, launch_matmul_as<4, 2, 2, 4, 4, 1>},
     {128, 128, launch_matmul_as<2, 2, 2, 2, 4, 2>},
@@ -1251,10 +1252,17 @@ static const MatmulConfig kMatmul[] = {
 };
 
 static const MatmulConfig* matmul_config(const Mx4Matmul& p) {
-  // few rows, or more than the kernels' 32-bit offsets reach
-  if (p.M <= 32 || std::max<int64_t>(p.M, p.N) * (p.K / 2) >= (int64_t(1) << 32) - 16) return nullptr;
+  // operands past the kernels' 32-bit offsets
+  if (std::max<int64_t>(p.M, p.N) * (p.K / 2) >= (int64_t(1) << 32) - 16) return nullptr;
   const auto tiles = [&](const MatmulConfig& c) { return ceil_div(p.M, c.bm) * ceil_div(p.N, c.bn); };
   const int64_t cus = device_cus();
+  // Up to two 16 x 16 tiles a CU, or four with little K: no scale layout, no LDS, one launch.
+  // Against the 64 x 64 tiles with their scale layout (us; tiles, M x K x N):
+  //   256  33 x 4096 x 1001    5.7 against 10.5      1024  64 x 1024 x 4096    6.3 against  6.5
+  //   512  24 x 8192 x 4096   14.8 against 15.5       819  200 x 2080 x 1001   5.9 against  8.9
+  //   896  16 x 4096 x 14336  16.2 against 14.1      1024  32 x 4096 x 8192   16.1 against 11.4
+  const int64_t small = ceil_div(p.M, 16) * ceil_div(p.N, 16);
+  if (small <= 2 * cus || (small <= 4 * cus && (int64_t)p.M * p.N * p.K <= (int64_t(1) << 29))) return nullptr;
   return 5 * tiles(kMatmul[0]) >= 3 * cus   ? &kMatmul[0]
          : 2 * tiles(kMatmul[1]) >= cus ? &kMatmul[1]
                                           : &kMatmul[2];

@@ -162,6 +162,17 @@ def test_matmul_large_tiles(M, K, N):
         ref.close(got, y, ref.rounded(y, err, out), f"matmul large {out}")
 
 
+# their 64 x 64 tiles: more 16 x 16 tiles than the kernel for few outputs takes
+@pytest.mark.parametrize("M,K,N", [(500, 160, 1030), (531, 1056, 1000), (20, 416, 9004), (300, 2080, 1001)])
+def test_matmul_small_tiles(M, K, N):
+    (a, sa), (w, s) = matrix(M + 1, M, K, lo=120, hi=134), matrix(K + N, N, K)
+    y, err = ref.dot(ref.values(a, sa), ref.values(w, s))
+    for out in (BF16, F16, F32):
+        say("matmul small tiles", M, K, N, out)
+        got = swq.mx4_matmul(a, sa, w, s, out_mode=MODE[out])
+        ref.close(got, y, ref.rounded(y, err, out), f"matmul small tiles {out}")
+
+
 def test_leading_dimensions_and_empty():
     x, (w, s) = acts(1, 2, 3, 64), matrix(2, 40, 64)
     say("leading dimensions")

@@ -44,7 +44,7 @@ def test_linear(poison, M, K, N, dtype):
     both(poison, lambda: swq.mx4_linear(x, w, s))
 
 
-@pytest.mark.parametrize("M,K,N", [(3, 1056, 70), (40, 160, 300), (1500, 160, 1530), (3100, 288, 3336)])
+@pytest.mark.parametrize("M,K,N", [(3, 1056, 70), (40, 160, 300), (500, 544, 1030), (1500, 160, 1530), (3100, 288, 3336)])
 def test_matmul(poison, M, K, N):
     (a, sa), (w, s) = matrix(M, M, K), matrix(N, N, K)
     say("poison mx4 matmul", M, K, N)
