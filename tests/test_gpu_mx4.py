@@ -382,7 +382,7 @@ def moe_case(seed, T, k, E, H, I, Ho, dtype, spread=True):
 
 MOE = [(1, 2, 4, 64, 32, 64), (1, 8, 16, 2048, 96, 130), (3, 1, 2, 96, 64, 33), (5, 4, 8, 160, 224, 96),
        (20, 6, 6, 128, 352, 257), (40, 8, 60, 256, 160, 128), (130, 2, 3, 512, 96, 200), (300, 3, 5, 96, 288, 64),
-       (70, 1, 1, 64, 64, 64)]
+       (70, 1, 1, 64, 64, 64), (1500, 3, 5, 64, 32, 64), (1100, 4, 37, 64, 96, 40)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
