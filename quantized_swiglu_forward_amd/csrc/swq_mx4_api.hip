@@ -9,11 +9,13 @@ using namespace swq;
 namespace {
 
 constexpr int kWsSlot = 2;            // the experts' workspace beside the MLP's two
-// Most tokens whose slots are taken one by one (8 of 64 experts, 2048 x 1024; us, by expert / one by one: 5 tokens 44 / 40, 6 45 / 45,
-// 8 51 / 57, 16 62 / 106).
+// Most tokens whose slots are taken one by one (8 of 64 experts, 2048 x 1024; us, by expert /
+// one by one: 5 tokens 44 / 40, 6 45 / 45, 8 51 / 57, 16 62 / 106).
 constexpr int64_t kDirectTokens = 6;
-// The experts' float32 outputs that wait for their sum: what the 256 MB last-level cache still holds when the
-// sum reads them (4096 tokens, 8 of 64 experts, 2048 columns, 268 MB: in one piece 529 us, in two 515, in three 558).
+// The experts' float32 outputs that wait for their sum: what the 256 MB last-level cache still
+// holds when the sum reads them (4096 tokens, 8 of 64 experts, 2048 columns, 268 MB: in one
+// piece 529 us, in two 515, in three 558).  Equal pieces: 1280 and 768 columns, the least rounds of tiles
+// over the CUs, took 528 where two of 1024 took 530.
 constexpr int64_t kPartBytes = int64_t(160) << 20;
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 20;
 
@@ -236,7 +238,8 @@ int swiglu_q_route(const void* logits, int64_t T, int64_t E, int k, int type, in
                    float* weights, void* stream) {
   if (!logits || !ids || !weights) return SWQ_ERR_NULL;
   if (!type_ok(type) || scoring < SWQ_ROUTE_SOFTMAX || scoring > SWQ_ROUTE_SIGMOID_CHOSEN) return SWQ_ERR_UNSUPPORTED;
-  if (T < 0 || T > kMaxRows || E < 1 || E > SWQ_MAX_EXPERTS || k < 1 || k > SWQ_MAX_CHOSEN || k > E) return SWQ_ERR_SHAPE;
+  if (T < 0 || T > kMaxRows || E < 1 || E > SWQ_MAX_EXPERTS || k < 1 || k > SWQ_MAX_CHOSEN || k > E)
+    return SWQ_ERR_SHAPE;
   if (!aligned(logits, type_bytes(type)) || !aligned(ids, 4) || !aligned(weights, 4)) return SWQ_ERR_ALIGN;
   if (T == 0) return SWQ_OK;
   (void)hipGetLastError();
@@ -342,8 +345,8 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
     d.vec = vec_ok(d.N, d.out, nullptr, SWQ_TYPE_F32);
     rc = check_status(launch_mx4_gemm(d, stream));
     if (rc != SWQ_OK) return rc;
-    rc = check_status(launch_combine((const float*)(ws + part), ids, weights,
-                                     residual ? (const uint16_t*)residual + n : nullptr, T, (int)k, (int)E, d.N, Ho, type,
+    const uint16_t* res = residual ? (const uint16_t*)residual + n : nullptr;
+    rc = check_status(launch_combine((const float*)(ws + part), ids, weights, res, T, (int)k, (int)E, d.N, Ho, type,
                                      out_mode, (char*)out + n * type_bytes(out_mode), stream));
     if (rc != SWQ_OK) return rc;
   }

@@ -70,8 +70,9 @@ __device__ __forceinline__ bool tile_of(int b, int ntm, int ntn, int& tm, int& t
 
 // The tiles of a product grouped by at most 64 experts, found by every wave on its own from
 // the offsets: lane e holds expert e's rows (offsets made non-decreasing and cut at
-// the rows) and the tiles up to its last.  The tiles of the rows before the first and after the last
-// group, of no expert, follow.  (A plan kernel of its own would cost a launch, 4 to 5 us.)
+// the rows) and the tiles up to its last.  The tiles of the rows before the first and
+// after the last group, of no expert, follow.  Against a plan kernel before the product (us a call):
+// 70 rows of 32 experts, 1504 x 2049, 14.1 against 16.4; 6007 rows, 2048 x 1408, 50.3 against 53.5.
 struct OffsetTiles {
   int start, end, upto, experts;
   int before, after;           // rows of no expert: [0, before), [after, rows)
@@ -225,6 +226,12 @@ __device__ __forceinline__ void finish4(const MxGemm& p, int64_t at, int col, f3
 // 128 inputs c = wave, wave + W, ... on its own, weights and x straight to
 // registers, U chunks of loads in flight, and the waves' sums meet in LDS at the
 // end.  No barrier stands between the loads.
+//
+// Measured: 70 float16 rows of 32 experts, 1504 x 2049 (53 MB): 10.4 us with the weights in the last-level
+// cache (5.1 TB/s), 15.6 from memory.  16 tokens, 8 of 64 experts: gate and up 2048 x 1024 37 us (123 MB,
+// 3.3 TB/s), down 22; at 2080 x 1056 28 and 17: rows a power of two of bytes apart fall on
+// few channels of the L2.  16 x 5632 x 2048: 9.9 us, the chain of load, MFMA and join.
+
 // Row tiles whose partial sums meet in LDS at once, and the f32x4 of LDS that this takes.
 constexpr int few_pass(int rt, int nw, int w) {
   int rp = rt;
@@ -380,13 +387,18 @@ __global__ __launch_bounds__(64 * W, 2) void mx4_few_kernel(MxGemm p) {
 //
 // One row of x: the weights' bytes are all there is.  A wave takes U chunks at once; its
 // part of x is one load of 16 bytes per lane, put into the wave's own stretch of
-// LDS and read back by every column of the operand (all 16 rows of the MFMA's second operand hold the
-// same row; row 0's result counts).
+// LDS and read back by every column of the operand (all 16 rows of the MFMA's second
+// operand hold the same row; row 0's result counts).  A lane's four loads of codes are neighbours, so
+// a wave takes whole lines of the weights.
+//
+// Bound by latency (the launch, x, the weights, the join) where a CU has one block: 2048 x 5632
+// 5.0 us (6.1 MB).  One token, 8 of 64 experts, 2048 x 1024: gate and up 9.0 us (17.8 MB, 2.0 TB/s),
+// down with the weighted sum 7.4.
 
 constexpr int kRowU = 4, kRowStretch = kRowU * 16;       // chunks in flight; u32x4 of LDS per wave and plane
 
-// Sums of a wave over the chunks 4 i .. 4 i + 3, i = first, first + step, ..., for the 16 columns of each of NW matrices
-// (four neighbours: 256 bytes of each row).
+// Sums of a wave over the chunks 4 i .. 4 i + 3, i = first, first + step, ..., for the 16 columns
+// of each of NW matrices (four neighbours: 256 bytes of each row).
 template <int XS, int NW>
 __device__ __forceinline__ void row_sums(const __amdgpu_buffer_rsrc_t (&wr)[NW], const __amdgpu_buffer_rsrc_t (&sr)[NW],
                                          const uint16_t* x, int64_t plane, int K, int first, int step, u32x4* own,
@@ -546,10 +558,19 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
 // 16 NF columns of W (SwiGLU: NF / 2 column tiles of the gate and the same of the
 // up matrix).  A chunk is 128 inputs: lane 16 h + r takes block h of a chunk
 // in four steps, so its codes are one 16-byte load and its scale one byte,
-// straight from memory to registers one chunk ahead (a column's codes are used
-// by WM waves only).  x goes through LDS, [BM * NP][128] bf16, two buffers, by
-// loads that write LDS; 16-byte unit u of a row sits at u ^ (row & 15), so the
-// sixteen rows that a read touches lie in different banks.
+// straight from memory to registers S - 1 chunks ahead (a column's codes are used
+// by WM waves only).  x goes through LDS, [BM * NP][128] bf16, S buffers, by
+// loads that write LDS; 16-byte unit u of a row sits at u ^ (row & 15), which keeps the
+// 64-byte pieces that four lanes load whole.  (Two rows of a read still meet in a bank, 4 cycles a read.
+// A placement without that, in whole pieces, took the same time; one that breaks the pieces
+// 294 us where this takes 225: the loads, not the reads, count.)
+//
+// Measured: 2048 x 4096 x 14336 225 us, 1.07 PFLOP/s (the library's bf16 product of that shape 205);
+// matrix units 54 % busy at the 1.9 GHz that the card's power leaves.  8192 x 2560 x 10240 379 us,
+// 1.13 PFLOP/s.  32768 rows of 64 experts: gate and up 2048 x 1024 303 us, 0.91 PFLOP/s, down 2 x 99 us, 0.70: a ninth
+// of the tiles' rows is past the experts' ends, the last round of tiles leaves CUs idle, and the
+// down projection's short K ends in 128 KB of float32 per tile.  Float16 x, two operands: 2048 x
+// 4096 x 14336 463 us, 1.04 PFLOP/s of bf16 products.
 template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   constexpr int W = WM * WN, BM = 16 * MF * WM, ROWS = BM * NP, BN = 16 * NF * WN, BNO = FUSED ? BN / 2 : BN;
@@ -713,7 +734,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   }
 }
 
-// The sums of a K split: four neighbouring outputs per thread.
+// The sums of a K split, added in the order of the splits: four neighbouring outputs per thread.
+// 256 x 5632 x 2048: 4 us after the 16 of the split tiles, a launch and a load's latency.
 __global__ __launch_bounds__(256) void mx4_join_kernel(MxGemm p) {
   const int per = (p.N + 3) / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / per;
@@ -745,7 +767,7 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(MxGemm p) {
 // The scales' bytes lie K / 32 apart, at any address, and a stage of 128
 // inputs needs four per row.  A first kernel lays them out as the MFMA takes
 // them: for 32 rows and a stage, two bytes per lane, byte e for k-step e
-// (blocks past K: 0).
+// (blocks past K: 0).  8192 + 10240 rows of 80: 5 us, 1.5 MB in and out, latency.
 __global__ __launch_bounds__(256) void mx4_scale_kernel(const uint8_t* __restrict__ sa, int M,
                                                         const uint8_t* __restrict__ sw, int N, int kb, int stages,
                                                         int pad_a, int pad_w, uint16_t* __restrict__ out) {
@@ -799,7 +821,8 @@ __device__ __forceinline__ void store_wide(const Mx4Matmul& p, const f32x16 (&ac
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = nw + 32 * j + 8 * e + 4 * h;
-          if (col < p.N) *(f32x4*)((float*)p.out + at + col) = (f32x4){v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+          if (col < p.N)
+            *(f32x4*)((float*)p.out + at + col) = (f32x4){v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
         }
       } else {
 #pragma unroll
@@ -825,7 +848,12 @@ __device__ __forceinline__ void store_wide(const Mx4Matmul& p, const f32x16 (&ac
 // of each operand and its scales, S stages in LDS; a k-step reads its successor's
 // operands into registers while its MFMAs run, and a stage that has been read makes
 // room for the loads of the one S ahead.  16-byte unit u of a row sits at u ^ (row / 4 & 3):
-// the rows that a read touches lie in different banks.
+// the rows that a read touches lie in different banks (no conflict cycles counted).  As many blocks as
+// the CUs hold take the tiles in turn, and a block's next loads go out before its stores.
+//
+// 8192 x 2560 x 10240: 131 us, 3.3 PFLOP/s, 168 MB of outputs; matrix units 44 % busy.  The 20
+// stages of a tile are bound by what a CU takes from its L2 (32 KB a stage), and the outputs,
+// 32 us of the memory's time, overlap only in part.
 template <int AF, int WF, int WM, int WN, int S>
 struct MmShape {
   static constexpr int W = WM * WN, BM = 32 * AF * WM, BN = 32 * WF * WN, ROWS = BM + BN;
@@ -1006,6 +1034,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void mx4_matmul_ke
 // Few outputs: 16 x 16 per block, everything straight to registers; the W
 // waves take steps of 128 inputs in turn, U of them in flight, and add their
 // sums in wave order.  (16 x 16 x 128 MFMA: lane 16 h + r holds row r's block h.)
+// 200 x 2080 x 1001: 6.6 us; 33 x 1024 x 1001 3.3, two loads' latency and the launch.
 template <int W, int U>
 __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
   __shared__ f32x4 lds[W * 64];
@@ -1054,9 +1083,9 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 }  // namespace
 
 // What a product runs on: the few-row kernel up to 24 rows (a grouped product: 10 of an average
-// expert, 20 of binary16 x; 32 experts, K x N = 2048 x 1408, 8 / 16 / 32 rows each: few-row kernel 22 / 28 / 45 us,
-// tiles 28 / 35 / 29), else the tile shape whose fullest CU is done first.  Measured on one
-// MI355X, a CU takes 1.77 us per chunk of a 128 x 256 tile, 0.98 of a 128 x 128 and
+// expert, 20 of binary16 x; 32 experts, K x N = 2048 x 1408, 8 / 16 / 32 rows each:
+// few-row kernel 22 / 28 / 45 us, tiles 28 / 35 / 29), else the tile shape whose fullest
+// CU is done first.  Measured on one MI355X, a CU takes 1.77 us per chunk of a 128 x 256 tile, 0.98 of a 128 x 128 and
 // 0.62 of a 64 x 128 one, however many blocks it holds (bf16 x; us):
 //   rows x K x N          64 x 128   128 x 128   128 x 256
 //   1024 x 5632 x 2048        34         48          82
@@ -1072,7 +1101,8 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int mx4_gemm_kind(const MxGemm& p) {
   const int64_t each = p.rows / p.E;
-  if (each <= (p.E == 1 ? 24 : p.xsrc == kXBf16 ? 10 : 20) || (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20))) return kFew;
+  if (each <= (p.E == 1 ? 24 : p.xsrc == kXBf16 ? 10 : 20)) return kFew;
+  if (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20)) return kFew;
   const int64_t part = p.E == 1 ? 0 : p.E / 2;           // half a tile per expert for its last, partial one
   const int64_t n = p.w2 ? 2 * (int64_t)p.N : p.N, cus = device_cus();
   const auto cost = [&](int bm, int bn, int us) {
@@ -1145,10 +1175,11 @@ static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
 template <int RT, int XS, bool FUSED>
 static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
   constexpr int D = FUSED ? 2 : 1;
-  const int64_t tiles = p.tiles || p.offsets ? std::min<int64_t>(p.max_tiles, p.rows) : (p.rows + 16 * RT - 1) / (16 * RT);
+  const int64_t tiles = p.tiles || p.offsets ? std::min<int64_t>(p.max_tiles, p.rows) : ceil_div(p.rows, 16 * RT);
   const int64_t need = device_cus() * 7 / 8;
   if (p.N / (16 * 4 / D) * tiles >= need) return launch_few_as<RT, 4 / D, XS, FUSED, 8, 1>(p, st);
-  if (p.N / (16 * 2 / D) * tiles >= need || FUSED) return launch_few_as<RT, 2 / D, XS, FUSED, 8, RT == 1 ? 2 : 1>(p, st);
+  if (p.N / (16 * 2 / D) * tiles >= need || FUSED)
+    return launch_few_as<RT, 2 / D, XS, FUSED, 8, RT == 1 ? 2 : 1>(p, st);
   if constexpr (!FUSED) return launch_few_as<RT, 1, XS, FUSED, 8, RT <= 2 ? 2 : 1>(p, st);
   return hipErrorInvalidValue;
 }
@@ -1178,7 +1209,8 @@ static hipError_t launch_gemm(const MxGemm& p, hipStream_t st) {
            : p.xsrc == kXF16 ? launch_few<kXF16, FUSED>(p, st)
                              : launch_few<kXPlanes, FUSED>(p, st);
   if (p.xsrc != kXBf16)
-    return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 2, 2, FUSED>(p, st) : launch_tiled<4, 4, 1, 4, 2, 2, FUSED>(p, st);
+    return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 2, 2, FUSED>(p, st)
+                            : launch_tiled<4, 4, 1, 4, 2, 2, FUSED>(p, st);
   return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 1, 4, FUSED>(p, st)
          : k == kMidTiles ? launch_tiled<8, 2, 1, 4, 1, 2, FUSED>(p, st)
                           : launch_tiled<8, 4, 1, 4, 1, 2, FUSED>(p, st);
@@ -1202,6 +1234,8 @@ hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStre
 }
 
 namespace {
+// Binary16 x as two planes of bf16, once, for products whose tiles read a row of x many times (six bytes
+// of traffic per input; few rows are split where they are read).
 __global__ __launch_bounds__(256) void mx4_split_kernel(const f16x8* __restrict__ x, int64_t n8,
                                                         bf16x8* __restrict__ hi, bf16x8* __restrict__ lo) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -1284,8 +1318,8 @@ hipError_t launch_mx4_matmul(const Mx4Matmul& p, void* ws, hipStream_t st) {
   const int stages = (p.K + 127) / 128;
   const int pad_a = (int)round_up(p.M, c->bm), pad_w = (int)round_up(p.N, c->bn);
   const int64_t threads = (int64_t)(pad_a + pad_w) * stages;
-  mx4_scale_kernel<<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(p.sa, p.M, p.s, p.N, p.K / 32, stages, pad_a,
-                                                                          pad_w, (uint16_t*)ws);
+  mx4_scale_kernel<<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(p.sa, p.M, p.s, p.N, p.K / 32, stages,
+                                                                          pad_a, pad_w, (uint16_t*)ws);
   return c->launch(p, (const uint16_t*)ws, stages, pad_a, st);
 }
 

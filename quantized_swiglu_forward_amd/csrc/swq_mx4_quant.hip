@@ -11,7 +11,13 @@
 namespace swq {
 namespace {
 
-// One thread per 8 inputs (one word of codes), four threads per block.
+// Bound by the bytes: 8192 x 10240 bf16 (168 MB in, 45 MB out) takes 43 us, 5.0 TB/s (a
+// large copy reaches 5.2); its inverse 31 us, the codes still in the last-level
+// cache.  48 x 2048 takes 2.5 us each, one load's latency and the launch.
+
+// One thread per 8 inputs (one word of codes), four threads per block: a wave reads one contiguous
+// kilobyte (16-bit inputs) and writes 256 bytes, and the block's maximum is two
+// lane exchanges.  Maximum and scale are exact; the one rounding is the code's.
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void* __restrict__ x, int64_t words,
                                                            uint32_t* __restrict__ codes,
@@ -48,6 +54,8 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const void* __restric
   if ((i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
+// One thread per word of codes.  code * 2^e is exact in float32 and rounded once, to nearest even, for
+// 16-bit outputs.
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, int64_t words,
