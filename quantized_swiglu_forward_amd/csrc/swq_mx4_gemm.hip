@@ -229,8 +229,8 @@ __device__ __forceinline__ void finish4(const MxGemm& p, int64_t at, int col, f3
 //
 // Measured: 70 float16 rows of 32 experts, 1504 x 2049 (53 MB): 10.4 us with the weights in the last-level
 // cache (5.1 TB/s), 15.6 from memory.  16 tokens, 8 of 64 experts: gate and up 2048 x 1024 37 us (123 MB,
-// 3.3 TB/s), down 22; at 2080 x 1056 28 and 17: rows a power of two of bytes apart fall on
-// few channels of the L2.  16 x 5632 x 2048: 9.9 us, the chain of load, MFMA and join.
+// 3.3 TB/s), down 22; at 2080 x 1056, where rows are no power of two of
+// bytes apart, 28 and 17 (4.7 TB/s).  16 x 5632 x 2048: 9.9 us, the chain of load, MFMA and join.
 
 // Row tiles whose partial sums meet in LDS at once, and the f32x4 of LDS that this takes.
 constexpr int few_pass(int rt, int nw, int w) {
