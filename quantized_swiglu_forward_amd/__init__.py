@@ -412,6 +412,8 @@ def _mx4_shape(codes, scales, what, K=-1, dims=2):
                          f"{dims}-dimensional MXFP4 matrix")
     if K >= 0 and c[-1] * 8 != K:
         raise ValueError(f"{what}: the weights have {c[-1] * 8} inputs, x has {K}")
+    if K == 0:                                # (so that the callers' test for no rows is x.numel() == 0)
+        raise ValueError(f"{what}: a product needs inputs (K = 0)")
     return c[:-1]
 
 
