@@ -154,14 +154,15 @@ int swiglu_q_mx4_linear(const void* x, const uint32_t* W, const void* s, const v
   g.kind = mx4_gemm_kind(g);
   g.splits = mx4_gemm_splits(g);
   const int64_t planes = planes_bytes(g, M), parts = g.splits > 1 ? g.splits * M * N * 4 : 0;
+  void* ws = nullptr;
   if (planes + parts) {
-    void* ws = nullptr;
     rc = stream_workspace((hipStream_t)stream, (size_t)(planes + parts), &ws, kWsSlot);
-    if (rc == SWQ_OK) rc = to_planes(g, M, ws, (hipStream_t)stream);
     if (rc != SWQ_OK) return rc;
     g.parts = (float*)((char*)ws + planes);
   }
-  (void)hipGetLastError();
+  (void)hipGetLastError();            // before the first launch: an error left by others is not this call's
+  rc = to_planes(g, M, ws, (hipStream_t)stream);
+  if (rc != SWQ_OK) return rc;
   return check_status(launch_mx4_gemm(g, (hipStream_t)stream));
 }
 

@@ -1,0 +1,53 @@
+"""The MXFP4 operators, the router and the experts' MLP on the GPU where a
+caller's state or a size is out of the ordinary: errors that other code left
+behind."""
+import pytest
+import torch
+
+import quantized_swiglu_forward_amd as swq
+from gpu_helpers import say
+from test_gpu_mx4 import BF16, F16, acts, matrix, moe_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    swq.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def leave_an_error():
+    """What a failed HIP call of other code leaves in this thread (the host refuses the device number)."""
+    assert swq.lib().hipSetDevice(1 << 20) != 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_error_of_other_code(M, dtype):
+    """An error that an earlier call of other code left is not this call's: it runs and reports success."""
+    t = swq.SWQ_TYPE_F16 if dtype == F16 else swq.SWQ_TYPE_BF16
+    K, N, T, k, E = 96, 130, M, 2, 3
+    x, (w, s) = acts(M, M, K, dtype=dtype), matrix(2, E, N, K)
+    (wu, su), (wd, sd) = matrix(3, E, N // 32 * 32, K), matrix(4, E, K, N // 32 * 32)
+    off = torch.tensor([0, M // 3, M // 2, M], dtype=torch.int32).cuda()
+    _, ids, weights, _ = moe_case(1, T, k, E, 32, 32, 32, dtype)
+    a, sa = swq.mx4_quantize(x)
+    gate = w[:, :wu.shape[1]].contiguous(), s[:, :wu.shape[1]].contiguous()
+    say("error of other code", M, dtype)
+    want = [swq.mx4_linear(x, w[0], s[0]), swq.mx4_matmul(a, sa, w[0], s[0], out_mode=t),
+            swq.mx4_grouped_linear(x, off, w, s), swq.moe_mlp(x, ids, weights, *gate, wu, su, wd, sd)]
+    got = [torch.full_like(y, float("nan")) for y in want]
+    torch.cuda.synchronize()
+    calls = [lambda o: swq.swiglu_q_mx4_linear(x, w[0], s[0], None, M, K, N, t, t, o),
+             lambda o: swq.swiglu_q_mx4_matmul(a, sa, w[0], s[0], M, K, N, t, o),
+             lambda o: swq.swiglu_q_mx4_grouped_linear(x, off, w, s, M, E, K, N, t, t, o),
+             lambda o: swq.swiglu_q_moe_mlp(x, ids, weights, *gate, wu, su, wd, sd, None, T, k, E, K, wu.shape[1], K,
+                                            t, t, o)]
+    for call, o in zip(calls, got):
+        leave_an_error()
+        assert call(o) == swq.SWQ_OK
+    for p, q in zip(want, got):
+        assert torch.equal(p, q)
