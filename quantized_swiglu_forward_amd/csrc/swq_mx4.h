@@ -67,22 +67,26 @@ struct MxGemm {
 #ifdef __HIPCC__
   // the parts of an output's way to memory that this product has
   __device__ uint16_t* low_plane() const { return hidden_planes ? (uint16_t*)out + out_plane : nullptr; }
+  __device__ int stride() const { return N; }                 // from one output row to the next
   __device__ void add_residual(float* f, int64_t at) const;   // eight neighbours, 16-byte aligned
   __device__ void add_one(float& f, int64_t at) const;
 #endif
 };
 
+// out[m, n] = sum_k a[m, k] w[n, k] of two MXFP4 operands; rows of out are ld apart (N, or more
+// where the launch takes some columns).
 struct Mx4Matmul {
   const uint32_t* a;
   const uint8_t* sa;
   const uint32_t* w;
   const uint8_t* s;
   void* out;
-  int M, K, N, out_type;
+  int M, K, N, ld, out_type;
   int vec;                  // as MxGemm
 
 #ifdef __HIPCC__
   __device__ uint16_t* low_plane() const { return nullptr; }
+  __device__ int stride() const { return ld; }
   __device__ void add_residual(float*, int64_t) const {}
   __device__ void add_one(float&, int64_t) const {}
 #endif

@@ -178,7 +178,7 @@ int swiglu_q_mx4_matmul(const uint32_t* A, const void* sa, const uint32_t* W, co
   if (rc != SWQ_OK) return rc;
   if (!aligned(out, type_bytes(out_mode))) return SWQ_ERR_ALIGN;
   if (M == 0) return SWQ_OK;
-  Mx4Matmul p{A, (const uint8_t*)sa, W, (const uint8_t*)sw, out, (int)M, (int)K, (int)N, out_mode,
+  Mx4Matmul p{A, (const uint8_t*)sa, W, (const uint8_t*)sw, out, (int)M, (int)K, (int)N, (int)N, out_mode,
               vec_ok(N, out, nullptr, out_mode)};
   void* ws = nullptr;
   if (const int64_t need = mx4_matmul_workspace(p)) {

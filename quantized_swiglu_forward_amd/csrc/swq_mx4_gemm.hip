@@ -129,7 +129,7 @@ __device__ __forceinline__ void drain16(const Spec& p, const float* buf, int row
       if (u >= 16 * UNITS || lr >= rows || col >= p.N) continue;
       const f32x4 a = *(const f32x4*)(buf + lr * LD + c), b = *(const f32x4*)(buf + lr * LD + c + 4);
       float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      const int64_t at = row_at(lr) * p.N + col;
+      const int64_t at = row_at(lr) * p.stride() + col;
       p.add_residual(f, at);
       if (p.out_type == kTypeF32) {
         *(f32x4*)((float*)p.out + at) = (f32x4){f[0], f[1], f[2], f[3]};
@@ -154,7 +154,7 @@ __device__ __forceinline__ void drain16(const Spec& p, const float* buf, int row
       const int u = i * 64 + lane, lr = u / COLS, c = u % COLS, col = col0 + c;
       if (lr >= rows || col >= p.N) continue;
       float f = buf[lr * LD + c];
-      const int64_t at = row_at(lr) * p.N + col;
+      const int64_t at = row_at(lr) * p.stride() + col;
       p.add_one(f, at);
       if (p.out_type == kTypeF32) ((float*)p.out)[at] = f;
       else ((uint16_t*)p.out)[at] = to_16(f, p.out_type);
@@ -813,7 +813,7 @@ __device__ __forceinline__ void store_wide(const Mx4Matmul& p, const f32x16 (&ac
   for (int i = 0; i < AF; ++i) {
     const int m = mw + 32 * i + r;
     if (m >= p.M) continue;
-    const int64_t at = (int64_t)m * p.N;
+    const int64_t at = (int64_t)m * p.ld;
 #pragma unroll
     for (int j = 0; j < WF; ++j) {
       const f32x16& v = acc[i][j];
@@ -883,8 +883,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void mx4_matmul_ke
   // together, a row past the end repeating the tile's first.  Scales: load i of wave w
   // takes the 128 bytes of row groups 2 (W i + w) and the next (the operands put together).
   constexpr int OF_A = BM / (16 * W);                  // the loads that are of A
-  // The descriptors cover the whole operands (under 4 GiB each): they stay in scalar
-  // registers whatever the tile.
+  // The descriptors cover the whole operands of the launch (under 4 GiB each, kSlabBytes): they stay in
+  // scalar registers whatever the tile.
   const i32x4 ra = make_srsrc(p.a, (uint32_t)p.M * (uint32_t)row_bytes);
   const i32x4 rw = make_srsrc(p.w, (uint32_t)p.N * (uint32_t)row_bytes);
   const i32x4 rs = make_srsrc(scales, (uint32_t)(pad_a + ntn * BN) * (uint32_t)stages * 4u);
@@ -1285,10 +1285,28 @@ static const MatmulConfig kMatmul[] = {
     {64, 64, launch_matmul_as<1, 1, 2, 2, 7, 2>},
 };
 
+// The tiles address their operands with 32-bit byte offsets.  An operand past them is taken in slabs of
+// rows, about equal ones of whole tiles, each with launches of its own: 1114112 x 8192 x 512
+// (4.25 GiB of codes) in two slabs 3.2 ms (2.9 PFLOP/s);
+// the kernel for few outputs, which needs no slabs, takes 60.
+constexpr int64_t kSlabBytes = (int64_t(1) << 32) - 16;
+static int64_t slab_rows(int64_t rows, int64_t K) {
+  const int64_t slabs = ceil_div(rows, kSlabBytes / (K / 2) / 256 * 256);
+  return slabs < 2 ? rows : round_up(ceil_div(rows, slabs), 256);
+}
+static Mx4Matmul slab(const Mx4Matmul& p, int64_t m, int64_t n) {      // the one that starts at row m, column n
+  Mx4Matmul q = p;
+  q.a += m * (p.K / 8);
+  q.sa += m * (p.K / 32);
+  q.w += n * (p.K / 8);
+  q.s += n * (p.K / 32);
+  q.out = (char*)p.out + (m * p.ld + n) * type_bytes(p.out_type);
+  q.M = (int)std::min(slab_rows(p.M, p.K), p.M - m);
+  q.N = (int)std::min(slab_rows(p.N, p.K), p.N - n);
+  return q;
+}
+
 static const MatmulConfig* matmul_config(const Mx4Matmul& p) {
-  // operands past the kernels' 32-bit offsets
-  if (std::max<int64_t>(p.M, p.N) * (p.K / 2) >= (int64_t(1) << 32) - 16) return nullptr;
-  const auto tiles = [&](const MatmulConfig& c) { return ceil_div(p.M, c.bm) * ceil_div(p.N, c.bn); };
   const int64_t cus = device_cus();
   // Up to two 16 x 16 tiles a CU, or four with little K: no scale layout, no LDS, one launch.
   // Against the 64 x 64 tiles with their scale layout (us; tiles, M x K x N):
@@ -1297,6 +1315,8 @@ static const MatmulConfig* matmul_config(const Mx4Matmul& p) {
   //   896  16 x 4096 x 14336  16.2 against 14.1      1024  32 x 4096 x 8192   16.1 against 11.4
   const int64_t small = ceil_div(p.M, 16) * ceil_div(p.N, 16);
   if (small <= 2 * cus || (small <= 4 * cus && (int64_t)p.M * p.N * p.K <= (int64_t(1) << 29))) return nullptr;
+  const Mx4Matmul q = slab(p, 0, 0);
+  const auto tiles = [&](const MatmulConfig& c) { return ceil_div(q.M, c.bm) * ceil_div(q.N, c.bn); };
   return 5 * tiles(kMatmul[0]) >= 3 * cus   ? &kMatmul[0]
          : 2 * tiles(kMatmul[1]) >= cus ? &kMatmul[1]
                                           : &kMatmul[2];
@@ -1304,23 +1324,30 @@ static const MatmulConfig* matmul_config(const Mx4Matmul& p) {
 
 int64_t mx4_matmul_workspace(const Mx4Matmul& p) {
   const MatmulConfig* c = matmul_config(p);
-  return c ? (round_up(p.M, c->bm) + round_up(p.N, c->bn)) * ((p.K + 127) / 128) * 4 : 0;
+  const Mx4Matmul q = slab(p, 0, 0);         // the largest; the others' scales take its place in turn
+  return c ? (round_up(q.M, c->bm) + round_up(q.N, c->bn)) * ((p.K + 127) / 128) * 4 : 0;
 }
 
 hipError_t launch_mx4_matmul(const Mx4Matmul& p, void* ws, hipStream_t st) {
   const MatmulConfig* c = matmul_config(p);
-  if (!c) {
-    const int64_t tiles = (int64_t)((p.N + 15) / 16) * ((p.M + 15) / 16);
-    if (tiles >= (1LL << 31)) return hipErrorInvalidValue;
+  if (!c) {                                  // few blocks, by the rule above
+    const int64_t tiles = ceil_div(p.N, 16) * ceil_div(p.M, 16);
     mx4_matmul_few_kernel<8, 2><<<dim3((unsigned)tiles), 512, 0, st>>>(p);
     return hipGetLastError();
   }
   const int stages = (p.K + 127) / 128;
-  const int pad_a = (int)round_up(p.M, c->bm), pad_w = (int)round_up(p.N, c->bn);
-  const int64_t threads = (int64_t)(pad_a + pad_w) * stages;
-  mx4_scale_kernel<<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(p.sa, p.M, p.s, p.N, p.K / 32, stages,
-                                                                          pad_a, pad_w, (uint16_t*)ws);
-  return c->launch(p, (const uint16_t*)ws, stages, pad_a, st);
+  const int64_t ms = slab_rows(p.M, p.K), ns = slab_rows(p.N, p.K);
+  for (int64_t m = 0; m < p.M; m += ms)
+    for (int64_t n = 0; n < p.N; n += ns) {
+      const Mx4Matmul q = slab(p, m, n);
+      const int pad_a = (int)round_up(q.M, c->bm), pad_w = (int)round_up(q.N, c->bn);
+      const int64_t threads = (int64_t)(pad_a + pad_w) * stages;
+      mx4_scale_kernel<<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(
+          q.sa, q.M, q.s, q.N, q.K / 32, stages, pad_a, pad_w, (uint16_t*)ws);
+      const hipError_t rc = c->launch(q, (const uint16_t*)ws, stages, pad_a, st);
+      if (rc != hipSuccess) return rc;
+    }
+  return hipSuccess;
 }
 
 }  // namespace swq

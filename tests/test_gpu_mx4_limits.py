@@ -1,12 +1,13 @@
 """The MXFP4 operators, the router and the experts' MLP on the GPU where a
 caller's state or a size is out of the ordinary: errors that other code left
-behind."""
+behind, operands of 4 GiB and more."""
 import pytest
 import torch
 
+import mx4_reference as ref
 import quantized_swiglu_forward_amd as swq
 from gpu_helpers import say
-from test_gpu_mx4 import BF16, F16, acts, matrix, moe_case
+from test_gpu_mx4 import BF16, F16, F32, MODE, acts, matrix, moe_case
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,28 @@ def test_error_of_other_code(M, dtype):
         assert call(o) == swq.SWQ_OK
     for p, q in zip(want, got):
         assert torch.equal(p, q)
+
+
+# One operand of more than 4 GiB, whose rows come in two slabs (the second begins at 524544):
+# rows of outputs of both widths, and as many outputs as the kernel for few could not launch.
+PAST_4_GIB = [(1048876, 8192, 70), (1048876, 8192, 4096), (70, 8192, 1048877), (5, 8192, 1048880)]
+
+
+@pytest.mark.parametrize("M,K,N", PAST_4_GIB)
+def test_matmul_past_4_gib(M, K, N):
+    rows = max(M, N)
+    large = torch.zeros(rows, K // 8, dtype=torch.int32, device="cuda")
+    scales = torch.full((rows, K // 32), 127, dtype=torch.uint8, device="cuda")
+    pick = torch.tensor([0, 1, 300, rows // 3, 524543, 524544, 524671, 524672, 524700, rows - 2, rows - 1]).cuda()
+    large[pick], scales[pick] = matrix(1, len(pick), K, lo=120, hi=134)
+    c, s = matrix(2, min(M, N), K)
+    for out in (BF16, F32) if M * N < 1 << 30 else (BF16,):
+        say("matmul past 4 GiB", M, K, N, out)
+        a, w = ((large, scales), (c, s)) if M > N else ((c, s), (large, scales))
+        got = swq.mx4_matmul(*a, *w, out_mode=MODE[out])
+        y, err = ref.dot(ref.values(large[pick], scales[pick]), ref.values(c, s))
+        rows_of = got if M > N else got.t()
+        ref.close(rows_of[pick], y, ref.rounded(y, err, out), f"past 4 GiB {out}")
+        live = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        live[pick] = True
+        assert torch.equal((rows_of != 0).any(1), live)          # (zero codes: zeros)
