@@ -77,25 +77,45 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint32_t* __r
   }
 }
 
+// One launch holds fewer than 2^32 threads (of more the rest is left out, with no error); words past
+// kLaunchWords go to further launches.
+constexpr int64_t kLaunchWords = int64_t(1) << 30;
+
+template <int TYPE>
+void quantize_as(const void* x, int64_t words, uint32_t* codes, uint8_t* scales, hipStream_t st) {
+  for (int64_t w = 0; w < words; w += kLaunchWords) {
+    const int64_t n = words - w < kLaunchWords ? words - w : kLaunchWords;
+    mx4_quantize_kernel<TYPE><<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(
+        (const char*)x + w * 8 * type_bytes(TYPE), n, codes + w, scales + w / 4);
+  }
+}
+
+template <int TYPE>
+void dequantize_as(const uint32_t* codes, const uint8_t* scales, int64_t words, void* out, hipStream_t st) {
+  for (int64_t w = 0; w < words; w += kLaunchWords) {
+    const int64_t n = words - w < kLaunchWords ? words - w : kLaunchWords;
+    mx4_dequantize_kernel<TYPE><<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(
+        codes + w, scales + w / 4, n, (char*)out + w * 8 * type_bytes(TYPE));
+  }
+}
+
 }  // namespace
 
 hipError_t launch_mx4_quantize(const void* x, int64_t blocks, int type, uint32_t* codes, uint8_t* scales,
                                hipStream_t st) {
   const int64_t words = blocks * 4;
-  const dim3 grid((unsigned)((words + 255) / 256));
-  if (type == kTypeF32) mx4_quantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(x, words, codes, scales);
-  else if (type == kTypeF16) mx4_quantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(x, words, codes, scales);
-  else mx4_quantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(x, words, codes, scales);
+  if (type == kTypeF32) quantize_as<kTypeF32>(x, words, codes, scales, st);
+  else if (type == kTypeF16) quantize_as<kTypeF16>(x, words, codes, scales, st);
+  else quantize_as<kTypeBf16>(x, words, codes, scales, st);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_dequantize(const uint32_t* codes, const uint8_t* scales, int64_t blocks, int type, void* out,
                                  hipStream_t st) {
   const int64_t words = blocks * 4;
-  const dim3 grid((unsigned)((words + 255) / 256));
-  if (type == kTypeF32) mx4_dequantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(codes, scales, words, out);
-  else if (type == kTypeF16) mx4_dequantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(codes, scales, words, out);
-  else mx4_dequantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(codes, scales, words, out);
+  if (type == kTypeF32) dequantize_as<kTypeF32>(codes, scales, words, out, st);
+  else if (type == kTypeF16) dequantize_as<kTypeF16>(codes, scales, words, out, st);
+  else dequantize_as<kTypeBf16>(codes, scales, words, out, st);
   return hipGetLastError();
 }
 

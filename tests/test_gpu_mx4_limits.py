@@ -1,6 +1,6 @@
 """The MXFP4 operators, the router and the experts' MLP on the GPU where a
 caller's state or a size is out of the ordinary: errors that other code left
-behind, operands of 4 GiB and more."""
+behind, operands of 4 GiB and more, more threads than one launch holds."""
 import pytest
 import torch
 
@@ -77,3 +77,36 @@ def test_matmul_past_4_gib(M, K, N):
         live = torch.zeros(rows, dtype=torch.bool, device="cuda")
         live[pick] = True
         assert torch.equal((rows_of != 0).any(1), live)          # (zero codes: zeros)
+
+
+def room(gib):
+    """Whether the card has this much memory left for a test; what torch holds unused is given back first."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of GPU memory")
+
+
+def test_quantize_past_a_launch():
+    """More than 2^35 elements, 2^32 words of codes: rows at the borders of the launches and the last ones
+    against the same rows alone."""
+    room(100)
+    K = 1 << 17
+    R = (1 << 18) + 3                                  # one launch takes 2^33 elements, 2^16 rows
+    pick = [0, 1, 65535, 65536, 131071, 131072, 196608, 262143, 262144, R - 1]
+    say("quantize past a launch")
+    x = torch.zeros(R, K, dtype=BF16, device="cuda")
+    part = acts(5, len(pick), K)
+    x[pick] = part
+    codes, scales = swq.mx4_quantize(x)
+    c, s = swq.mx4_quantize(part)
+    assert torch.equal(codes[pick], c) and torch.equal(scales[pick], s)
+    live = torch.zeros(R, dtype=torch.bool, device="cuda")
+    live[pick] = True
+    rows_with = lambda t: torch.cat([(u != 0).any(1) for u in t.split(1 << 14)])
+    assert torch.equal(rows_with(codes), live) and torch.equal(rows_with(scales), live)
+    x.fill_(float("nan"))
+    swq.mx4_dequantize(codes, scales, BF16, out=x)
+    assert torch.equal(x[pick], swq.mx4_dequantize(c, s, BF16)) and torch.equal(rows_with(x), live)
+    del x, codes, scales
+    torch.cuda.empty_cache()
