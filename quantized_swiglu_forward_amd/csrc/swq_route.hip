@@ -357,10 +357,18 @@ static hipError_t launch_route_k(const void* logits, int64_t T, int E, int k, in
 
 hipError_t launch_route(const void* logits, int64_t T, int E, int k, int type, int scoring, int* ids, float* weights,
                         hipStream_t st) {
-  if (T * 64 >= (int64_t(1) << 39)) return hipErrorInvalidValue;
-  return type == kTypeF32   ? launch_route_k<kTypeF32>(logits, T, E, k, scoring, ids, weights, st)
-         : type == kTypeF16 ? launch_route_k<kTypeF16>(logits, T, E, k, scoring, ids, weights, st)
-                            : launch_route_k<kTypeBf16>(logits, T, E, k, scoring, ids, weights, st);
+  // a launch holds fewer than 2^32 threads, up to 64 of them a token
+  constexpr int64_t kLaunchTokens = int64_t(1) << 24;
+  for (int64_t t = 0; t < T; t += kLaunchTokens) {
+    const int64_t n = T - t < kLaunchTokens ? T - t : kLaunchTokens;
+    const void* l = (const char*)logits + t * E * type_bytes(type);
+    const hipError_t rc = type == kTypeF32 ? launch_route_k<kTypeF32>(l, n, E, k, scoring, ids + t * k, weights + t * k, st)
+                          : type == kTypeF16
+                              ? launch_route_k<kTypeF16>(l, n, E, k, scoring, ids + t * k, weights + t * k, st)
+                              : launch_route_k<kTypeBf16>(l, n, E, k, scoring, ids + t * k, weights + t * k, st);
+    if (rc != hipSuccess) return rc;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {

@@ -110,3 +110,23 @@ def test_quantize_past_a_launch():
     assert torch.equal(x[pick], swq.mx4_dequantize(c, s, BF16)) and torch.equal(rows_with(x), live)
     del x, codes, scales
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,T,E", [(BF16, (1 << 28) + 5, 4), (F16, (1 << 24) + 3, 264), (F32, (1 << 24) + 3, 257)])
+def test_route_past_a_launch(dtype, T, E):
+    """Tokens of several launches (the first case: 2^32 threads in all and more): those at the borders and the last ones
+    against the same tokens alone."""
+    room(40)
+    pick = torch.tensor([0, 1, (1 << 24) - 1, 1 << 24, T // 2, T - 2, T - 1]).cuda()
+    lo = torch.zeros(T, E, dtype=dtype, device="cuda")
+    lo[pick] = part = acts(3, len(pick), E, dtype=dtype)
+    say("route past a launch", dtype, T, E)
+    ids = torch.full((T, 2), -7, dtype=torch.int32, device="cuda")
+    weights = torch.full((T, 2), float("nan"), device="cuda")
+    swq.route(lo, 2, swq.SWQ_ROUTE_SOFTMAX_CHOSEN, ids=ids, weights=weights)
+    i, w = swq.route(part, 2, swq.SWQ_ROUTE_SOFTMAX_CHOSEN)
+    assert torch.equal(ids[pick], i) and torch.equal(weights[pick], w)
+    ids[pick], weights[pick] = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 0.5
+    assert bool((ids[:, 0] == 0).all()) and bool((ids[:, 1] == 1).all()) and bool((weights == 0.5).all())
+    del lo, ids, weights
+    torch.cuda.empty_cache()
