@@ -1248,8 +1248,12 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(const f16x8* __restrict_
 }  // namespace
 
 hipError_t launch_mx4_split(const uint16_t* x, int64_t n, uint16_t* planes, int64_t plane, hipStream_t st) {
-  mx4_split_kernel<<<dim3((unsigned)((n / 8 + 255) / 256)), 256, 0, st>>>((const f16x8*)x, n / 8, (bf16x8*)planes,
-                                                                         (bf16x8*)(planes + plane));
+  constexpr int64_t kLaunch = int64_t(1) << 30;          // a launch holds fewer than 2^32 threads
+  for (int64_t i = 0; i < n / 8; i += kLaunch) {
+    const int64_t n8 = std::min(kLaunch, n / 8 - i);
+    mx4_split_kernel<<<dim3((unsigned)((n8 + 255) / 256)), 256, 0, st>>>(
+        (const f16x8*)x + i, n8, (bf16x8*)planes + i, (bf16x8*)(planes + plane) + i);
+  }
   return hipGetLastError();
 }
 

@@ -1,5 +1,7 @@
 // The router's choice, the order of a product grouped by expert, and the sum
 // over a token's experts.
+#include <algorithm>
+
 #include "swq_mx4.h"
 #include "swq_mx4_device.h"
 
@@ -380,11 +382,19 @@ hipError_t launch_plan(const RoutePlan& p, hipStream_t st) {
 hipError_t launch_combine(const float* part, const int* ids, const float* weights, const uint16_t* res, int64_t T,
                           int k, int E, int N, int64_t ld, int type, int out_type, void* out, hipStream_t st) {
   const bool wide = N % 4 == 0 && ld % 4 == 0 && (uintptr_t)out % (4 * type_bytes(out_type)) == 0;
-  const int64_t threads = T * (wide ? N / 4 : N);
-  if ((threads + 255) / 256 >= (1LL << 31)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((threads + 255) / 256));
-  if (wide) combine_kernel<4><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, ld, type, out_type, out);
-  else combine_kernel<1><<<grid, 256, 0, st>>>(part, ids, weights, res, T, k, E, N, ld, type, out_type, out);
+  // a launch holds fewer than 2^32 threads: tokens of 2^30 at a time
+  const int64_t per = wide ? N / 4 : N, tokens = std::max<int64_t>((int64_t(1) << 30) / per, 1);
+  for (int64_t t = 0; t < T; t += tokens) {
+    const int64_t n = std::min(tokens, T - t);
+    const dim3 grid((unsigned)((n * per + 255) / 256));
+    const float* p = part + t * k * N;
+    const uint16_t* r = res ? res + t * ld : nullptr;
+    void* o = (char*)out + t * ld * type_bytes(out_type);
+    if (wide)
+      combine_kernel<4><<<grid, 256, 0, st>>>(p, ids + t * k, weights + t * k, r, n, k, E, N, ld, type, out_type, o);
+    else
+      combine_kernel<1><<<grid, 256, 0, st>>>(p, ids + t * k, weights + t * k, r, n, k, E, N, ld, type, out_type, o);
+  }
   return hipGetLastError();
 }
 

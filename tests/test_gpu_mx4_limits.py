@@ -7,7 +7,7 @@ import torch
 import mx4_reference as ref
 import quantized_swiglu_forward_amd as swq
 from gpu_helpers import say
-from test_gpu_mx4 import BF16, F16, F32, MODE, acts, matrix, moe_case
+from test_gpu_mx4 import BF16, F16, F32, HIDDEN, MODE, acts, matrix, moe_case
 
 pytestmark = pytest.mark.gpu
 
@@ -129,4 +129,49 @@ def test_route_past_a_launch(dtype, T, E):
     ids[pick], weights[pick] = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 0.5
     assert bool((ids[:, 0] == 0).all()) and bool((ids[:, 1] == 1).all()) and bool((weights == 0.5).all())
     del lo, ids, weights
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("Ho", [257, 260])
+def test_moe_sums_past_a_launch(Ho):
+    """So many tokens that the sums over their experts take several launches, one output or four a thread:
+    tokens at the borders (every 2^22nd, 2^24th) and the last ones against the formula."""
+    room(80)
+    T, H, I, E = (1 << 24) + 5, 32, 32, 2
+    pick = torch.tensor([0, (1 << 22) - 1, 1 << 22, 3 << 22, (1 << 24) - 1, 1 << 24, T - 2, T - 1]).cuda()
+    x = torch.zeros(T, H, dtype=BF16, device="cuda")
+    x[pick] = acts(1, len(pick), H)
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    ids[pick[1::2]] = 1
+    weights = torch.full((T, 1), 0.75, device="cuda")
+    ws = [matrix(2 + i, *sh) for i, sh in enumerate(((E, I, H), (E, I, H), (E, Ho, I)))]
+    out = torch.full((T, Ho), float("nan"), dtype=BF16, device="cuda")
+    say("moe sums past a launch", Ho)
+    swq.moe_mlp(x, ids, weights, *ws[0], *ws[1], *ws[2], out=out)
+    y, err = ref.experts(ref.to64(x[pick]), ids[pick].cpu().numpy(), ref.to64(weights[pick]),
+                         *(ref.values(*w) for w in ws), None, HIDDEN[BF16])
+    ref.close(out[pick], y, ref.rounded(y, err, BF16), "moe sums past a launch")
+    out[pick] = 0
+    assert not any(bool((part != 0).any()) for part in out.split(1 << 22))       # (zero rows: zeros)
+    del x, out
+    swq.swiglu_q_release_workspace()
+    torch.cuda.empty_cache()
+
+
+def test_linear_split_past_a_launch():
+    """float16 rows of more than 2^33 elements, whose split takes several launches."""
+    room(80)
+    M, K, N = 8200, 1 << 20, 8
+    pick = torch.tensor([0, 8191, 8192, M - 1]).cuda()
+    x = torch.zeros(M, K, dtype=F16, device="cuda")
+    x[pick] = acts(1, len(pick), K, dtype=F16)
+    w, s = matrix(2, N, K)
+    say("linear split past a launch")
+    got = swq.mx4_linear(x, w, s, out_mode=swq.SWQ_LINEAR_F32)
+    y, err = ref.dot(ref.to64(x[pick]), ref.values(w, s))
+    ref.close(got[pick], y, ref.rounded(y, err, F32), "linear split past a launch")
+    got[pick] = 0
+    assert not bool(got.any())
+    del x
+    swq.swiglu_q_release_workspace()
     torch.cuda.empty_cache()
