@@ -252,7 +252,8 @@ int swiglu_q_mlp(const void *x,
  * need it (partial sums of a K split, binary16 rows as two bf16 planes, the scales
  * of two MXFP4 operands in the matrix instructions' order, the experts' order, hidden
  * tensor and outputs), with the rules for graphs and concurrent calls given at the
- * top.
+ * top.  A product with MXFP4 weights whose launch would take 2^32 threads or more
+ * (2^20 columns for each of 1024 experts' few rows, say) is refused: SWQ_ERR_SHAPE.
  */
 
 /* Element types (and the out_mode values beyond the affine linear's two). */

@@ -55,9 +55,10 @@ struct MxGemm {
   int hidden_planes;        // 1: write the hidden tensor as two bf16 planes
   const RowTile* tiles;     // tile table, or null
   const int* ntiles;
-  const int* offsets;       // without tiles: [E + 1] the experts' first rows, E <= 64, or null
+  const int* offsets;       // without a table: [E + 1] the experts' first rows, E <= 64, or null
   const int* perm;          // slot -> row of out, or null (the same)
-  int max_tiles;
+  int max_tiles;            // with tiles or offsets: the most there can be; else 0
+  int check_only;           // 1: the launch functions launch nothing and say whether one launch can hold the product
   int kind;                 // kFew .. kLargeTiles (mx4_gemm_kind)
   int splits;               // K splits (mx4_gemm_splits; 0 and 1: none) and their partial sums [splits][rows][N]
   float* parts;

@@ -65,6 +65,12 @@ int vec_ok(int64_t N, const void* out, const void* res, int out_type) {
   return N % 4 == 0 && aligned(out, 4 * type_bytes(out_type)) && (!res || aligned(res, 8));
 }
 
+// Whether a launch can hold the product (sizes, kind and tiles are set, pointers need not be).
+bool fits(MxGemm g) {
+  g.check_only = 1;
+  return launch_mx4_gemm(g, nullptr) == hipSuccess;
+}
+
 // x as the product's kernels read it: binary16 rows become two bf16 planes in
 // the workspace where they ask for it.
 int64_t planes_bytes(const MxGemm& g, int64_t rows) {
@@ -95,7 +101,6 @@ int run_plan(MxGemm& g, char* ws, const PlanLayout& l, const int* ids, const int
   if (perm) *perm = r.perm;
   g.tiles = r.tiles;
   g.ntiles = r.ntiles;
-  g.max_tiles = (int)max_row_tiles(g.rows, g.E, tile);
   return check_status(launch_plan(r, st));
 }
 
@@ -153,6 +158,7 @@ int swiglu_q_mx4_linear(const void* x, const uint32_t* W, const void* s, const v
   g.vec = vec_ok(N, out, residual, out_mode);
   g.kind = mx4_gemm_kind(g);
   g.splits = mx4_gemm_splits(g);
+  if (!fits(g)) return SWQ_ERR_SHAPE;
   const int64_t planes = planes_bytes(g, M), parts = g.splits > 1 ? g.splits * M * N * 4 : 0;
   void* ws = nullptr;
   if (planes + parts) {
@@ -219,6 +225,8 @@ int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uin
   g.kind = mx4_gemm_kind(g);
   const int tile = mx4_gemm_tile(g);
   const bool planned = E > kOffsetExperts;
+  g.max_tiles = (int)max_row_tiles(P, E, tile);
+  if (!fits(g)) return SWQ_ERR_SHAPE;
   const PlanLayout l = planned ? plan_layout(P, E, tile, false) : PlanLayout{0, 0, 0};
   void* ws = nullptr;
   if (const int64_t need = l.total + planes_bytes(g, P)) rc = stream_workspace(stream, (size_t)need, &ws, kWsSlot);
@@ -228,7 +236,6 @@ int swiglu_q_mx4_grouped_linear(const void* x, const int32_t* offsets, const uin
     rc = run_plan(g, (char*)ws, l, nullptr, offsets, tile, stream);
   } else {
     g.offsets = offsets;
-    g.max_tiles = (int)max_row_tiles(P, E, tile);
   }
   if (rc == SWQ_OK) rc = to_planes(g, P, (char*)ws + l.total, stream);
   if (rc != SWQ_OK) return rc;
@@ -294,44 +301,48 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   const bool direct = T <= kDirectTokens;
   g.kind = direct ? (int)kFew : mx4_gemm_kind(g);
   const int tile = mx4_gemm_tile(g);
+  const int64_t cols = part_columns(P, Ho);
+  if (direct) g.ids = ids;
+  else g.max_tiles = (int)max_row_tiles(P, E, tile);
+  MxGemm d = g;                       // the down projection
+  d.w = Wd;
+  d.s = (const uint8_t*)sd;
+  d.w2 = nullptr;
+  d.s2 = nullptr;
+  d.K = (int)I;
+  d.N = (int)(direct || Ho < cols ? Ho : cols);
+  d.wrows = Ho;
+  d.xsrc = f16 ? kXPlanes : kXBf16;
+  d.out_type = SWQ_TYPE_F32;
+  d.hidden_planes = 0;
+  d.check_only = 1;
+  if (!fits(g) || (direct ? launch_mx4_down(d, weights, (int)k, stream) : launch_mx4_gemm(d, stream)) != hipSuccess)
+    return SWQ_ERR_SHAPE;
+  d.check_only = 0;
   const PlanLayout l = direct ? PlanLayout{0, 0, 0} : plan_layout(P, E, tile, true);
   const int64_t hidden = align256(P * I * 2) * (f16 ? 2 : 1);
-  const int64_t part = l.total + hidden, cols = part_columns(P, Ho);
-  const int64_t xplanes = part + (direct ? 0 : align256(P * cols * 4));
+  const int64_t part = l.total + hidden, xplanes = part + (direct ? 0 : align256(P * cols * 4));
   void* ws_v = nullptr;
   rc = stream_workspace(stream, (size_t)(xplanes + (direct ? 0 : planes_bytes(g, T))), &ws_v, kWsSlot);
   if (rc != SWQ_OK) return rc;
   char* ws = (char*)ws_v;
   (void)hipGetLastError();
-  const int* perm = nullptr;
-  if (direct) {
-    g.ids = ids;
-  } else {
+  if (!direct) {
+    const int* perm = nullptr;
     rc = run_plan(g, ws, l, ids, nullptr, tile, stream, &perm);
     if (rc == SWQ_OK) rc = to_planes(g, T, ws + xplanes, stream);
     if (rc != SWQ_OK) return rc;
+    g.xperm = perm;
+    d.perm = perm;
+    d.tiles = g.tiles;
+    d.ntiles = g.ntiles;
   }
-  g.xperm = perm;
   g.out = ws + l.total;
   g.out_plane = align256(P * I * 2) / 2;
   rc = check_status(launch_mx4_gemm(g, stream));
   if (rc != SWQ_OK) return rc;
-  MxGemm d = g;
   d.x = (const uint16_t*)(ws + l.total);
   d.plane = g.out_plane;
-  d.xperm = nullptr;
-  d.w = Wd;
-  d.s = (const uint8_t*)sd;
-  d.w2 = nullptr;
-  d.s2 = nullptr;
-  d.out = ws + part;
-  d.perm = perm;
-  d.K = (int)I;
-  d.N = (int)Ho;
-  d.wrows = Ho;
-  d.xsrc = f16 ? kXPlanes : kXBf16;
-  d.out_type = SWQ_TYPE_F32;
-  d.hidden_planes = 0;
   if (direct) {
     d.res = (const uint16_t*)residual;
     d.out = out;
@@ -339,6 +350,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
     d.vec = vec_ok(Ho, out, residual, out_mode);
     return check_status(launch_mx4_down(d, weights, (int)k, stream));
   }
+  d.out = ws + part;
   for (int64_t n = 0; n < Ho; n += cols) {
     d.N = (int)(Ho - n < cols ? Ho - n : cols);
     d.w = Wd + n * (I / 8);

@@ -1135,12 +1135,16 @@ int mx4_gemm_tile(const MxGemm& p) {
 
 bool mx4_gemm_takes_planes(const MxGemm& p) { return p.kind != kFew; }
 
+// A launch of 2^32 threads or more is cut off without an error.
+static bool one_launch(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+
 template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED>
 static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
   constexpr int BM = 16 * MF * WM, BNO = 16 * NF * WN / (FUSED ? 2 : 1);
-  const int64_t ntm = p.tiles || p.offsets ? p.max_tiles : (p.rows + BM - 1) / BM, ntn = (p.N + BNO - 1) / BNO;
-  const int64_t blocks = (ntm * ntn + 7) / 8 * 8;
-  if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+  const int64_t ntm = p.max_tiles ? p.max_tiles : ceil_div(p.rows, BM), ntn = ceil_div(p.N, BNO);
+  const int64_t blocks = ceil_div(ntm * ntn, 8) * 8;
+  if (!one_launch(blocks, 64 * WM * WN)) return hipErrorInvalidConfiguration;
+  if (p.check_only) return hipSuccess;
   if constexpr (!FUSED && MF == 4 && NF == 2) {
     if (p.splits > 1) {
       // K split: float32 partial sums [split][row][column] in the workspace, added in split order
@@ -1164,8 +1168,9 @@ static hipError_t launch_tiled(const MxGemm& p, hipStream_t st) {
 template <int RT, int CT, int XS, bool FUSED, int W, int U>
 static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
   const int64_t ntn = (p.N + 16 * CT - 1) / (16 * CT);
-  const int64_t ntm = p.tiles || p.offsets ? p.max_tiles : (p.rows + 16 * RT - 1) / (16 * RT);
-  if (ntm * ntn >= (1LL << 31)) return hipErrorInvalidValue;
+  const int64_t ntm = p.max_tiles ? p.max_tiles : ceil_div(p.rows, 16 * RT);
+  if (!one_launch(ntm * ntn, 64 * W)) return hipErrorInvalidConfiguration;
+  if (p.check_only) return hipSuccess;
   mx4_few_kernel<RT, CT, XS, FUSED, W, U><<<dim3((unsigned)(ntm * ntn)), 64 * W, 0, st>>>(p);
   return hipGetLastError();
 }
@@ -1175,7 +1180,7 @@ static hipError_t launch_few_as(const MxGemm& p, hipStream_t st) {
 template <int RT, int XS, bool FUSED>
 static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
   constexpr int D = FUSED ? 2 : 1;
-  const int64_t tiles = p.tiles || p.offsets ? std::min<int64_t>(p.max_tiles, p.rows) : ceil_div(p.rows, 16 * RT);
+  const int64_t tiles = p.max_tiles ? std::min<int64_t>(p.max_tiles, p.rows) : ceil_div(p.rows, 16 * RT);
   const int64_t need = device_cus() * 7 / 8;
   if (p.N / (16 * 4 / D) * tiles >= need) return launch_few_as<RT, 4 / D, XS, FUSED, 8, 1>(p, st);
   if (p.N / (16 * 2 / D) * tiles >= need || FUSED)
@@ -1187,14 +1192,15 @@ static hipError_t launch_few_rt(const MxGemm& p, hipStream_t st) {
 template <int XS, bool FUSED, int W>
 static hipError_t launch_row(const MxGemm& p, hipStream_t st) {
   const int64_t blocks = (int64_t)p.rows * ((p.N + 15) / 16);
-  if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+  if (!one_launch(blocks, 64 * W)) return hipErrorInvalidConfiguration;
+  if (p.check_only) return hipSuccess;
   mx4_row_kernel<XS, FUSED, W><<<dim3((unsigned)blocks), 64 * W, 0, st>>>(p);
   return hipGetLastError();
 }
 
 template <int XS, bool FUSED>
 static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
-  if (!p.tiles && !p.offsets && (p.ids || p.rows == 1))      // rows one by one; four waves cover 2048 inputs at once
+  if (!p.max_tiles && (p.ids || p.rows == 1))      // rows one by one; four waves cover 2048 inputs at once
     return p.K <= 4 * kRowU * 128 ? launch_row<XS, FUSED, 4>(p, st) : launch_row<XS, FUSED, 8>(p, st);
   const int rt = few_tiles(p);
   return rt == 1 ? launch_few_rt<1, XS, FUSED>(p, st) : rt == 2 ? launch_few_rt<2, XS, FUSED>(p, st)
@@ -1223,7 +1229,8 @@ hipError_t launch_mx4_gemm(const MxGemm& p, hipStream_t st) {
 hipError_t launch_mx4_down(const MxGemm& p, const float* weights, int k, hipStream_t st) {
   constexpr int W = 16;
   const int64_t blocks = (int64_t)(p.rows / k) * ((p.N + 15) / 16);
-  if (blocks >= (1LL << 31)) return hipErrorInvalidValue;
+  if (!one_launch(blocks, 64 * W)) return hipErrorInvalidConfiguration;
+  if (p.check_only) return hipSuccess;
   // as many waves per slot as leave no slot waiting, and no more than it has chunks for
   int share = W;
   while (share > 1 && (share * k > W || (share - 1) * kRowU * 128 >= p.K)) share >>= 1;
