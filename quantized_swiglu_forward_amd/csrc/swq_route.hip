@@ -220,6 +220,12 @@ __device__ __forceinline__ int block_scan(int v, int* wave_total) {
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(RoutePlan p) {
   __shared__ int count[kMaxExperts], next[kMaxExperts], total[kPlanThreads / 64];
+#ifdef SWQ_LDS_POISON
+  lds_poison(count, sizeof(count), kPoisonExp);
+  lds_poison(next, sizeof(next), kPoisonExp);
+  lds_poison(total, sizeof(total), kPoisonExp);
+  __syncthreads();
+#endif
   const int t = threadIdx.x, mask = gridDim.x - 1;
   int rows = 0, first = 0, last = 0;           // of expert t; the end of the last expert's rows
   if (p.ids) {
