@@ -1200,8 +1200,9 @@ static hipError_t launch_row(const MxGemm& p, hipStream_t st) {
 
 template <int XS, bool FUSED>
 static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
-  if (!p.max_tiles && (p.ids || p.rows == 1))      // rows one by one; four waves cover 2048 inputs at once
-    return p.K <= 4 * kRowU * 128 ? launch_row<XS, FUSED, 4>(p, st) : launch_row<XS, FUSED, 8>(p, st);
+  if constexpr (XS != kXPlanes)                    // (planes: the hidden tensor of experts by tiles, else mx4_down_kernel)
+    if (!p.max_tiles && (p.ids || p.rows == 1))    // rows one by one; four waves cover 2048 inputs at once
+      return p.K <= 4 * kRowU * 128 ? launch_row<XS, FUSED, 4>(p, st) : launch_row<XS, FUSED, 8>(p, st);
   const int rt = few_tiles(p);
   return rt == 1 ? launch_few_rt<1, XS, FUSED>(p, st) : rt == 2 ? launch_few_rt<2, XS, FUSED>(p, st)
                                                                 : launch_few_rt<4, XS, FUSED>(p, st);
@@ -1210,10 +1211,11 @@ static hipError_t launch_few(const MxGemm& p, hipStream_t st) {
 template <bool FUSED>
 static hipError_t launch_gemm(const MxGemm& p, hipStream_t st) {
   const int k = p.kind;
-  if (k == kFew)
-    return p.xsrc == kXBf16  ? launch_few<kXBf16, FUSED>(p, st)
-           : p.xsrc == kXF16 ? launch_few<kXF16, FUSED>(p, st)
-                             : launch_few<kXPlanes, FUSED>(p, st);
+  if (k == kFew) {
+    if constexpr (!FUSED)
+      if (p.xsrc == kXPlanes) return launch_few<kXPlanes, false>(p, st);
+    return p.xsrc == kXBf16 ? launch_few<kXBf16, FUSED>(p, st) : launch_few<kXF16, FUSED>(p, st);
+  }
   if (p.xsrc != kXBf16)
     return k == kSmallTiles ? launch_tiled<4, 2, 1, 4, 2, 2, FUSED>(p, st)
                             : launch_tiled<4, 4, 1, 4, 2, 2, FUSED>(p, st);
