@@ -1082,7 +1082,9 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 
 }  // namespace
 
-// What a product runs on: the few-row kernel up to 24 rows (a grouped product: 10 of an average
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// What a product runs on: the few-row kernel up to 24 rows, 32 of binary16 x (a grouped product: 10 of an average
 // expert, 20 of binary16 x; 32 experts, K x N = 2048 x 1408, 8 / 16 / 32 rows each:
 // few-row kernel 22 / 28 / 45 us, tiles 28 / 35 / 29), else the tile shape whose fullest
 // CU is done first.  Measured on one MI355X, a CU takes 1.77 us per chunk of a 128 x 256 tile, 0.98 of a 128 x 128 and
@@ -1093,22 +1095,31 @@ __global__ __launch_bounds__(64 * W) void mx4_matmul_few_kernel(Mx4Matmul p) {
 //   6144 x 2048 x 1408        54         49          56
 //   2048 x 4096 x 14336      286        217         218
 //   8192 x 2560 x 10240      471        391         353
+// binary16 x, whose rows are two operands, takes 64 rows a tile: 0.95 us per chunk of 64 x 128 and 1.66 of
+// 64 x 256, 2.2 where a CU has a single one (us; one to two rounds of tiles, three and more):
+//   rows x K x N          64 x 128   64 x 256      rows x K x N          64 x 128   64 x 256
+//   256 x 4096 x 14336       64         70         512 x 4096 x 14336      121        111
+//   384 x 2048 x 5632        37         40         1024 x 2048 x 5632       57         64
+//   768 x 4096 x 4096        68         73         2048 x 2560 x 10240     189        168
+// and its few-row kernel holds up to 32 rows (32 x K x N = 4096 x 4096, 4096 x 14336, 2560 x 10240, 5632 x 2048: 15 / 23 /
+// 18 / 18 us against 18 / 28 / 20 / 17 by tiles, bf16 13 / 20 / 18 / 16 against 14 / 20 / 15 / 14).
 // Where their tiles leave CUs idle the 64 x 128 kernel splits K (K x N = 5632 x 2048,
 // 32 / 64 / 256 rows: few-row kernel 15 / 26 / 27, split 13 / 15 / 19; 8192 x 512 20 / 35 / 35 against
 // 14 / 15 / 18).  On small weights, K N <= 2^20, the second launch costs more than
 // it gives: 1024 x 1024, 256 rows, few-row 8, split 11.
-static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 int mx4_gemm_kind(const MxGemm& p) {
   const int64_t each = p.rows / p.E;
-  if (each <= (p.E == 1 ? 24 : p.xsrc == kXBf16 ? 10 : 20)) return kFew;
+  const bool f16 = p.xsrc != kXBf16;
+  if (each <= (p.E == 1 ? (f16 ? 32 : 24) : f16 ? 20 : 10)) return kFew;
   if (p.E == 1 && each <= 256 && (int64_t)p.K * p.N <= (1 << 20)) return kFew;
   const int64_t part = p.E == 1 ? 0 : p.E / 2;           // half a tile per expert for its last, partial one
   const int64_t n = p.w2 ? 2 * (int64_t)p.N : p.N, cus = device_cus();
-  const auto cost = [&](int bm, int bn, int us) {
-    return us * ceil_div((ceil_div(p.rows, bm) + part) * ceil_div(n, bn), cus);
-  };
-  const int64_t large = cost(128, 256, 177), mid = cost(128, 128, 98), small = cost(64, 128, 62);
+  const auto rounds = [&](int bm, int bn) { return ceil_div((ceil_div(p.rows, bm) + part) * ceil_div(n, bn), cus); };
+  if (f16) {
+    const int64_t large = rounds(64, 256);
+    return 95 * rounds(64, 128) <= (large == 1 ? 220 : 166 * large) ? kSmallTiles : kLargeTiles;
+  }
+  const int64_t large = 177 * rounds(128, 256), mid = 98 * rounds(128, 128), small = 62 * rounds(64, 128);
   if (small <= mid && small <= large) return kSmallTiles;
   return mid < large ? kMidTiles : kLargeTiles;
 }
