@@ -1,6 +1,9 @@
 // C-ABI entry points of the microscaled 4-bit (MXFP4) operators, the router
 // and the experts' MLP (declared in include/swiglu_q.h): validation on the
 // host, then launches on the caller's stream.
+#include <algorithm>
+#include <cmath>
+
 #include "../../include/swiglu_q.h"
 #include "swq_mx4.h"
 
@@ -9,9 +12,26 @@ using namespace swq;
 namespace {
 
 constexpr int kWsSlot = 2;            // the experts' workspace beside the MLP's two
-// Most tokens whose slots are taken one by one (8 of 64 experts, 2048 x 1024; us, by expert /
-// one by one: 5 tokens 44 / 40, 6 45 / 45, 8 51 / 57, 16 62 / 106).
+// Whether the tokens' slots (T k of them) are taken one by one, each reading its expert's weights, or by expert.
+// One by one saves the plan, a join and the few-row kernel's poorer reading, about 37.5 MB's worth and a fifth of
+// the bytes of the experts reached; it pays for every expert that several tokens share, again.  The experts reached are
+// reckoned for ids that spread evenly.  Measured, us one by one / by expert (columns: tokens):
+//   k of E, H x I           2           3           4           5           6           8           12
+//   8 of 64   2048 x 1024   20 / 31     28 / 36     33 / 43     41 / 45     45 / 53     58 / 57     82 / 67
+//   8 of 256  2048 x 1024   20 / 31     28 / 37     32 / 45     42 / 53     46 / 57     59 / 69     85 / 89
+//   4 of 16   2048 x 1024   14 / 23     19 / 29     21 / 29     26 / 29     28 / 29     34 / 30     47 / 30
+//   4 of 4    2048 x 1024   12 / 21     17 / 21     19 / 21     24 / 21     26 / 21     33 / 21     46 / 31
+//   8 of 8    2048 x 1024   19 / 24     27 / 24     31 / 25     40 / 24     43 / 24     56 / 25     78 / 34
+//   2 of 8    4096 x 4096   33 / 45     45 / 55     59 / 59     70 / 65     83 / 65    105 / 64    154 / 73
+//   4 of 32   2880 x 2880   31 / 44     40 / 47     51 / 64     59 / 66     71 / 74     89 / 89    123 / 108
+// Past six tokens only many experts (256) or small ones (512 x 256: 7 / 15) still gain, and all go by expert.
 constexpr int64_t kDirectTokens = 6;
+bool slot_by_slot(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t Ho) {
+  if (T > kDirectTokens) return false;
+  const double expert = (2.0 * H * I + (double)I * Ho) * (0.5 + 1.0 / 32);      // bytes
+  const double reached = E * (1 - std::pow(1 - std::min(1.0, (double)k / E), (double)T));
+  return (T * k - reached) * expert <= 37.5e6 + 0.2 * reached * expert;
+}
 // The experts' float32 outputs that wait for their sum: what the 256 MB last-level cache still
 // holds when the sum reads them (4096 tokens, 8 of 64 experts, 2048 columns, 268 MB: in one
 // piece 529 us, in two 515, in three 558).  Equal pieces: 1280 and 768 columns, the least rounds of tiles
@@ -298,7 +318,7 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   // projection.  Else by expert: the workspace holds the plan, the hidden
   // tensor in the plan's order (two planes for binary16), the experts' outputs
   // in the slots' order, and x as planes.
-  const bool direct = T <= kDirectTokens;
+  const bool direct = slot_by_slot(T, k, E, H, I, Ho);
   g.kind = direct ? (int)kFew : mx4_gemm_kind(g);
   const int tile = mx4_gemm_tile(g);
   const int64_t cols = part_columns(P, Ho);

@@ -72,6 +72,35 @@ def test_moe_few_tokens_of_long_k(T, k, E, H, I, Ho, dtype):
     ref.close(got, y, ref.rounded(y, err, F32), "moe of long k")
 
 
+# Tokens on both sides of the border between slot by slot (few tokens that share few experts) and by expert,
+# the few-row kernels of the latter with one, two and four row tiles.
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,k,E,H,I,Ho", [(8, 8, 64, 256, 96, 130), (16, 8, 16, 96, 64, 33), (17, 8, 40, 160, 96, 64),
+                                          (33, 4, 12, 96, 352, 70), (2, 64, 64, 64, 32, 40), (3, 64, 70, 64, 32, 40),
+                                          (129, 1, 9, 288, 64, 96), (128, 1, 9, 288, 64, 96), (24, 6, 100, 64, 64, 130)])
+def test_moe_few_tokens(T, k, E, H, I, Ho, dtype):
+    x, ids, weights, ws = moe_case(T + E, T, k, E, H, I, Ho, dtype)
+    res = acts(7, T, Ho, dtype=dtype)
+    say("moe of few tokens", T, k, E, H, I, Ho, dtype)
+    got = swq.moe_mlp(x, ids, weights, *ws[0], *ws[1], *ws[2], residual=res)
+    y, err = ref.experts(ref.to64(x), ids.cpu().numpy(), ref.to64(weights), *(ref.values(*t) for t in ws),
+                         ref.to64(res), HIDDEN[dtype])
+    ref.close(got, y, ref.rounded(y, err, dtype), "moe of few tokens")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,k,E", [(4, 4, 4), (5, 4, 4), (3, 8, 8)])
+def test_moe_shared_experts(T, k, E, dtype):
+    """Every token to every expert, weights large enough to be read once (sizes on both sides of the border)."""
+    H, I, Ho = 2048, 1024, 2048
+    x, ids, weights, ws = moe_case(T + E, T, k, E, H, I, Ho, dtype, spread=False)
+    say("moe of shared experts", T, k, E, dtype)
+    got = swq.moe_mlp(x, ids, weights, *ws[0], *ws[1], *ws[2], out_mode=swq.SWQ_LINEAR_F32)
+    y, err = ref.experts(ref.to64(x), ids.cpu().numpy(), ref.to64(weights), *(ref.values(*t) for t in ws), None,
+                         HIDDEN[dtype])
+    ref.close(got, y, ref.rounded(y, err, F32), "moe of shared experts")
+
+
 # ------------------------------------------- plans from offsets: 66 experts ----
 
 def taken(offsets, P):

@@ -50,8 +50,7 @@ MOE = dict(x=P, ids=P, weights=P, Wg=P, sg=P, Wu=P, su=P, Wd=P, sd=P, residual=N
     (swq.swiglu_q_mx4_linear, LINEAR, dict(M=2, N=1 << 30, type=2, out_mode=2)),
     (swq.swiglu_q_mx4_linear, LINEAR, dict(M=1 << 30, N=8, type=2, out_mode=2)),      # 64 rows a block of 256
     (swq.swiglu_q_mx4_grouped_linear, GROUPED, dict(P=4096, E=1024, N=1 << 20)),
-    (swq.swiglu_q_moe_mlp, MOE, dict(T=6, k=64, I=1 << 20)),                  # hidden columns, slot by slot
-    (swq.swiglu_q_moe_mlp, MOE, dict(T=6, k=2, Ho=1 << 26)),                  # outputs of the same
+    (swq.swiglu_q_moe_mlp, MOE, dict(T=1, k=2, Ho=1 << 26)),                  # slot by slot: outputs
     (swq.swiglu_q_moe_mlp, MOE, dict(T=64, k=64, E=1024, I=1 << 20)),         # by expert
 ])
 def test_more_threads_than_a_launch(fn, base, kw):
