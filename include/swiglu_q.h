@@ -292,7 +292,8 @@ int swiglu_q_mx4_dequantize(const uint32_t *codes, const void *scales, int64_t R
  * (type SWQ_TYPE_BF16 or SWQ_TYPE_F16), residual [M, N] or NULL, out [M, N] in x's
  * type (out_mode = type) or float32 (SWQ_LINEAR_F32).  Exact products, float32
  * sums, the residual added before the one rounding.  A result past float32's
- * range is an infinity; a NaN scale makes its row's column NaN.
+ * range is an infinity, and so is a weight (codes from 4 on at scale bytes 253 and 254, which
+ * the quantizer never writes): times a zero of x it gives NaN.  A NaN scale makes its row's column NaN.
  */
 int swiglu_q_mx4_linear(const void *x, const uint32_t *W, const void *s, const void *residual,
                         int64_t M, int64_t K, int64_t N, int type, int out_mode,

@@ -53,7 +53,7 @@ int check_shape(int64_t rows, int64_t K, int64_t N) {
   return SWQ_OK;
 }
 
-// 16-byte aligned codes, the weights' rows per expert below 2^31.
+// A matrix of codes and scales: both there, the codes 16-byte aligned.
 int check_codes(const uint32_t* W, const void* s) {
   if (!W || !s) return SWQ_ERR_NULL;
   return aligned(W, 16) ? SWQ_OK : SWQ_ERR_ALIGN;
@@ -314,7 +314,12 @@ int swiglu_q_moe_mlp(const void* x, const int32_t* ids, const float* weights, co
   g.hidden_planes = f16;
   g.xrows = (int)T;
   g.vec = 2;
-  // few tokens: every slot on its own, no plan, the weighted sum in the down
+  // The hidden tensor is rounded to x's precision where it leaves the registers: bf16 x to bf16, as the dense
+  // MLP's (swiglu_q_mlp), binary16 x to two bf16 planes, 16 bits.  Against the same formulas in 64 bits bf16
+  // outputs are off by 0.0019 to 0.0022 of their norm where an unrounded hidden tensor gives 0.0017, the output's own
+  // rounding; two planes for bf16 x too would double the down projection's products (4096 tokens, 8 of 64
+  // experts, 2048 x 1024: 2 x 153 us in place of 2 x 105, of 517 in all).
+  // Few tokens: every slot on its own, no plan, the weighted sum in the down
   // projection.  Else by expert: the workspace holds the plan, the hidden
   // tensor in the plan's order (two planes for binary16), the experts' outputs
   // in the slots' order, and x as planes.

@@ -570,7 +570,7 @@ __global__ __launch_bounds__(64 * W) void mx4_down_kernel(MxGemm p, const float*
 // 1.13 PFLOP/s.  32768 rows of 64 experts: gate and up 2048 x 1024 303 us, 0.91 PFLOP/s, down 2 x 99 us, 0.70: a ninth
 // of the tiles' rows is past the experts' ends, the last round of tiles leaves CUs idle, and the
 // down projection's short K ends in 128 KB of float32 per tile.  Float16 x, two operands: 2048 x
-// 4096 x 14336 463 us, 1.04 PFLOP/s of bf16 products.
+// 4096 x 14336 421 to 463 us, 1.04 to 1.14 PFLOP/s of bf16 products.
 template <int MF, int NF, int WM, int WN, int NP, int S, bool FUSED, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_gemm_kernel(MxGemm p) {
   constexpr int W = WM * WN, BM = 16 * MF * WM, ROWS = BM * NP, BN = 16 * NF * WN, BNO = FUSED ? BN / 2 : BN;
@@ -851,9 +851,10 @@ __device__ __forceinline__ void store_wide(const Mx4Matmul& p, const f32x16 (&ac
 // the rows that a read touches lie in different banks (no conflict cycles counted).  As many blocks as
 // the CUs hold take the tiles in turn, and a block's next loads go out before its stores.
 //
-// 8192 x 2560 x 10240: 131 us, 3.3 PFLOP/s, 168 MB of outputs; matrix units 44 % busy.  The 20
-// stages of a tile are bound by what a CU takes from its L2 (32 KB a stage), and the outputs,
-// 32 us of the memory's time, overlap only in part.
+// 8192 x 2560 x 10240: 131 to 134 us, 3.3 PFLOP/s, 168 MB of outputs; matrix units 45 % busy.  What bounds it was not
+// found: its reads from L2 (13.1 M requests of 64 bytes, 840 MB, 86 % of all requests hit) come to 6.4 TB/s, less than
+// the 8.3 that the product of bf16 rows takes, and waves wait 46 % of their cycles; the outputs, 32 us of the
+// memory's time, overlap only in part.
 template <int AF, int WF, int WM, int WN, int S>
 struct MmShape {
   static constexpr int W = WM * WN, BM = 32 * AF * WM, BN = 32 * WF * WN, ROWS = BM + BN;
@@ -1300,8 +1301,7 @@ static hipError_t launch_matmul_as(const Mx4Matmul& p, const uint16_t* ws, int s
 //   256 x 256   149   77   27     eight waves; the others four, and two blocks a CU
 //   128 x 128   197   90   16
 //    64 x  64   299  140    8.9   seven stages deep
-// (a CU takes about 10 TB/s / 256 from its L2, so the larger tile's fewer bytes count;
-// 128 x 256 took 179, 87 and 23).  256 x 256 where it gives three fifths of the CUs a tile, 128 x 128
+// (the larger tile reads fewer bytes from L2; 128 x 256 took 179, 87 and 23).  256 x 256 where it gives three fifths of the CUs a tile, 128 x 128
 // where it gives half of them one, else 64 x 64.
 static const MatmulConfig kMatmul[] = {
     {256, 256, launch_matmul_as<4, 2, 2, 4, 4, 1>},
