@@ -345,6 +345,107 @@ int swiglu_q_moe_mlp(const void *x, const int32_t *ids, const float *weights,
                      int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int64_t Ho,
                      int type, int out_mode, void *out, void *stream);
 
+/*
+ * ---- Products with 16-bit weights, and training ---------------------------------
+ *
+ * What of such a layer is not quantised, forward and backward: a projection with bias,
+ * activation and residual (the router's logits are one), 8-bit activation
+ * checkpoints and what the backward pass makes of them, the router's balance loss and
+ * the gradient of its logits.  As above: device pointers, contiguous
+ * row-major, work enqueued on `stream`, arguments checked on the host before any
+ * HIP call, nothing launched on error, deterministic results, every output element
+ * written, no clearing needed between graph replays.  Sizes are any (no multiples):
+ * rows up to 2^30, inputs and outputs up to 2^20.  x, W and dout of the products need 16-byte
+ * alignment, checkpoints none, everything else its element size.  The products and the
+ * balance loss take a workspace of the (device, stream), with the rules for graphs and
+ * concurrent calls given at the top.
+ *
+ * A checkpoint of a tensor [R, K] is int8 codes q [R, K] and one e8m0 byte b per 32
+ * neighbours of a row, scales uint8 [R, ceil(K / 32)] (a row's last block may be
+ * shorter): the value is q 2^(b - 133), 255 = NaN (the Open Compute Project's MXINT8:
+ * codes of six fraction bits times 2^(b - 127)).  A block's step is the smallest power of two, from 2^-126
+ * on, at which no code passes 127, so a value is off by at most half a step, 1/127 of the
+ * block's largest magnitude; ties to even; a block with an infinity or a NaN gets the NaN scale and zero
+ * codes.
+ */
+
+/* Activations. */
+#define SWQ_ACT_NONE       0
+#define SWQ_ACT_RELU       1
+#define SWQ_ACT_SILU       2  /* z sigma(z)                                              */
+#define SWQ_ACT_GELU       3  /* z (1 + erf(z / sqrt 2)) / 2                             */
+#define SWQ_ACT_GELU_TANH  4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2       */
+
+/* x [R, K] (bf16, float32 or binary16 by `type`) to a checkpoint, and the values [R, K]
+ * of one in `type` (one rounding; exact in bf16 and float32). */
+int swiglu_q_mx8_quantize(const void *x, int64_t R, int64_t K, int type, void *codes, void *scales, void *stream);
+int swiglu_q_mx8_dequantize(const void *codes, const void *scales, int64_t R, int64_t K, int type, void *out,
+                            void *stream);
+
+/*
+ * out = act(z) + residual with z = x W^T + bias: x [M, K], W [N, K], bias [N] or NULL,
+ * residual [M, N] or NULL, all bf16 or all binary16 by `type`; out [M, N] in that type
+ * (out_mode = type) or float32 (SWQ_LINEAR_F32).  Exact products, float32
+ * sums, bias, activation and residual in float32, one rounding.
+ * z NULL, or what the backward pass needs: z [M, N] in x's type, or with z_scales a
+ * checkpoint (z its codes), each made from the float32 sums.  M == 0 returns SWQ_OK with nothing launched.
+ */
+int swiglu_q_dense_linear(const void *x, const void *W, const void *bias, const void *residual, int64_t M, int64_t K,
+                          int64_t N, int type, int act, int out_mode, void *out, void *z, void *z_scales,
+                          void *stream);
+
+/*
+ * Its gradients: dz = dout act'(z); dx [M, K] = dz W; dW [N, K] = dz^T x; dbias [N] = sum_m dz,
+ * each NULL where not wanted (not all three); the residual's gradient is dout itself.
+ * dout [M, N], W and the gradients in `type`; x (needed for dW) and z (needed unless act is
+ * SWQ_ACT_NONE) in `type`, or checkpoints where their scales are not NULL (x, z the codes).  act'(0) of
+ * SWQ_ACT_RELU is 0.  dz is float32, rounded to `type` for the products (dbias sums it unrounded); float32
+ * sums, one rounding.  M == 0 writes dW and dbias as zeros.
+ */
+int swiglu_q_dense_linear_backward(const void *dout, const void *x, const void *x_scales, const void *W, const void *z,
+                                   const void *z_scales, int64_t M, int64_t K, int64_t N, int type, int act, void *dx,
+                                   void *dW, void *dbias, void *stream);
+
+/*
+ * hidden = silu(gate) up for gate and up [R, K] (bf16 or binary16), in float32 with one rounding;
+ * with the four checkpoint pointers (all or none) gate and up as checkpoints too.
+ */
+int swiglu_q_swiglu(const void *gate, const void *up, int64_t R, int64_t K, int type, void *hidden, void *gate_codes,
+                    void *gate_scales, void *up_codes, void *up_scales, void *stream);
+
+/*
+ * Its gradients: dgate = dhidden up silu'(gate), dup = dhidden silu(gate), and with hidden not NULL
+ * the hidden tensor again (the down projection's dW needs it).  gate and up in `type`, or
+ * checkpoints where their scales are not NULL.
+ */
+int swiglu_q_swiglu_backward(const void *dhidden, const void *gate, const void *gate_scales, const void *up,
+                             const void *up_scales, int64_t R, int64_t K, int type, void *dgate, void *dup,
+                             void *hidden, void *stream);
+
+/*
+ * The router's balance loss: with logits [T, E] and ids [T, k] as swiglu_q_route takes and gives them,
+ * c_e the slots whose id is e, N their sum, T' the tokens with a slot, p_te the softmax over a
+ * token's experts (SWQ_ROUTE_SIGMOID*: sigma_te / sum_e sigma_te) and P_e the mean of p_te over these tokens,
+ *   loss [1] = E sum_e (c_e / N) P_e    (1 where all experts are alike; 0 without a slot)
+ * counts int32 [E] = c_e; slopes float32 [E] = E c_e / (N T'), the loss's derivative by p_te, for
+ * swiglu_q_route_backward.  Ids outside [0, E) are no slots, an expert whose logit is -inf
+ * or NaN has p = 0.  T k below 2^31.  T == 0 writes zeros.
+ */
+int swiglu_q_balance_loss(const void *logits, const int32_t *ids, int64_t T, int64_t E, int k, int type, int scoring,
+                          float *loss, int32_t *counts, float *slopes, void *stream);
+
+/*
+ * The gradient dlogits [T, E] (in the logits' type) of the routing weights that swiglu_q_route
+ * gave for ids, dweights float32 [T, k] (NULL: none), and of the balance loss, slopes as
+ * swiglu_q_balance_loss left them (NULL: none) times *dloss, a float32 on the device (NULL: 1).
+ * The choice of the experts and the counts are constants.  A slot whose id is outside [0, E) adds nothing (its
+ * dweights entry is not read as a number), an expert whose logit is -inf or NaN gets 0, and so does
+ * a token without a slot.  The same id in two slots counts as two slots.
+ */
+int swiglu_q_route_backward(const void *logits, const int32_t *ids, const float *dweights, const float *slopes,
+                            const float *dloss, int64_t T, int64_t E, int k, int type, int scoring, void *dlogits,
+                            void *stream);
+
 /* 1 if the combination is supported by swiglu_q_forward, else 0 (mirrors the
  * pages' support predicate, restricted to what this library implements). */
 int swiglu_q_supported(int64_t H, int bits_g, int gs_g, int bits_u, int gs_u,

@@ -26,6 +26,7 @@ SWQ_LINEAR_BF16, SWQ_LINEAR_F32, SWQ_LINEAR_F16 = 0, 1, 2
 SWQ_TYPE_BF16, SWQ_TYPE_F32, SWQ_TYPE_F16 = 0, 1, 2
 SWQ_ROUTE_SOFTMAX, SWQ_ROUTE_SOFTMAX_CHOSEN, SWQ_ROUTE_SIGMOID, SWQ_ROUTE_SIGMOID_CHOSEN = range(4)
 SWQ_MAX_EXPERTS, SWQ_MAX_CHOSEN = 1024, 64
+SWQ_ACT_NONE, SWQ_ACT_RELU, SWQ_ACT_SILU, SWQ_ACT_GELU, SWQ_ACT_GELU_TANH = range(5)
 
 _lib = None
 
@@ -80,6 +81,22 @@ def load_library(path):
     L.swiglu_q_route.restype = i32
     L.swiglu_q_moe_mlp.argtypes = [vp] * 10 + [i64] * 6 + [i32, i32, vp, vp]
     L.swiglu_q_moe_mlp.restype = i32
+    L.swiglu_q_mx8_quantize.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    L.swiglu_q_mx8_quantize.restype = i32
+    L.swiglu_q_mx8_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+    L.swiglu_q_mx8_dequantize.restype = i32
+    L.swiglu_q_dense_linear.argtypes = [vp] * 4 + [i64, i64, i64, i32, i32, i32, vp, vp, vp, vp]
+    L.swiglu_q_dense_linear.restype = i32
+    L.swiglu_q_dense_linear_backward.argtypes = [vp] * 6 + [i64, i64, i64, i32, i32, vp, vp, vp, vp]
+    L.swiglu_q_dense_linear_backward.restype = i32
+    L.swiglu_q_swiglu.argtypes = [vp, vp, i64, i64, i32] + [vp] * 6
+    L.swiglu_q_swiglu.restype = i32
+    L.swiglu_q_swiglu_backward.argtypes = [vp] * 5 + [i64, i64, i32] + [vp] * 4
+    L.swiglu_q_swiglu_backward.restype = i32
+    L.swiglu_q_balance_loss.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, vp, vp, vp]
+    L.swiglu_q_balance_loss.restype = i32
+    L.swiglu_q_route_backward.argtypes = [vp] * 5 + [i64, i64, i32, i32, i32, vp, vp]
+    L.swiglu_q_route_backward.restype = i32
     L.swiglu_q_supported.argtypes = [i64, i32, i32, i32, i32, i32]
     L.swiglu_q_supported.restype = i32
     L.swiglu_q_set_m_threshold.argtypes = [i32]
@@ -193,6 +210,48 @@ def swiglu_q_moe_mlp(x, ids, weights, Wg, sg, Wu, su, Wd, sd, residual, T, k, E,
     return lib().swiglu_q_moe_mlp(_ptr(x), _ptr(ids), _ptr(weights), _ptr(Wg), _ptr(sg), _ptr(Wu), _ptr(su), _ptr(Wd),
                                   _ptr(sd), _ptr(residual), T, k, E, H, I, Ho, type, out_mode, _ptr(out),
                                   _stream(stream))
+
+
+def swiglu_q_mx8_quantize(x, R, K, type, codes, scales, stream=None) -> int:
+    return lib().swiglu_q_mx8_quantize(_ptr(x), R, K, type, _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def swiglu_q_mx8_dequantize(codes, scales, R, K, type, out, stream=None) -> int:
+    return lib().swiglu_q_mx8_dequantize(_ptr(codes), _ptr(scales), R, K, type, _ptr(out), _stream(stream))
+
+
+def swiglu_q_dense_linear(x, W, bias, residual, M, K, N, type, act, out_mode, out, z=None, z_scales=None,
+                          stream=None) -> int:
+    return lib().swiglu_q_dense_linear(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), M, K, N, type, act, out_mode,
+                                       _ptr(out), _ptr(z), _ptr(z_scales), _stream(stream))
+
+
+def swiglu_q_dense_linear_backward(dout, x, x_scales, W, z, z_scales, M, K, N, type, act, dx, dW, dbias,
+                                   stream=None) -> int:
+    return lib().swiglu_q_dense_linear_backward(_ptr(dout), _ptr(x), _ptr(x_scales), _ptr(W), _ptr(z), _ptr(z_scales),
+                                                M, K, N, type, act, _ptr(dx), _ptr(dW), _ptr(dbias), _stream(stream))
+
+
+def swiglu_q_swiglu(gate, up, R, K, type, hidden, gate_codes=None, gate_scales=None, up_codes=None, up_scales=None,
+                    stream=None) -> int:
+    return lib().swiglu_q_swiglu(_ptr(gate), _ptr(up), R, K, type, _ptr(hidden), _ptr(gate_codes), _ptr(gate_scales),
+                                 _ptr(up_codes), _ptr(up_scales), _stream(stream))
+
+
+def swiglu_q_swiglu_backward(dhidden, gate, gate_scales, up, up_scales, R, K, type, dgate, dup, hidden=None,
+                             stream=None) -> int:
+    return lib().swiglu_q_swiglu_backward(_ptr(dhidden), _ptr(gate), _ptr(gate_scales), _ptr(up), _ptr(up_scales), R, K,
+                                          type, _ptr(dgate), _ptr(dup), _ptr(hidden), _stream(stream))
+
+
+def swiglu_q_balance_loss(logits, ids, T, E, k, type, scoring, loss, counts, slopes, stream=None) -> int:
+    return lib().swiglu_q_balance_loss(_ptr(logits), _ptr(ids), T, E, k, type, scoring, _ptr(loss), _ptr(counts),
+                                       _ptr(slopes), _stream(stream))
+
+
+def swiglu_q_route_backward(logits, ids, dweights, slopes, dloss, T, E, k, type, scoring, dlogits, stream=None) -> int:
+    return lib().swiglu_q_route_backward(_ptr(logits), _ptr(ids), _ptr(dweights), _ptr(slopes), _ptr(dloss), T, E, k,
+                                         type, scoring, _ptr(dlogits), _stream(stream))
 
 
 def swiglu_q_path_for(M, H, I) -> int:
@@ -360,16 +419,16 @@ def mlp(x, wg, sg, bg, wu, su, bu, wd, sd, bd, spec_g, spec_u, spec_d, residual=
 _types = {}      # torch type -> SWQ_TYPE_*; the rest is set with it
 _dtypes = ()     # SWQ_TYPE_* -> torch type
 _words = ()      # types of codes
-_bytes = _int32 = _float32 = None
+_bytes = _int8 = _int32 = _float32 = None
 _raw_stream = _device_now = _on_device = None   # torch's current stream of a GPU, current GPU, GPU guard
 
 
 def _load_types():
-    global _types, _dtypes, _words, _bytes, _int32, _float32, _raw_stream, _device_now, _on_device
+    global _types, _dtypes, _words, _bytes, _int8, _int32, _float32, _raw_stream, _device_now, _on_device
     import torch
     _dtypes = (torch.bfloat16, torch.float32, torch.float16)
     _words = (torch.int32, torch.uint32)
-    _bytes, _int32, _float32 = torch.uint8, torch.int32, torch.float32
+    _bytes, _int8, _int32, _float32 = torch.uint8, torch.int8, torch.int32, torch.float32
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -597,6 +656,240 @@ def moe_mlp(x, ids, weights, wg, sg, wu, su, wd, sd, residual=None, out_mode=Non
               wg.data_ptr(), sg.data_ptr(), wu.data_ptr(), su.data_ptr(), wd.data_ptr(), sd.data_ptr(), res, n // H,
               ids.shape[-1], E, H, I, Ho, t, mode, out.data_ptr())
     return out
+
+
+# ---- products with 16-bit weights, and training ---------------------------------
+#
+# Rules as above.  A checkpoint is a pair (codes int8 [..., K], scales uint8
+# [..., ceil(K / 32)]), as mx8_quantize returns it.
+
+def _mx8(kept, what):
+    """The codes and scales of a checkpoint."""
+    _types or _load_types()
+    codes, scales = kept
+    if codes.dtype is not _int8 or scales.dtype is not _bytes:
+        raise TypeError(f"{what}: a checkpoint is int8 codes and uint8 scales")
+    c, s = codes.shape, scales.shape
+    if len(c) < 1 or len(s) != len(c) or c[:-1] != s[:-1] or s[-1] != (c[-1] + 31) // 32:
+        raise ValueError(f"{what}: codes {tuple(c)} and scales {tuple(s)} are not one checkpoint")
+    return codes, scales
+
+
+def _kept(kept, t, shape, what):
+    """(data, scales or None) of a tensor of type number t or a checkpoint, of the given shape."""
+    if isinstance(kept, (tuple, list)):
+        data, scales = _mx8(kept, what)
+    else:
+        data, scales = kept, None
+        if data.dtype is not _dtypes[t]:
+            raise TypeError(f"{what}: must be {_dtypes[t]} or a checkpoint")
+    if data.shape != shape:
+        raise ValueError(f"{what}: must have shape {tuple(shape)}")
+    return data, scales
+
+
+def mx8_quantize(x, codes=None, scales=None, stream=None):
+    """The 8-bit checkpoint (codes int8 [..., K], scales uint8 [..., ceil(K / 32)]) of x
+    [..., K] (bf16, float16 or float32; any K from 1 on)."""
+    t = _type(x, "mx8_quantize")
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] == 0:
+        raise ValueError("mx8_quantize: the last dimension must not be empty")
+    dev = _same_place("mx8_quantize", x)
+    K, n, lead = shape[-1], x.numel(), shape[:-1]
+    codes = x.new_empty(shape, dtype=_int8) if codes is None else _out(codes, shape, _int8, x, "mx8_quantize codes")
+    each = lead + ((K + 31) // 32,)
+    scales = (x.new_empty(each, dtype=_bytes) if scales is None
+              else _out(scales, each, _bytes, x, "mx8_quantize scales"))
+    if n:
+        _call((_lib or lib()).swiglu_q_mx8_quantize, dev, stream, x.data_ptr(), n // K, K, t, codes.data_ptr(),
+              scales.data_ptr())
+    return codes, scales
+
+
+def mx8_dequantize(codes, scales, dtype=None, out=None, stream=None):
+    """The values [..., K] of a checkpoint, in bf16 (default), float16 or float32."""
+    _mx8((codes, scales), "mx8_dequantize")
+    dtype = _dtypes[0] if dtype is None else dtype
+    dev = _same_place("mx8_dequantize", codes, scales)
+    shape, n = codes.shape, codes.numel()
+    out = codes.new_empty(shape, dtype=dtype) if out is None else _out(out, shape, dtype, codes, "mx8_dequantize")
+    t = _type(out, "mx8_dequantize")
+    if n:
+        _call((_lib or lib()).swiglu_q_mx8_dequantize, dev, stream, codes.data_ptr(), scales.data_ptr(),
+              n // shape[-1], shape[-1], t, out.data_ptr())
+    return out
+
+
+def dense_linear(x, w, bias=None, act=SWQ_ACT_NONE, residual=None, keep=None, out_mode=None, out=None, stream=None):
+    """``act(z) + residual``, ``z = x W^T + bias``, for x [..., K], W [N, K], bias [N] and residual
+    [..., N], all bf16 or all float16.  Returns ``out`` [..., N] in x's type, or float32 with SWQ_LINEAR_F32; with
+    keep the pair (out, z), z for ``dense_linear_backward``: keep="same" in x's type, keep="mx8" as
+    a checkpoint (codes, scales)."""
+    t = _type(x, "dense_linear", wide=False)
+    if len(w.shape) != 2 or w.dtype != x.dtype or len(x.shape) < 1 or w.shape[1] != x.shape[-1]:
+        raise ValueError(f"dense_linear: w must be {x.dtype} [N, K] with x's K")
+    N, K = w.shape
+    if K == 0 or N == 0:
+        raise ValueError("dense_linear: a product needs inputs and outputs (K = 0 or N = 0)")
+    if bias is not None and (bias.dtype != x.dtype or bias.shape != (N,)):
+        raise ValueError(f"dense_linear: bias must be {x.dtype} [{N}]")
+    mode = _out_mode(out_mode, t, "dense_linear")
+    lead = x.shape[:-1]
+    shape = lead + (N,)
+    res = _residual(residual, x, shape, "dense_linear")
+    dev = _same_place("dense_linear", x, w, bias, residual)
+    out = x.new_empty(shape, dtype=_dtypes[mode]) if out is None else _out(out, shape, _dtypes[mode], x, "dense_linear")
+    z = scales = None
+    if keep == "same":
+        kept = z = x.new_empty(shape)
+    elif keep == "mx8":
+        kept = z, scales = x.new_empty(shape, dtype=_int8), x.new_empty(lead + ((N + 31) // 32,), dtype=_bytes)
+    elif keep is not None:
+        raise ValueError('dense_linear: keep must be None, "same" or "mx8"')
+    n = x.numel()
+    if n:
+        _call((_lib or lib()).swiglu_q_dense_linear, dev, stream, x.data_ptr(), w.data_ptr(),
+              None if bias is None else bias.data_ptr(), res, n // K, K, N, t, act, mode, out.data_ptr(),
+              None if z is None else z.data_ptr(), None if scales is None else scales.data_ptr())
+    return out if keep is None else (out, kept)
+
+
+def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True, True), dx=None, dw=None, dbias=None,
+                          stream=None):
+    """(dx [..., K], dw [N, K], dbias [N]) of ``dense_linear`` for dout [..., N], in dout's type (bf16 or
+    float16); None where want says False.  x and z (not needed with SWQ_ACT_NONE) are tensors of
+    that type or checkpoints (codes, scales).  The residual's gradient is dout itself."""
+    t = _type(dout, "dense_linear_backward", wide=False)
+    if len(w.shape) != 2 or w.dtype != dout.dtype or len(dout.shape) < 1 or w.shape[0] != dout.shape[-1]:
+        raise ValueError(f"dense_linear_backward: w must be {dout.dtype} [N, K] with dout's N")
+    N, K = w.shape
+    if K == 0 or N == 0:
+        raise ValueError("dense_linear_backward: a product needs inputs and outputs (K = 0 or N = 0)")
+    want_x, want_w, want_b = want
+    lead = dout.shape[:-1]
+    x, xs = _kept(x, t, lead + (K,), "dense_linear_backward x")
+    zs = None
+    if z is not None:
+        z, zs = _kept(z, t, dout.shape, "dense_linear_backward z")
+    elif act != SWQ_ACT_NONE:
+        raise ValueError("dense_linear_backward: an activation's gradient needs z")
+    dev = _same_place("dense_linear_backward", dout, x, xs, w, z, zs)
+    dtype = dout.dtype
+    if not want_x:
+        dx = None
+    else:
+        dx = (dout.new_empty(lead + (K,)) if dx is None
+              else _out(dx, lead + (K,), dtype, dout, "dense_linear_backward dx"))
+    if not want_w:
+        dw = None
+    else:
+        dw = dout.new_empty((N, K)) if dw is None else _out(dw, (N, K), dtype, dout, "dense_linear_backward dw")
+    if not want_b:
+        dbias = None
+    else:
+        dbias = dout.new_empty((N,)) if dbias is None else _out(dbias, (N,), dtype, dout, "dense_linear_backward dbias")
+    if want_x or want_w or want_b:
+        n = dout.numel()
+        # (with no rows the gradients of W and the bias are zeros; empty tensors have no address)
+        at = [None if q is None else q.data_ptr() for q in (xs, z, zs, dx, dw, dbias)]
+        if n:
+            _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, dout.data_ptr(), x.data_ptr(), at[0],
+                  w.data_ptr(), at[1], at[2], n // N, K, N, t, act, *at[3:])
+        elif want_w or want_b:
+            full = w.data_ptr()
+            _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, full, full, None, full, full, None, 0, K,
+                  N, t, act, None, *at[4:])
+    return dx, dw, dbias
+
+
+def swiglu(gate, up, keep=False, hidden=None, stream=None):
+    """``silu(gate) * up`` for gate and up [..., K] (bf16 or float16).  With keep the triple (hidden, gate,
+    up), gate and up as checkpoints for ``swiglu_backward``."""
+    t = _type(gate, "swiglu", wide=False)
+    shape = gate.shape
+    if up.dtype != gate.dtype or up.shape != shape or len(shape) < 1 or shape[-1] == 0:
+        raise ValueError("swiglu: gate and up must be of one type and shape [..., K], K from 1 on")
+    dev = _same_place("swiglu", gate, up)
+    hidden = gate.new_empty(shape) if hidden is None else _out(hidden, shape, gate.dtype, gate, "swiglu hidden")
+    K, n = shape[-1], gate.numel()
+    at = (None,) * 4
+    if keep:
+        each = shape[:-1] + ((K + 31) // 32,)
+        kept = [gate.new_empty(s, dtype=d) for s, d in ((shape, _int8), (each, _bytes)) * 2]
+        at = [q.data_ptr() for q in kept]
+    if n:
+        _call((_lib or lib()).swiglu_q_swiglu, dev, stream, gate.data_ptr(), up.data_ptr(), n // K, K, t,
+              hidden.data_ptr(), *at)
+    return (hidden, (kept[0], kept[1]), (kept[2], kept[3])) if keep else hidden
+
+
+def swiglu_backward(dhidden, gate, up, hidden=False, stream=None):
+    """(dgate, dup) of ``swiglu`` for dhidden [..., K] (bf16 or float16), with hidden=True the triple (dgate, dup,
+    hidden), the forward call's result again.  gate and up are tensors of that type or checkpoints."""
+    t = _type(dhidden, "swiglu_backward", wide=False)
+    shape = dhidden.shape
+    if len(shape) < 1 or shape[-1] == 0:
+        raise ValueError("swiglu_backward: dhidden must be [..., K], K from 1 on")
+    gate, gs = _kept(gate, t, shape, "swiglu_backward gate")
+    up, us = _kept(up, t, shape, "swiglu_backward up")
+    dev = _same_place("swiglu_backward", dhidden, gate, gs, up, us)
+    outs = [dhidden.new_empty(shape) for _ in range(3 if hidden else 2)]
+    K, n = shape[-1], dhidden.numel()
+    if n:
+        _call((_lib or lib()).swiglu_q_swiglu_backward, dev, stream, dhidden.data_ptr(), gate.data_ptr(),
+              None if gs is None else gs.data_ptr(), up.data_ptr(), None if us is None else us.data_ptr(), n // K, K, t,
+              outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr() if hidden else None)
+    return tuple(outs)
+
+
+def _slots(logits, ids, what):
+    """(T, E, k) of logits [..., E] and ids [..., k]."""
+    if len(logits.shape) < 1 or ids.dtype != _int32 or len(ids.shape) < 1 or ids.shape[:-1] != logits.shape[:-1]:
+        raise ValueError(f"{what}: ids must be int32 [..., k] with the logits' leading shape")
+    E, k = logits.shape[-1], ids.shape[-1]
+    return logits.shape[:-1].numel(), E, k
+
+
+def balance_loss(logits, ids, scoring=SWQ_ROUTE_SOFTMAX, stream=None):
+    """(loss float32 [], counts int32 [E], slopes float32 [E]) of a router's choice: logits [..., E] and
+    ``route``'s ids [..., k].  The loss is ``E sum_e f_e P_e``, f_e the expert's share of the slots, P_e its mean
+    probability over the tokens with a slot; counts are the experts' slots, slopes go to ``route_backward``."""
+    t = _type(logits, "balance_loss")
+    T, E, k = _slots(logits, ids, "balance_loss")
+    dev = _same_place("balance_loss", logits, ids)
+    loss = logits.new_empty((), dtype=_float32)
+    counts, slopes = logits.new_empty((E,), dtype=_int32), logits.new_empty((E,), dtype=_float32)
+    at = loss.data_ptr()
+    _call((_lib or lib()).swiglu_q_balance_loss, dev, stream, logits.data_ptr() if T else at,
+          ids.data_ptr() if T else at, T, E, k, t, scoring, at, counts.data_ptr(), slopes.data_ptr())
+    return loss, counts, slopes
+
+
+def route_backward(logits, ids, dweights=None, scoring=SWQ_ROUTE_SOFTMAX, slopes=None, dloss=None, dlogits=None,
+                   stream=None):
+    """dlogits [..., E] in the logits' type: the gradient of ``route``'s weights for ids, given theirs (dweights
+    float32 [..., k]), and of ``balance_loss``, given its slopes and its own gradient dloss (float32, one
+    value on the GPU; None: 1).  Either may be left out, not both."""
+    t = _type(logits, "route_backward")
+    T, E, k = _slots(logits, ids, "route_backward")
+    if dweights is None and slopes is None:
+        raise ValueError("route_backward: needs dweights or slopes")
+    if dweights is not None and (dweights.dtype != _float32 or dweights.shape != ids.shape):
+        raise ValueError("route_backward: dweights must be float32 of ids' shape")
+    if slopes is not None and (slopes.dtype != _float32 or slopes.shape != (E,)):
+        raise ValueError(f"route_backward: slopes must be float32 [{E}]")
+    if dloss is not None and (slopes is None or dloss.dtype != _float32 or dloss.numel() != 1):
+        raise ValueError("route_backward: dloss must be one float32 beside slopes")
+    dev = _same_place("route_backward", logits, ids, dweights, slopes, dloss)
+    shape = logits.shape
+    dlogits = (logits.new_empty(shape) if dlogits is None
+               else _out(dlogits, shape, logits.dtype, logits, "route_backward dlogits"))
+    if T and E:
+        _call((_lib or lib()).swiglu_q_route_backward, dev, stream, logits.data_ptr(), ids.data_ptr(),
+              None if dweights is None else dweights.data_ptr(), None if slopes is None else slopes.data_ptr(),
+              None if dloss is None else dloss.data_ptr(), T, E, k, t, scoring, dlogits.data_ptr())
+    return dlogits
 
 
 def debug_gemm_tensors(x, wg, sg, bg, wu, su, bu, bits_g, gs_g, bits_u=None, gs_u=None,

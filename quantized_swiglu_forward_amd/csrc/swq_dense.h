@@ -1,0 +1,68 @@
+// Internal interface between the host code and the kernels of the products
+// with 16-bit weights, the 8-bit activation checkpoints, the SwiGLU with
+// checkpoints and the router's loss and gradient.
+#pragma once
+
+#include "swq_mx4.h"
+
+namespace swq {
+
+// Activations of a product's epilogue (values fixed by the public header).
+enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+// How the inner index r of an operand runs: along its rows (element p of row ...
+// at p * ld + r) or down its columns (r * ld + p).
+enum : int { kAlong = 0, kDown = 1 };
+
+// out[p, q] = act(sum_r a(p, r) b(q, r) + bias[q]) + res[p, q]; the argument of act also to
+// z (in the operands' type, or with z_scales as an 8-bit checkpoint).  p < P, q < Q, r < R.
+struct DenseGemm {
+  const uint16_t* a;
+  const uint16_t* b;
+  int64_t lda, ldb;
+  int way_a, way_b;         // kAlong, kDown
+  int64_t P, Q, R;
+  int type;                 // the operands', the bias's, the residual's and z's 16-bit type
+  int act;
+  const uint16_t* bias;     // [Q] or null
+  const uint16_t* res;      // [P, Q] or null
+  void* out;                // [P, Q]
+  int out_type;
+  void* z;                  // [P, Q] or null
+  uint8_t* z_scales;        // [P, ceil(Q / 32)]: z as a checkpoint; or null
+};
+hipError_t launch_dense_gemm(const DenseGemm& g, hipStream_t st);
+
+// A tensor [R, K] in 16 bits, or with scales as an 8-bit checkpoint (K / 32 scales a row, rounded up).
+struct Kept {
+  const void* data;
+  const uint8_t* scales;
+};
+
+hipError_t launch_mx8_quantize(const void* x, int64_t R, int64_t K, int type, void* codes, uint8_t* scales,
+                               hipStream_t st);
+hipError_t launch_mx8_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int type, void* out,
+                                 hipStream_t st);
+
+// hidden = silu(gate) up, with gate and up as checkpoints where the codes are not null
+hipError_t launch_swiglu(const uint16_t* gate, const uint16_t* up, int64_t R, int64_t K, int type, uint16_t* hidden,
+                         void* gcodes, uint8_t* gscales, void* ucodes, uint8_t* uscales, hipStream_t st);
+hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, int64_t R, int64_t K, int type,
+                                  uint16_t* dgate, uint16_t* dup, uint16_t* hidden, hipStream_t st);
+
+// dz = dout act'(z) (null: not wanted) and its column sums (dbias, null: not wanted) [M, N]; parts: float32
+// [act_parts(M, N)][N].
+int64_t act_parts(int64_t M, int64_t N);
+hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
+                               uint16_t* dbias, float* parts, hipStream_t st);
+hipError_t launch_zero16(uint16_t* p, int64_t n, hipStream_t st);
+
+// The router's balance loss (parts: balance_workspace bytes) and the gradient of its logits.
+int64_t balance_workspace(int64_t T, int E);
+hipError_t launch_balance(const void* logits, const int* ids, int64_t T, int E, int k, int type, int scoring,
+                          float* loss, int* counts, float* slopes, void* parts, hipStream_t st);
+hipError_t launch_route_backward(const void* logits, const int* ids, const float* dweights, const float* slopes,
+                                 const float* dloss, int64_t T, int E, int k, int type, int scoring, void* dlogits,
+                                 hipStream_t st);
+
+}  // namespace swq

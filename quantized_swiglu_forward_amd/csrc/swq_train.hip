@@ -1,0 +1,299 @@
+// 8-bit activation checkpoints, the SwiGLU that leaves them behind and its
+// gradient, and the gradient of a product's activation with the bias's sums.
+#include <algorithm>
+
+#include "swq_dense.h"
+#include "swq_dense_device.h"
+
+namespace swq {
+namespace {
+
+// A tensor [R, K] in pieces of eight neighbours of a row, four pieces to a block of 32 (the last of a row may be
+// shorter, and its pieces empty).  Piece i is piece i % (4 blocks) of row i / (4 blocks).
+struct Pieces {
+  int64_t R, K;
+  uint32_t per_row;         // 4 ceil(K / 32)
+};
+struct Piece {
+  int64_t at;               // its first element
+  int64_t block;            // its block's scale
+  int n;                    // elements, 0 .. 8
+};
+__device__ __forceinline__ Piece piece_of(const Pieces& t, int64_t i) {
+  const int64_t row = i / t.per_row;
+  const uint32_t c = (uint32_t)(i - row * t.per_row);
+  const int64_t left = t.K - 8 * (int64_t)c;
+  return {row * t.K + 8 * (int64_t)c, row * (t.per_row / 4) + (c >> 2), left >= 8 ? 8 : left > 0 ? (int)left : 0};
+}
+
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* x, int64_t at, int n, float* v) {
+  if constexpr (TYPE == kTypeF32) {
+    const uint32_t* f = (const uint32_t*)x + at;
+    if (n == 8) {
+      const u32x4 a = *(const u32x4_any*)f, b = *(const u32x4_any*)(f + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(a[j]), v[4 + j] = __uint_as_float(b[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? __uint_as_float(f[j]) : 0.0f;
+    }
+  } else {
+    const uint16_t* f = (const uint16_t*)x + at;
+    if (n == 8) {
+      const u32x4 a = *(const u32x4_any*)f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = from_16((uint16_t)(a[j >> 1] >> (16 * (j & 1))), TYPE);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? from_16(f[j], TYPE) : 0.0f;
+    }
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store8(void* y, int64_t at, int n, const float* v) {
+  if constexpr (TYPE == kTypeF32) {
+    float* f = (float*)y + at;
+    if (n == 8) {
+      *(u32x4_any*)f = __builtin_bit_cast(u32x4, (f32x4){v[0], v[1], v[2], v[3]});
+      *(u32x4_any*)(f + 4) = __builtin_bit_cast(u32x4, (f32x4){v[4], v[5], v[6], v[7]});
+    } else {
+      for (int j = 0; j < n; ++j) f[j] = v[j];
+    }
+  } else {
+    uint16_t* f = (uint16_t*)y + at;
+    if (n == 8) {
+      *(u32x4_any*)f = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
+                               pack16<TYPE>(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) f[j] = to_16(v[j], TYPE);
+    }
+  }
+}
+
+__device__ __forceinline__ void decode8(const void* codes, float scale, int64_t at, int n, float* v) {
+  const uint8_t* c = (const uint8_t*)codes + at;
+  u32x2 w = {0u, 0u};
+  if (n == 8) {
+    w = *(const u32x2_any*)c;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) w[j >> 2] |= (uint32_t)c[j] << (8 * (j & 3));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = mx8_value(w[j >> 2], j & 3, scale);
+}
+
+// The block's maximum over its four pieces (neighbouring lanes), codes and scale.
+__device__ __forceinline__ void encode8(const float* v, const Piece& p, void* codes, uint8_t* scales) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+  const Mx8Step s = mx8_step(m);
+  int q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = mx8_code(v[j], s);
+  uint8_t* c = (uint8_t*)codes + p.at;
+  const u32x2 w = {pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7])};
+  if (p.n == 8) {
+    *(u32x2_any*)c = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < p.n) c[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+  }
+  if ((threadIdx.x & 3) == 0) scales[p.block] = (uint8_t)s.byte;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void mx8_quantize_kernel(const void* __restrict__ x, Pieces t, int64_t first,
+                                                           int64_t end, void* __restrict__ codes,
+                                                           uint8_t* __restrict__ scales) {
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= end) return;                        // whole blocks leave together
+  const Piece p = piece_of(t, i);
+  float v[8];
+  load8<TYPE>(x, p.at, p.n, v);
+  encode8(v, p, codes, scales);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void mx8_dequantize_kernel(const void* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, Pieces t,
+                                                             int64_t first, int64_t end, void* __restrict__ out) {
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= end) return;
+  const Piece p = piece_of(t, i);
+  float v[8];
+  decode8(codes, mx8_scale(scales[p.block]), p.at, p.n, v);
+  store8<TYPE>(out, p.at, p.n, v);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void swiglu_kernel(const uint16_t* __restrict__ gate,
+                                                     const uint16_t* __restrict__ up, Pieces t, int64_t first,
+                                                     int64_t end, uint16_t* __restrict__ hidden,
+                                                     void* __restrict__ gcodes, uint8_t* __restrict__ gscales,
+                                                     void* __restrict__ ucodes, uint8_t* __restrict__ uscales) {
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= end) return;
+  const Piece p = piece_of(t, i);
+  float g[8], u[8], y[8];
+  load8<TYPE>(gate, p.at, p.n, g);
+  load8<TYPE>(up, p.at, p.n, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = silu_times(g[j], u[j]);
+  store8<TYPE>(hidden, p.at, p.n, y);
+  if (gcodes) {
+    encode8(g, p, gcodes, gscales);
+    encode8(u, p, ucodes, uscales);
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void load_kept(const Kept& x, const Piece& p, float* v) {
+  if (x.scales) decode8(x.data, mx8_scale(x.scales[p.block]), p.at, p.n, v);
+  else load8<TYPE>(x.data, p.at, p.n, v);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void swiglu_backward_kernel(const uint16_t* __restrict__ dhidden, Kept gate, Kept up,
+                                                              Pieces t, int64_t first, int64_t end,
+                                                              uint16_t* __restrict__ dgate, uint16_t* __restrict__ dup,
+                                                              uint16_t* __restrict__ hidden) {
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= end) return;
+  const Piece p = piece_of(t, i);
+  float d[8], g[8], u[8], y[8];
+  load8<TYPE>(dhidden, p.at, p.n, d);
+  load_kept<TYPE>(gate, p, g);
+  load_kept<TYPE>(up, p, u);
+  if (hidden) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = silu_times(g[j], u[j]);
+    store8<TYPE>(hidden, p.at, p.n, y);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float s = sigma(g[j]);
+    u[j] = d[j] * u[j] * (s * fmaf(g[j], 1.0f - s, 1.0f));
+    y[j] = d[j] * (g[j] * s);
+  }
+  store8<TYPE>(dgate, p.at, p.n, u);
+  store8<TYPE>(dup, p.at, p.n, y);
+}
+
+// One launch holds fewer than 2^32 threads (of more the rest is left out, with no error).
+constexpr int64_t kLaunchPieces = int64_t(1) << 30;
+
+template <class F>
+hipError_t over_pieces(int64_t R, int64_t K, F launch) {
+  const Pieces t{R, K, (uint32_t)((K + 31) / 32 * 4)};
+  const int64_t all = R * t.per_row;
+  for (int64_t i = 0; i < all; i += kLaunchPieces) {
+    const int64_t end = std::min(all, i + kLaunchPieces);
+    launch(dim3((unsigned)((end - i + 255) / 256)), t, i, end);
+  }
+  return hipGetLastError();
+}
+
+// dz and the sums of its columns: a thread has one column of a stretch of rows.
+constexpr int64_t kActParts = 64;
+template <int TYPE>
+__global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dout, Kept z, int64_t M,
+                                                           int64_t N, int act, int64_t rows,
+                                                           uint16_t* __restrict__ dz, float* __restrict__ parts) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  const int64_t blocks = (N + 31) / 32;
+  const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(m0 + rows, M);
+  float sum = 0.0f;
+  for (int64_t m = m0; m < m1; ++m) {
+    float d = from_16(dout[m * N + n], TYPE);
+    if (act != kActNone) {
+      const float v = z.scales ? (float)((const int8_t*)z.data)[m * N + n] * mx8_scale(z.scales[m * blocks + n / 32])
+                               : from_16(((const uint16_t*)z.data)[m * N + n], TYPE);
+      d *= activate_slope(v, act);
+    }
+    sum += d;
+    if (dz) dz[m * N + n] = to_16(d, TYPE);
+  }
+  if (parts) parts[(int64_t)blockIdx.y * N + n] = sum;
+}
+template <int TYPE>
+__global__ __launch_bounds__(256) void act_sums_kernel(const float* __restrict__ parts, int64_t n_parts, int64_t N,
+                                                       uint16_t* __restrict__ dbias) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float sum = 0.0f;
+  for (int64_t i = 0; i < n_parts; ++i) sum += parts[i * N + n];
+  dbias[n] = to_16(sum, TYPE);
+}
+
+__global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+}  // namespace
+
+hipError_t launch_mx8_quantize(const void* x, int64_t R, int64_t K, int type, void* codes, uint8_t* scales,
+                               hipStream_t st) {
+  return over_pieces(R, K, [&](dim3 grid, Pieces t, int64_t i, int64_t end) {
+    if (type == kTypeF32) mx8_quantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(x, t, i, end, codes, scales);
+    else if (type == kTypeF16) mx8_quantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(x, t, i, end, codes, scales);
+    else mx8_quantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(x, t, i, end, codes, scales);
+  });
+}
+
+hipError_t launch_mx8_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int type, void* out,
+                                 hipStream_t st) {
+  return over_pieces(R, K, [&](dim3 grid, Pieces t, int64_t i, int64_t end) {
+    if (type == kTypeF32) mx8_dequantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
+    else if (type == kTypeF16) mx8_dequantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
+    else mx8_dequantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
+  });
+}
+
+hipError_t launch_swiglu(const uint16_t* gate, const uint16_t* up, int64_t R, int64_t K, int type, uint16_t* hidden,
+                         void* gcodes, uint8_t* gscales, void* ucodes, uint8_t* uscales, hipStream_t st) {
+  const auto kernel = type == kTypeF16 ? swiglu_kernel<kTypeF16> : swiglu_kernel<kTypeBf16>;
+  return over_pieces(R, K, [&](dim3 grid, Pieces t, int64_t i, int64_t end) {
+    kernel<<<grid, 256, 0, st>>>(gate, up, t, i, end, hidden, gcodes, gscales, ucodes, uscales);
+  });
+}
+
+hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, int64_t R, int64_t K, int type,
+                                  uint16_t* dgate, uint16_t* dup, uint16_t* hidden, hipStream_t st) {
+  const auto kernel = type == kTypeF16 ? swiglu_backward_kernel<kTypeF16> : swiglu_backward_kernel<kTypeBf16>;
+  return over_pieces(R, K, [&](dim3 grid, Pieces t, int64_t i, int64_t end) {
+    kernel<<<grid, 256, 0, st>>>(dhidden, gate, up, t, i, end, dgate, dup, hidden);
+  });
+}
+
+int64_t act_parts(int64_t M, int64_t) { return M < kActParts ? M : kActParts; }
+
+hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
+                               uint16_t* dbias, float* parts, hipStream_t st) {
+  const int64_t rows = (M + act_parts(M, N) - 1) / act_parts(M, N), n_parts = (M + rows - 1) / rows;
+  const dim3 grid((unsigned)((N + 255) / 256), (unsigned)n_parts);
+  const auto kernel = type == kTypeF16 ? act_backward_kernel<kTypeF16> : act_backward_kernel<kTypeBf16>;
+  kernel<<<grid, 256, 0, st>>>(dout, z, M, N, act, rows, dz, dbias ? parts : nullptr);
+  if (dbias) {
+    const auto sums = type == kTypeF16 ? act_sums_kernel<kTypeF16> : act_sums_kernel<kTypeBf16>;
+    sums<<<grid.x, 256, 0, st>>>(parts, n_parts, N, dbias);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_zero16(uint16_t* p, int64_t n, hipStream_t st) {
+  zero16_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0, st>>>(p, n);
+  return hipGetLastError();
+}
+
+}  // namespace swq
