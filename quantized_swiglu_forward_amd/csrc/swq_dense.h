@@ -30,8 +30,22 @@ struct DenseGemm {
   int out_type;
   void* z;                  // [P, Q] or null
   uint8_t* z_scales;        // [P, ceil(Q / 32)]: z as a checkpoint; or null
+  // set by plan_dense_gemm
+  int kind;                 // kernel and tile shape
+  int splits;               // blocks that share a tile's inner indexes, split_len each (a multiple of 64)
+  int64_t split_len;
+  int64_t part_ld;
+  float* parts;             // with splits > 1: their sums [splits][P][part_ld], dense_parts_bytes
 };
+// The operands of a planned product that takes whole units: rows of 16-byte units from 16-byte aligned bases, lda and ldb
+// multiples of 8, elements past R in a row's last unit zeros.
+inline bool dense_takes_units(const DenseGemm& g) { return g.kind != 0; }
+void plan_dense_gemm(DenseGemm& g);
+int64_t dense_parts_bytes(const DenseGemm& g);
 hipError_t launch_dense_gemm(const DenseGemm& g, hipStream_t st);
+// rows of K elements to rows of ceil8(K), zeros behind
+hipError_t launch_dense_pad(const uint16_t* src, int64_t R, int64_t K, uint16_t* dst, hipStream_t st);
+inline int64_t ceil8(int64_t n) { return (n + 7) / 8 * 8; }
 
 // A tensor [R, K] in 16 bits, or with scales as an 8-bit checkpoint (K / 32 scales a row, rounded up).
 struct Kept {
@@ -41,8 +55,9 @@ struct Kept {
 
 hipError_t launch_mx8_quantize(const void* x, int64_t R, int64_t K, int type, void* codes, uint8_t* scales,
                                hipStream_t st);
+// (rows of out are ld apart)
 hipError_t launch_mx8_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int type, void* out,
-                                 hipStream_t st);
+                                 int64_t ld, hipStream_t st);
 
 // hidden = silu(gate) up, with gate and up as checkpoints where the codes are not null
 hipError_t launch_swiglu(const uint16_t* gate, const uint16_t* up, int64_t R, int64_t K, int type, uint16_t* hidden,
@@ -50,8 +65,8 @@ hipError_t launch_swiglu(const uint16_t* gate, const uint16_t* up, int64_t R, in
 hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, int64_t R, int64_t K, int type,
                                   uint16_t* dgate, uint16_t* dup, uint16_t* hidden, hipStream_t st);
 
-// dz = dout act'(z) (null: not wanted) and its column sums (dbias, null: not wanted) [M, N]; parts: float32
-// [act_parts(M, N)][N].
+// dz = dout act'(z) [M, N], rows ceil8(N) apart with zeros behind (null: not wanted), and its column sums (dbias, null: not
+// wanted); parts: float32 [act_parts(M, N)][N].
 int64_t act_parts(int64_t M, int64_t N);
 hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
                                uint16_t* dbias, float* parts, hipStream_t st);

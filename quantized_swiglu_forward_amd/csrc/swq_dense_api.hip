@@ -32,13 +32,23 @@ int check_elements(int64_t R, int64_t K) {
 // A tensor in 16 bits (2-byte aligned) or a checkpoint (codes of any address).
 bool kept_aligned(const void* data, const void* scales) { return scales || aligned(data, 2); }
 
+// `need` bytes of the stream's workspace (none: null).
+int take(void* stream, int64_t need, char** ws) {
+  if (need == 0) return SWQ_OK;
+  void* p = nullptr;
+  const int rc = stream_workspace((hipStream_t)stream, (size_t)need, &p, kWsSlot);
+  *ws = (char*)p;
+  return rc;
+}
+
 }  // namespace
 
 extern "C" {
 
 int swiglu_q_dense_linear(const void* x, const void* W, const void* bias, const void* residual, int64_t M, int64_t K,
                           int64_t N, int type, int act, int out_mode, void* out, void* z, void* z_scales,
-                          void* stream) {
+                          void* stream_v) {
+  hipStream_t stream = (hipStream_t)stream_v;
   if (!x || !W || !out || (z_scales && !z)) return SWQ_ERR_NULL;
   if (!type16_ok(type) || !act_ok(act) || (out_mode != type && out_mode != SWQ_LINEAR_F32)) return SWQ_ERR_UNSUPPORTED;
   int rc = check_shape(M, K, N);
@@ -62,8 +72,24 @@ int swiglu_q_dense_linear(const void* x, const void* W, const void* bias, const 
   g.out_type = out_mode;
   g.z = z;
   g.z_scales = (uint8_t*)z_scales;
-  (void)hipGetLastError();
-  return check_status(launch_dense_gemm(g, (hipStream_t)stream));
+  plan_dense_gemm(g);
+  // Workspace: x and W with rows of whole 16-byte units, the partial sums of a split.
+  const bool pad = K % 8 != 0 && dense_takes_units(g);
+  const int64_t x_bytes = pad ? align256(M * ceil8(K) * 2) : 0, w_bytes = pad ? align256(N * ceil8(K) * 2) : 0;
+  char* ws = nullptr;
+  rc = take(stream_v, x_bytes + w_bytes + dense_parts_bytes(g), &ws);
+  if (rc != SWQ_OK) return rc;
+  (void)hipGetLastError();            // before the first launch: an error left by others is not this call's
+  if (pad) {
+    rc = check_status(launch_dense_pad(g.a, M, K, (uint16_t*)ws, stream));
+    if (rc == SWQ_OK) rc = check_status(launch_dense_pad(g.b, N, K, (uint16_t*)(ws + x_bytes), stream));
+    if (rc != SWQ_OK) return rc;
+    g.a = (const uint16_t*)ws;
+    g.b = (const uint16_t*)(ws + x_bytes);
+    g.lda = g.ldb = ceil8(K);
+  }
+  g.parts = (float*)(ws + x_bytes + w_bytes);
+  return check_status(launch_dense_gemm(g, stream));
 }
 
 int swiglu_q_dense_linear_backward(const void* dout, const void* x, const void* x_scales, const void* W, const void* z,
@@ -84,55 +110,51 @@ int swiglu_q_dense_linear_backward(const void* dout, const void* x, const void* 
     if (dbias && e == hipSuccess) e = launch_zero16((uint16_t*)dbias, N, stream);
     return check_status(e);
   }
-  // Workspace: dz, x as 16 bits, the partial sums of the bias's gradient.
-  const bool has_dz = act != SWQ_ACT_NONE && (dx || dW), plain_x = dW && x_scales;
-  const int64_t dz_bytes = has_dz ? align256(M * N * 2) : 0, x_bytes = plain_x ? align256(M * K * 2) : 0;
+  DenseGemm gx{}, gw{};
+  gx.type = gx.out_type = gw.type = gw.out_type = type;
+  gx.way_a = kAlong;
+  gx.way_b = gw.way_a = gw.way_b = kDown;
+  gx.lda = gw.lda = ceil8(N);
+  gx.ldb = gw.ldb = ceil8(K);
+  gx.P = M, gx.Q = K, gx.R = N;
+  gw.P = N, gw.Q = K, gw.R = M;
+  gx.out = dx;
+  gw.out = dW;
+  if (dx) plan_dense_gemm(gx);
+  if (dW) plan_dense_gemm(gw);
+  // Workspace: dz (where dout itself will not do), x and W with rows of whole 16-byte units, the partial sums of the
+  // splits, which take turns, and of the bias's gradient.
+  const bool has_dz = (act != SWQ_ACT_NONE || N % 8 != 0) && (dx || dW);
+  const bool has_x = dW && (x_scales || K % 8 != 0), has_w = dx && K % 8 != 0;
+  const int64_t dz_bytes = has_dz ? align256(M * ceil8(N) * 2) : 0, x_bytes = has_x ? align256(M * ceil8(K) * 2) : 0;
+  const int64_t w_bytes = has_w ? align256(N * ceil8(K) * 2) : 0;
+  const int64_t parts = align256(std::max(dx ? dense_parts_bytes(gx) : 0, dW ? dense_parts_bytes(gw) : 0));
   const int64_t sums = dbias ? act_parts(M, N) * N * 4 : 0;
   char* ws = nullptr;
-  if (dz_bytes + x_bytes + sums) {
-    void* p = nullptr;
-    rc = stream_workspace(stream, (size_t)(dz_bytes + x_bytes + sums), &p, kWsSlot);
-    if (rc != SWQ_OK) return rc;
-    ws = (char*)p;
-    (void)hipGetLastError();
-  }
-  uint16_t* dz = has_dz ? (uint16_t*)ws : nullptr;
+  rc = take(stream_v, dz_bytes + x_bytes + w_bytes + parts + sums, &ws);
+  if (rc != SWQ_OK) return rc;
+  (void)hipGetLastError();
+  uint16_t* const dz = has_dz ? (uint16_t*)ws : nullptr;
+  uint16_t* const x16 = (uint16_t*)(ws + dz_bytes);
+  uint16_t* const w16 = (uint16_t*)(ws + dz_bytes + x_bytes);
+  gx.parts = gw.parts = (float*)(ws + dz_bytes + x_bytes + w_bytes);
   if (has_dz || dbias) {
     rc = check_status(launch_act_backward((const uint16_t*)dout, Kept{z, (const uint8_t*)z_scales}, M, N, type, act, dz,
-                                          (uint16_t*)dbias, (float*)(ws + dz_bytes + x_bytes), stream));
+                                          (uint16_t*)dbias, (float*)((char*)gx.parts + parts), stream));
     if (rc != SWQ_OK) return rc;
   }
-  DenseGemm g{};
-  g.type = g.out_type = type;
-  g.a = dz ? dz : (const uint16_t*)dout;
-  g.lda = N;
+  gx.a = gw.a = has_dz ? dz : (const uint16_t*)dout;
   if (dx) {
-    g.way_a = kAlong;
-    g.b = (const uint16_t*)W;
-    g.ldb = K;
-    g.way_b = kDown;
-    g.P = M;
-    g.Q = K;
-    g.R = N;
-    g.out = dx;
-    rc = check_status(launch_dense_gemm(g, stream));
+    if (has_w) rc = check_status(launch_dense_pad((const uint16_t*)W, N, K, w16, stream));
+    gx.b = has_w ? w16 : (const uint16_t*)W;
+    if (rc == SWQ_OK) rc = check_status(launch_dense_gemm(gx, stream));
     if (rc != SWQ_OK) return rc;
   }
   if (dW) {
-    g.b = (const uint16_t*)x;
-    if (plain_x) {
-      rc = check_status(launch_mx8_dequantize(x, (const uint8_t*)x_scales, M, K, type, ws + dz_bytes, stream));
-      if (rc != SWQ_OK) return rc;
-      g.b = (const uint16_t*)(ws + dz_bytes);
-    }
-    g.way_a = kDown;
-    g.ldb = K;
-    g.way_b = kDown;
-    g.P = N;
-    g.Q = K;
-    g.R = M;
-    g.out = dW;
-    rc = check_status(launch_dense_gemm(g, stream));
+    if (x_scales) rc = check_status(launch_mx8_dequantize(x, (const uint8_t*)x_scales, M, K, type, x16, ceil8(K), stream));
+    else if (has_x) rc = check_status(launch_dense_pad((const uint16_t*)x, M, K, x16, stream));
+    gw.b = has_x ? x16 : (const uint16_t*)x;
+    if (rc == SWQ_OK) rc = check_status(launch_dense_gemm(gw, stream));
   }
   return rc;
 }
@@ -157,7 +179,7 @@ int swiglu_q_mx8_dequantize(const void* codes, const void* scales, int64_t R, in
   if (!aligned(out, type_bytes(type))) return SWQ_ERR_ALIGN;
   if (R == 0) return SWQ_OK;
   (void)hipGetLastError();
-  return check_status(launch_mx8_dequantize(codes, (const uint8_t*)scales, R, K, type, out, (hipStream_t)stream));
+  return check_status(launch_mx8_dequantize(codes, (const uint8_t*)scales, R, K, type, out, K, (hipStream_t)stream));
 }
 
 int swiglu_q_swiglu(const void* gate, const void* up, int64_t R, int64_t K, int type, void* hidden, void* gate_codes,

@@ -8,6 +8,19 @@
 namespace swq {
 namespace {
 
+// A buffer offset past every buffer's end: the load returns zeros and touches no memory.
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f.template operator()<I>();
+    each<N, I + 1>(f);
+  }
+}
+
 template <int TYPE>
 __device__ __forceinline__ f32x4 mfma_16(u32x4 a, u32x4 b, f32x4 c) {
   if constexpr (TYPE == kTypeF16)
@@ -16,87 +29,586 @@ __device__ __forceinline__ f32x4 mfma_16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                    0);
 }
-
-// 64 x 64 outputs per block, four waves of 32 x 32, 32 inner indexes at a time through LDS.
 template <int TYPE>
-__global__ __launch_bounds__(256) void dense_kernel(DenseGemm g) {
-  constexpr int PITCH = 40;
-  __shared__ __attribute__((aligned(16))) uint16_t la[64 * PITCH], lb[64 * PITCH];
-  __shared__ float lz[64 * 65];
+__device__ __forceinline__ f32x16 mfma_wide(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (TYPE == kTypeF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
+// XCD-aware order of the tiles: the hardware deals consecutive blocks to the eight XCDs in turn, so block b
+// takes tile b / 8 of a contiguous eighth of the order, and an XCD's L2 sees neighbours.  In the
+// order, bands of eight row tiles run along their columns (bands of 4 the same, of 2 and 16 3 % slower, of 1 and 32 5 to 15).
+__device__ __forceinline__ bool tile_at(int b, int ntp, int ntq, int& tp, int& tq) {
+  constexpr int high = 8;
+  const int total = ntp * ntq, per = (total + 7) / 8;
+  const int t = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || t >= total) return false;
+  const int band = t / (high * ntq), in = t - band * high * ntq, rows = min(high, ntp - high * band);
+  tp = high * band + in % rows;
+  tq = in / rows;
+  return true;
+}
+
+// ------------------------------------------------------------------ epilogue ----
+
+// Eight neighbouring sums of row p from column q on, n of them (0 .. 8) in the matrix; four neighbouring lanes
+// have a block of 32 columns, and all four call it.
+template <int TYPE>
+__device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64_t p, int64_t q, int n) {
+  const int64_t at = p * g.Q + q;
+  if (g.bias) {
+    if (n == 8) {
+      const u32x4 w = *(const u32x4_any*)(g.bias + q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += from_16((uint16_t)(w[j >> 1] >> (16 * (j & 1))), TYPE);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) v[j] += from_16(g.bias[q + j], TYPE);
+    }
+  }
+  if (g.z) {
+    if (g.z_scales) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, j < n ? __float_as_uint(v[j]) & 0x7FFFFFFFu : 0u);
+      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+      const Mx8Step s = mx8_step(m);
+      int c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = mx8_code(v[j], s);
+      const u32x2 w = {pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+      uint8_t* z = (uint8_t*)g.z + at;
+      if (n == 8) {
+        *(u32x2_any*)z = w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) z[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+      }
+      if ((q & 31) == 0 && n > 0) g.z_scales[p * ((g.Q + 31) / 32) + q / 32] = (uint8_t)s.byte;
+    } else {
+      uint16_t* z = (uint16_t*)g.z + at;
+      if (n == 8) {
+        *(u32x4_any*)z = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
+                                 pack16<TYPE>(v[6], v[7])};
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) z[j] = to_16(v[j], TYPE);
+      }
+    }
+  }
+  const auto through = [&](int act) SWQ_INLINE {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate(v[j], act);
+  };
+  switch (g.act) {                     // one branch for eight values
+    case kActRelu: through(kActRelu); break;
+    case kActSilu: through(kActSilu); break;
+    case kActGelu: through(kActGelu); break;
+    case kActGeluTanh: through(kActGeluTanh); break;
+  }
+  if (g.res) {
+    if (n == 8) {
+      const u32x4 w = *(const u32x4_any*)(g.res + at);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += from_16((uint16_t)(w[j >> 1] >> (16 * (j & 1))), TYPE);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) v[j] += from_16(g.res[at + j], TYPE);
+    }
+  }
+  if (g.out_type == kTypeF32) {
+    float* o = (float*)g.out + at;
+    if (n == 8) {
+      *(u32x4_any*)o = __builtin_bit_cast(u32x4, (f32x4){v[0], v[1], v[2], v[3]});
+      *(u32x4_any*)(o + 4) = __builtin_bit_cast(u32x4, (f32x4){v[4], v[5], v[6], v[7]});
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) o[j] = v[j];
+    }
+  } else {
+    uint16_t* o = (uint16_t*)g.out + at;
+    if (n == 8) {
+      *(u32x4_any*)o = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
+                               pack16<TYPE>(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) o[j] = to_16(v[j], TYPE);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- tiles ----
+//
+// WP x WQ waves, each 32 AF rows by 32 BF columns of 32 x 32 accumulators.  A stage is 64 inner indexes of both
+// operands in LDS, S stages, filled by loads that write LDS; a step of 16 reads its successor's operands into
+// registers while its products run, and a stage that has been read makes room for the loads of the one S ahead.
+//
+// Along: a row's 64 elements are 128 bytes, 16-byte unit u at u ^ (row / 2 & 7), and a lane's operand (eight
+// neighbours of a row) is one read.  Down: an inner index's BP elements are a row of LDS, unit u at u ^ 4 (r & 3)
+// (BP = 64: u ^ 4 (r / 2 & 1)), and an operand is two transposing reads of four inner indexes by
+// 16 columns each.  Either way the rows that a read touches lie in different banks.
+//
+// The second operand of the products is a, so that lane 32 h + r has row r's columns 8 e + 4 h .. + 3 in elements
+// 4 e .. 4 e + 3; the sums leave through the wave's own stretch of LDS, 32 rows at a time, as whole lines.
+template <int AF, int BF, int WP, int WQ, int S>
+struct DenseShape {
+  static constexpr int W = WP * WQ, BP = 32 * AF * WP, BQ = 32 * BF * WQ;
+  static constexpr int STAGE_A = BP * 128, STAGE = (BP + BQ) * 128;
+  static constexpr int LOADS_A = BP / (8 * W), LOADS = (BP + BQ) / (8 * W);     // per wave and stage
+  static constexpr int PITCH = 32 * BF + 4, FLUSH = 32 * PITCH * 4;             // floats; bytes of a wave's stretch
+  static constexpr int LDS = S * STAGE > W * FLUSH ? S * STAGE : W * FLUSH;
+  static_assert(BP % (8 * W) == 0 && BQ % (8 * W) == 0 && W % 2 == 0);
+};
+
+// A load of 16 bytes per lane to LDS at lds + FROM, `soff` bytes further than the lane's offset (which alone counts for
+// the range check).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int FROM>
+__device__ __forceinline__ void dma16_at(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_add_u32 m0, %0, %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               ::"s"(lds), "v"(voff), "s"(rs), "s"(soff), "n"(FROM) : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+
+// One operand: its loads and its place in LDS.  Load i of a wave takes the 64 units (W i + wave) 64 + lane of a stage.
+// Along: the descriptor has the tile's rows, a stage's offset is added behind the range check, so there are no
+// bytes at all behind the last stage, whose lanes past R read nothing.  Down: the descriptor moves with the stage
+// and ends at R.
+template <int WAY, int BP, int W>
+struct Operand {
+  static constexpr int UNITS = WAY == kAlong ? 8 : BP / 8, LOADS = BP / (8 * W);      // 16-byte units of a row of LDS
+  i32x4 rs;
+  uint64_t at;              // Down: the stage's address
+  int64_t left;             // Down: bytes from there to the end
+  int64_t ld;
+  uint32_t off[LOADS];      // the lane's offsets
+  int k, tail;              // Along: the lane's first inner index of a stage; indexes of the last stage
+
+  // Down: rows of LDS whose length is a multiple of 256 bytes begin in the same bank, of 128 every second, of 64
+  // every fourth
+  static constexpr int swap(int r) { return BP % 128 == 0 ? (r & 3) << 2 : BP % 64 == 0 ? (r >> 1 & 1) << 2 : 0; }
+
+  __device__ __forceinline__ void aim(const uint16_t* x, int64_t ld_, int64_t first, int64_t n, int64_t r0, int64_t r1,
+                                      int wave, int lane) {
+    ld = ld_;
+    if constexpr (WAY == kAlong) {
+      const int64_t rows = min(n - first, (int64_t)BP);
+      rs = make_srsrc(x + first * ld + r0, (uint32_t)((rows * ld - r0) * 2));
+      const int unit = lane % 8 ^ ((8 * wave + lane / 8) >> 1 & 7);         // (W even: the same in every load)
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) off[i] = (uint32_t)((8 * (W * i + wave) + lane / 8) * ld * 2) + unit * 16;
+      k = unit * 8;
+      tail = (int)((r1 - r0 - 1) & 63) + 1;
+    } else {
+      at = (uint64_t)(x + r0 * ld + first);
+      left = ((r1 - r0) * ld - first) * 2;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int u = (W * i + wave) * 64 + lane, row = u / UNITS;
+        off[i] = (uint32_t)(row * ld * 2) + (u % UNITS ^ swap(row)) * 16;
+      }
+    }
+  }
+  // before the loads of stage t; the stages come in order
+  __device__ __forceinline__ void begin(int t, int stages) {
+    if constexpr (WAY == kDown) {
+      const int64_t n = left < 0 ? 0 : left < (int64_t)kNowhere ? left : (int64_t)kNowhere;
+      rs = make_srsrc((const void*)at, (uint32_t)n);
+    } else {
+      if (t == stages - 1) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) off[i] = k < tail ? off[i] : kNowhere;
+      }
+      if (t >= stages) rs[2] = 0;
+    }
+  }
+  template <int i, int FROM>
+  __device__ __forceinline__ void load(int t, uint32_t lds) const {
+    dma16_at<FROM + W * i * 1024>(rs, lds, off[i], WAY == kAlong ? (uint32_t)t * 128u : 0u);
+  }
+  __device__ __forceinline__ void end() {
+    if constexpr (WAY == kDown) {
+      at += (uint64_t)(ld * 128);
+      left -= ld * 128;
+    }
+  }
+  // the lane's operand of step s, tile `tile` (of 32) of the block's
+  static __device__ __forceinline__ u32x4 read(const char* lds, int s, int tile, int lane) {
+    if constexpr (WAY == kAlong) {
+      const int r = lane & 31, h = lane >> 5;
+      return *(const u32x4*)(lds + (32 * tile + r) * 128 + (((2 * s + h) ^ (r >> 1 & 7)) * 16));
+    } else {
+      const int g = lane >> 4, l = lane & 15, r = 16 * s + 8 * (g >> 1) + (l >> 2);
+      const char* a = lds + r * (BP * 2) + (((4 * tile + 2 * (g & 1) + (l >> 1 & 1)) ^ swap(l >> 2)) * 16) + (l & 1) * 8;
+      typedef __attribute__((address_space(3))) i16x4* lds4;
+      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds_ptr_t)a);
+      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds_ptr_t)(a + 4 * BP * 2));
+      const u32x2 u = __builtin_bit_cast(u32x2, x), v = __builtin_bit_cast(u32x2, y);
+      return (u32x4){u[0], u[1], v[0], v[1]};
+    }
+  }
+};
+
+template <int TYPE, int WAY_A, int WAY_B, int AF, int BF, int WP, int WQ, int S, int OCC>
+__global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(DenseGemm g) {
+  using Sh = DenseShape<AF, BF, WP, WQ, S>;
+  constexpr int W = Sh::W, BP = Sh::BP, BQ = Sh::BQ;
+  __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
 #ifdef SWQ_LDS_POISON
-  lds_poison(la, sizeof(la), kPoisonFloat);
-  lds_poison(lb, sizeof(lb), kPoisonFloat);
-  lds_poison(lz, sizeof(lz), kPoisonFloat);
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
   __syncthreads();
 #endif
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, h = lane >> 4;
-  const int64_t tq = (g.Q + 63) / 64;
-  const int64_t p0 = (int64_t)blockIdx.x / tq * 64, q0 = (int64_t)blockIdx.x % tq * 64;
-  const int wp = (wave >> 1) * 32, wq = (wave & 1) * 32;
-  f32x4 acc[2][2] = {};
-  const auto stage = [&](uint16_t* l, const uint16_t* x, int64_t ld, int way, int64_t i0, int64_t n, int64_t r0) {
-    for (int e = tid; e < 64 * 32; e += 256) {
-      const int i = way == kAlong ? e >> 5 : e & 63, r = way == kAlong ? e & 31 : e >> 6;
-      const bool in = i0 + i < n && r0 + r < g.R;
-      l[i * PITCH + r] = in ? x[way == kAlong ? (i0 + i) * ld + r0 + r : (r0 + r) * ld + i0 + i] : (uint16_t)0;
-    }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave / WQ, wq = wave % WQ;
+  int tp, tq;
+  if (!tile_at(blockIdx.x, (int)((g.P + BP - 1) / BP), (int)((g.Q + BQ - 1) / BQ), tp, tq)) return;
+  const int64_t p0 = (int64_t)tp * BP, q0 = (int64_t)tq * BQ;
+  const int64_t r0 = (int64_t)blockIdx.y * g.split_len, r1 = min(r0 + g.split_len, g.R);
+  const int stages = (int)((r1 - r0 + 63) / 64);
+
+  Operand<WAY_A, BP, W> oa;
+  Operand<WAY_B, BQ, W> ob;
+  oa.aim(g.a, g.lda, p0, g.P, r0, r1, wave, lane);
+  ob.aim(g.b, g.ldb, q0, g.Q, r0, r1, wave, lane);
+  // load i of a stage; the stages are asked for in order
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * 1024);
+  const auto load = [&]<int i>(int t, int slot) SWQ_INLINE {
+    if constexpr (i == 0) oa.begin(t, stages), ob.begin(t, stages);
+    const uint32_t base = lds0 + slot * Sh::STAGE;
+    if constexpr (i < Sh::LOADS_A) oa.template load<i, 0>(t, base);
+    else ob.template load<i - Sh::LOADS_A, Sh::STAGE_A>(t, base);
+    if constexpr (i == Sh::LOADS - 1) oa.end(), ob.end();
   };
-  for (int64_t r0 = 0; r0 < g.R; r0 += 32) {
-    __syncthreads();
-    stage(la, g.a, g.lda, g.way_a, p0, g.P, r0);
-    stage(lb, g.b, g.ldb, g.way_b, q0, g.Q, r0);
-    __syncthreads();
-    u32x4 a[2], b[2];
+
+  f32x16 acc[AF][BF];
+  u32x4 a[2][AF], b[2][BF];
+  const auto read = [&]<int set, int i>(int s, int slot) SWQ_INLINE {
+    const char* l = lds + slot * Sh::STAGE;
+    if constexpr (i < BF) b[set][i] = ob.read(l + Sh::STAGE_A, s, wq * BF + i, lane);
+    else a[set][i - BF] = oa.read(l, s, wp * AF + i - BF, lane);
+  };
+  const auto meet = [&]() SWQ_INLINE {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // A step's products; before(n) is issued in front of the n-th.
+  constexpr int FRAGS = AF + BF, M = AF * BF;
+  constexpr int READS = (FRAGS + M - 1) / M, ISSUES = (Sh::LOADS + M - 1) / M;
+  constexpr int READS2 = (2 * FRAGS + M - 1) / M;      // before the barrier, so that it does not wait for them
+  const auto products = [&]<int SET>(auto before) SWQ_INLINE {
+    each<M>([&]<int n>() SWQ_INLINE {
+      constexpr int i = n / BF, j = n % BF;
+      before.template operator()<n>();
+      acc[i][j] = mfma_wide<TYPE>(b[SET][j], a[SET][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  each<S>([&]<int t>() SWQ_INLINE { each<Sh::LOADS>([&]<int i>() SWQ_INLINE { load.template operator()<i>(t, t); }); });
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[i] = *(const u32x4*)(la + (wp + 16 * i + r16) * PITCH + 8 * h);
-      b[i] = *(const u32x4*)(lb + (wq + 16 * i + r16) * PITCH + 8 * h);
+  for (int i = 0; i < AF; ++i)
+#pragma unroll
+    for (int j = 0; j < BF; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  wait_vmcnt<(S - 1) * Sh::LOADS>();
+  meet();
+  int slot = 0;
+  each<FRAGS>([&]<int i>() SWQ_INLINE { read.template operator()<0, i>(0, 0); });
+  // Loads are issued past the last stage too (they read nothing), so the counts hold to the end.
+  for (int t = 0; t < stages; ++t) {
+    each<3>([&]<int s>() SWQ_INLINE {
+      products.template operator()<s & 1>([&]<int n>() SWQ_INLINE {
+        constexpr int PER = s == 2 ? READS2 : READS;
+        each<PER>([&]<int e>() SWQ_INLINE {
+          if constexpr (n * PER + e < FRAGS) read.template operator()<(s + 1) & 1, n * PER + e>(s + 1, slot);
+        });
+      });
+    });
+    wait_vmcnt<(S - 2) * Sh::LOADS>();           // stage t + 1 is there
+    meet();
+    const int was = slot;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    products.template operator()<1>([&]<int n>() SWQ_INLINE {
+      each<READS>([&]<int e>() SWQ_INLINE {
+        if constexpr (n * READS + e < FRAGS) read.template operator()<0, n * READS + e>(0, slot);
+      });
+      each<ISSUES>([&]<int e>() SWQ_INLINE {
+        if constexpr (n * ISSUES + e < Sh::LOADS) load.template operator()<n * ISSUES + e>(t + S, was);
+      });
+    });
+  }
+  wait_vmcnt<0>();           // no load past the end may still write LDS
+  meet();
+
+  float* buf = (float*)(lds + wave * Sh::FLUSH);
+  constexpr int LANES = 4 * BF, ROWS = 64 / LANES;                     // of a row; rows at a time
+  const int r = lane & 31, h = lane >> 5, col = lane % LANES * 8;
+  const int64_t q = q0 + wq * 32 * BF + col;
+  const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
+  each<AF>([&]<int i>() SWQ_INLINE {
+#pragma unroll
+    for (int j = 0; j < BF; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *(f32x4*)(buf + r * Sh::PITCH + 32 * j + 8 * e + 4 * h) =
+            (f32x4){acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+#pragma unroll 1
+    for (int k = 0; k < 32; k += ROWS) {
+      const int row = k + lane / LANES;
+      if (lane >= ROWS * LANES || row >= 32) continue;
+      const int64_t p = p0 + (wp * AF + i) * 32 + row;
+      const f32x4 x = *(const f32x4*)(buf + row * Sh::PITCH + col), y = *(const f32x4*)(buf + row * Sh::PITCH + col + 4);
+      float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      if (p >= g.P) continue;
+      if (g.parts) {
+        if (n > 0) {
+          float* o = g.parts + ((int64_t)blockIdx.y * g.P + p) * g.part_ld + q;
+          *(f32x4*)o = x;
+          *(f32x4*)(o + 4) = y;
+        }
+      } else {
+        finish8<TYPE>(g, v, p, q, n);
+      }
+    }
+  });
+}
+
+// The sums of a split, added in its order.
+template <int TYPE>
+__global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t per_row) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t p = i / per_row, q = 8 * (i - p * per_row);
+  if (p >= g.P) return;                        // four neighbouring lanes leave together
+  const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
+  float v[8] = {};
+  if (n > 0) {
+    for (int s = 0; s < g.splits; ++s) {
+      const float* f = g.parts + ((int64_t)s * g.P + p) * g.part_ld + q;
+      const f32x4 x = *(const f32x4*)f, y = *(const f32x4*)(f + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += x[j], v[4 + j] += y[j];
+    }
+  }
+  finish8<TYPE>(g, v, p, q, n);
+}
+
+// Rows of another length: dst[r, 0 .. ceil8(K)) = src[r, 0 .. K), zeros behind.  A thread has eight elements at a time.
+__global__ __launch_bounds__(256) void dense_pad_kernel(const uint16_t* __restrict__ src, int64_t K, uint32_t per_row,
+                                                        int64_t n, uint16_t* __restrict__ dst) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per_row, k = 8 * (i - r * per_row);
+    u32x4 w = {0, 0, 0, 0};
+    const uint16_t* s = src + r * K + k;
+    if (k + 8 <= K) {
+      w = *(const u32x4_any*)s;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k + j < K) w[j >> 1] |= (uint32_t)s[j] << (16 * (j & 1));
+    }
+    *(u32x4*)(dst + 8 * i) = w;
+  }
+}
+
+// ----------------------------------------------------------------- few rows ----
+//
+// Up to 16 RT rows by 16 CT columns per block, both operands along their rows and straight to registers, at any
+// address and of any length.  The waves take chunks of 128 inner indexes in turn, and their sums meet in LDS, added in
+// wave order.  The weights' bytes count here: every weight is read once per block of rows.
+template <int TYPE, int RT, int CT>
+__global__ __launch_bounds__(1024) void dense_few_kernel(DenseGemm g) {
+  constexpr int PITCH = 16 * CT + 4, MAX_W = 16;
+  __shared__ __attribute__((aligned(16))) float sums[MAX_W * 16 * RT * PITCH];
+#ifdef SWQ_LDS_POISON
+  lds_poison(sums, sizeof(sums), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, W = blockDim.x >> 6;
+  const int r = lane & 15, h = lane >> 4;
+  const int64_t q0 = (int64_t)blockIdx.x * (16 * CT), p0 = (int64_t)blockIdx.y * (16 * RT);
+  const uint16_t* x[RT];
+  const uint16_t* w[CT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) x[i] = g.a + min(p0 + 16 * i + r, g.P - 1) * g.lda + 8 * h;
+#pragma unroll
+  for (int j = 0; j < CT; ++j) w[j] = g.b + min(q0 + 16 * j + r, g.Q - 1) * g.ldb + 8 * h;
+  f32x4 acc[RT][CT] = {};
+  const int R = (int)g.R, full = R >> 7;
+  for (int c = wave; c < full; c += W) {
+    u32x4 a[RT][4], b[CT][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int j = 0; j < CT; ++j) b[j][s] = *(const u32x4_any*)(w[j] + 128 * c + 32 * s);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) a[i][s] = *(const u32x4_any*)(x[i] + 128 * c + 32 * s);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_16<TYPE>(b[j], a[i], acc[i][j]);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = mfma_16<TYPE>(b[j][s], a[i][s], acc[i][j]);
+  }
+  if ((R & 127) && wave == full % W) {         // the rest, element by element at its end
+    const auto some = [&](const uint16_t* f, int n) SWQ_INLINE {
+      u32x4 v = {0, 0, 0, 0};
+      if (n >= 8) return (u32x4)*(const u32x4_any*)f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) v[e >> 1] |= (uint32_t)f[e] << (16 * (e & 1));
+      return v;
+    };
+#pragma unroll 1
+    for (int k = full * 128; k < R; k += 32) {
+      u32x4 a[RT], b[CT];
+#pragma unroll
+      for (int j = 0; j < CT; ++j) b[j] = some(w[j] + k, R - k - 8 * h);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) a[i] = some(x[i] + k, R - k - 8 * h);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = mfma_16<TYPE>(b[j], a[i], acc[i][j]);
+    }
   }
   // lane 16 h + r has columns 4 h .. 4 h + 3 of row r
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) lz[(wp + 16 * i + r16) * 65 + wq + 16 * j + 4 * h + e] = acc[i][j][e];
+    for (int j = 0; j < CT; ++j)
+      *(f32x4*)(sums + ((wave * RT + i) * 16 + r) * PITCH + 16 * j + 4 * h) = acc[i][j];
   __syncthreads();
-  const int64_t blocks = (g.Q + 31) / 32;
-  for (int e = tid; e < 64 * 64; e += 256) {          // a wave has a whole row
-    const int i = e >> 6, j = e & 63;
-    const int64_t p = p0 + i, q = q0 + j;
-    const bool in = p < g.P && q < g.Q;
-    float z = lz[i * 65 + j];
-    if (in && g.bias) z += from_16(g.bias[q], TYPE);
-    if (g.z_scales) {
-      uint32_t m = in ? __float_as_uint(z) & 0x7FFFFFFFu : 0u;
+  for (int t = threadIdx.x; t < 32 * RT * CT; t += blockDim.x) {
+    const int row = t / (2 * CT), col = t % (2 * CT) * 8;
+    const int64_t p = p0 + row, q = q0 + col;
+    float v[8] = {};
+    for (int u = 0; u < W; ++u) {
+      const float* f = sums + (u * RT * 16 + row) * PITCH + col;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-      const Mx8Step s = mx8_step(m);
-      if (in) ((int8_t*)g.z)[p * g.Q + q] = (int8_t)mx8_code(z, s);
-      if (in && (q & 31) == 0) g.z_scales[p * blocks + q / 32] = (uint8_t)s.byte;
-    } else if (g.z && in) {
-      ((uint16_t*)g.z)[p * g.Q + q] = to_16(z, TYPE);
+      for (int e = 0; e < 8; ++e) v[e] += f[e];
     }
-    if (!in) continue;
-    float y = activate(z, g.act);
-    if (g.res) y += from_16(g.res[p * g.Q + q], TYPE);
-    if (g.out_type == kTypeF32) ((float*)g.out)[p * g.Q + q] = y;
-    else ((uint16_t*)g.out)[p * g.Q + q] = to_16(y, TYPE);
+    if (p < g.P) finish8<TYPE>(g, v, p, q, q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0);
   }
+}
+
+template <int TYPE, int RT>
+void launch_few_rows(const DenseGemm& g, hipStream_t st) {
+  const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(1, (g.R + 127) / 128));
+  const int ct = g.z_scales || g.Q >= 32 * 512 ? 2 : 1;      // (a checkpoint's blocks are 32 columns)
+  const dim3 grid((unsigned)((g.Q + 16 * ct - 1) / (16 * ct)), (unsigned)((g.P + 16 * RT - 1) / (16 * RT)));
+  if (ct == 2) dense_few_kernel<TYPE, RT, 2><<<grid, 64 * waves, 0, st>>>(g);
+  else dense_few_kernel<TYPE, RT, 1><<<grid, 64 * waves, 0, st>>>(g);
+}
+
+template <int TYPE>
+void launch_few(const DenseGemm& g, hipStream_t st) {
+  if (g.P <= 16) launch_few_rows<TYPE, 1>(g, st);
+  else if (g.P <= 32) launch_few_rows<TYPE, 2>(g, st);
+  else launch_few_rows<TYPE, 4>(g, st);
+}
+
+// -------------------------------------------------------------------- choice ----
+
+enum : int { kFewRows = 0, kTiles64 = 1, kTiles128 = 2, kTiles256 = 3 };
+constexpr int kSide[] = {0, 64, 128, 256};
+
+template <int TYPE, int WA, int WB>
+void launch_tiles(const DenseGemm& g, hipStream_t st) {
+  const int64_t side = kSide[g.kind], tiles = (g.P + side - 1) / side * ((g.Q + side - 1) / side);
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)g.splits);
+  switch (g.kind) {
+    case kTiles256: dense_kernel<TYPE, WA, WB, 4, 2, 2, 4, 2, 1><<<grid, 512, 0, st>>>(g); break;
+    case kTiles128: dense_kernel<TYPE, WA, WB, 2, 2, 2, 2, 2, 2><<<grid, 256, 0, st>>>(g); break;
+    default: dense_kernel<TYPE, WA, WB, 1, 1, 2, 2, 4, 2><<<grid, 256, 0, st>>>(g); break;
+  }
+}
+
+template <int TYPE>
+void launch_ways(const DenseGemm& g, hipStream_t st) {
+  if (g.way_a == kDown) launch_tiles<TYPE, kDown, kDown>(g, st);
+  else if (g.way_b == kDown) launch_tiles<TYPE, kAlong, kDown>(g, st);
+  else launch_tiles<TYPE, kAlong, kAlong>(g, st);
 }
 
 }  // namespace
 
-hipError_t launch_dense_gemm(const DenseGemm& g, hipStream_t st) {
-  const int64_t blocks = (g.P + 63) / 64 * ((g.Q + 63) / 64);
-  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidValue;
-  if (g.type == kTypeF16) dense_kernel<kTypeF16><<<(unsigned)blocks, 256, 0, st>>>(g);
-  else dense_kernel<kTypeBf16><<<(unsigned)blocks, 256, 0, st>>>(g);
+// The few-row kernel up to 16 rows, and up to 64 where a row's length is no multiple of 8, which the tiles would have
+// copied first (rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 8.5 / 10.2, 16 x 4096 x 4096 9.9 / 10.5,
+// 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 11 / 18).  Else the tile shape and the split of the inner indexes whose
+// fullest CU is done first, in us.  Measured: a CU takes 0.2 us per stage of a 64 x 64 tile,
+// 0.46 of a 128 x 128 one (alone on its CU 0.47, 0.72 where all CUs are busy) and 1.1 of a 256 x 256 one, 1.5 where all CUs are
+// busy and the card's power limits them; a split writes and reads its float32 sums at 5.5 TB/s and takes
+// another launch.  (tiles of 256 / 128 / 64, us: 2048 x 4096 x 14336 194 / 226 / 358, 512 x 2048 x 5632 44 / 26 / 24,
+// 128 x 2048 x 5632 41 / 19 / 11; its gradient by x, four splits of 64 14, one 27.)
+constexpr int64_t kFewRowsMost = 16, kFewRowsOdd = 64;
+void plan_dense_gemm(DenseGemm& g) {
+  const int cus = device_cus();
+  const int64_t stages = (g.R + 63) / 64;
+  g.part_ld = ceil8(g.Q);
+  g.splits = 1;
+  g.split_len = stages * 64;
+  if (g.way_a == kAlong && g.way_b == kAlong && (g.P <= kFewRowsMost || (g.P <= kFewRowsOdd && g.R % 8 != 0))) {
+    g.kind = kFewRows;
+    return;
+  }
+  double best = 1e300;
+  int64_t splits = 1;
+  for (int kind = kTiles64; kind <= kTiles256; ++kind) {
+    const int64_t side = kSide[kind], tiles = (g.P + side - 1) / side * ((g.Q + side - 1) / side);
+    const int64_t most = tiles >= cus ? 2 : std::min<int64_t>(16, stages);
+    for (int64_t s = 1; s <= most; ++s) {
+      const int64_t len = (stages + s - 1) / s, blocks = tiles * s, n = (blocks + cus - 1) / cus;
+      const double load = blocks < cus ? (double)blocks / cus : 1.0;
+      const double each = kind == kTiles256 ? 2.2 + len * (1.1 + 0.4 * load)
+                          : kind == kTiles128 ? 0.7 + len * (n > 1 ? 0.46 : 0.47 + 0.25 * load)
+                                              : 0.3 + len * (n > 1 ? 0.2 : 0.23);
+      const double join = s > 1 ? 2.0 + (8.0 * s + 2.0) * g.P * g.Q / 5.5e6 : 0.0;
+      if (n * each + join < best) best = n * each + join, g.kind = kind, splits = s;
+    }
+  }
+  const int64_t len = (stages + splits - 1) / splits;
+  g.splits = (int)((stages + len - 1) / len);
+  g.split_len = len * 64;
+}
+
+int64_t dense_parts_bytes(const DenseGemm& g) { return g.splits > 1 ? g.splits * g.P * g.part_ld * 4 : 0; }
+
+hipError_t launch_dense_pad(const uint16_t* src, int64_t R, int64_t K, uint16_t* dst, hipStream_t st) {
+  const int64_t per_row = (K + 7) / 8, n = R * per_row;
+  const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20);
+  dense_pad_kernel<<<blocks, 256, 0, st>>>(src, K, (uint32_t)per_row, n, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t st) {
+  DenseGemm g = p;
+  if (g.splits <= 1) g.parts = nullptr;
+  if (g.kind == kFewRows) {
+    if (g.type == kTypeF16) launch_few<kTypeF16>(g, st);
+    else launch_few<kTypeBf16>(g, st);
+    return hipGetLastError();
+  }
+  if (g.type == kTypeF16) launch_ways<kTypeF16>(g, st);
+  else launch_ways<kTypeBf16>(g, st);
+  if (g.splits > 1) {
+    const uint32_t per_row = (uint32_t)((g.Q + 31) / 32 * 4);
+    const unsigned blocks = (unsigned)((g.P * per_row + 255) / 256);
+    if (g.type == kTypeF16) dense_join_kernel<kTypeF16><<<blocks, 256, 0, st>>>(g, per_row);
+    else dense_join_kernel<kTypeBf16><<<blocks, 256, 0, st>>>(g, per_row);
+  }
   return hipGetLastError();
 }
 

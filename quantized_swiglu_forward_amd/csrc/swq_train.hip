@@ -17,13 +17,14 @@ struct Pieces {
 struct Piece {
   int64_t at;               // its first element
   int64_t block;            // its block's scale
+  int64_t row;
   int n;                    // elements, 0 .. 8
 };
 __device__ __forceinline__ Piece piece_of(const Pieces& t, int64_t i) {
   const int64_t row = i / t.per_row;
   const uint32_t c = (uint32_t)(i - row * t.per_row);
   const int64_t left = t.K - 8 * (int64_t)c;
-  return {row * t.K + 8 * (int64_t)c, row * (t.per_row / 4) + (c >> 2), left >= 8 ? 8 : left > 0 ? (int)left : 0};
+  return {row * t.K + 8 * (int64_t)c, row * (t.per_row / 4) + (c >> 2), row, left >= 8 ? 8 : left > 0 ? (int)left : 0};
 }
 
 template <int TYPE>
@@ -126,13 +127,14 @@ __global__ __launch_bounds__(256) void mx8_quantize_kernel(const void* __restric
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx8_dequantize_kernel(const void* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, Pieces t,
-                                                             int64_t first, int64_t end, void* __restrict__ out) {
+                                                             int64_t first, int64_t end, void* __restrict__ out,
+                                                             int64_t ld) {
   const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= end) return;
   const Piece p = piece_of(t, i);
   float v[8];
   decode8(codes, mx8_scale(scales[p.block]), p.at, p.n, v);
-  store8<TYPE>(out, p.at, p.n, v);
+  store8<TYPE>(out, p.at + p.row * (ld - t.K), p.n, v);
 }
 
 template <int TYPE>
@@ -210,21 +212,21 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
                                                            int64_t N, int act, int64_t rows,
                                                            uint16_t* __restrict__ dz, float* __restrict__ parts) {
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  const int64_t blocks = (N + 31) / 32;
+  const int64_t blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
+  if (n >= (dz ? ld : N)) return;
   const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(m0 + rows, M);
   float sum = 0.0f;
   for (int64_t m = m0; m < m1; ++m) {
-    float d = from_16(dout[m * N + n], TYPE);
-    if (act != kActNone) {
+    float d = n < N ? from_16(dout[m * N + n], TYPE) : 0.0f;
+    if (act != kActNone && n < N) {
       const float v = z.scales ? (float)((const int8_t*)z.data)[m * N + n] * mx8_scale(z.scales[m * blocks + n / 32])
                                : from_16(((const uint16_t*)z.data)[m * N + n], TYPE);
       d *= activate_slope(v, act);
     }
     sum += d;
-    if (dz) dz[m * N + n] = to_16(d, TYPE);
+    if (dz) dz[m * ld + n] = to_16(d, TYPE);
   }
-  if (parts) parts[(int64_t)blockIdx.y * N + n] = sum;
+  if (parts && n < N) parts[(int64_t)blockIdx.y * N + n] = sum;
 }
 template <int TYPE>
 __global__ __launch_bounds__(256) void act_sums_kernel(const float* __restrict__ parts, int64_t n_parts, int64_t N,
@@ -252,11 +254,11 @@ hipError_t launch_mx8_quantize(const void* x, int64_t R, int64_t K, int type, vo
 }
 
 hipError_t launch_mx8_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int type, void* out,
-                                 hipStream_t st) {
+                                 int64_t ld, hipStream_t st) {
   return over_pieces(R, K, [&](dim3 grid, Pieces t, int64_t i, int64_t end) {
-    if (type == kTypeF32) mx8_dequantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
-    else if (type == kTypeF16) mx8_dequantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
-    else mx8_dequantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
+    if (type == kTypeF32) mx8_dequantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out, ld);
+    else if (type == kTypeF16) mx8_dequantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out, ld);
+    else mx8_dequantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out, ld);
   });
 }
 
@@ -281,7 +283,7 @@ int64_t act_parts(int64_t M, int64_t) { return M < kActParts ? M : kActParts; }
 hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
                                uint16_t* dbias, float* parts, hipStream_t st) {
   const int64_t rows = (M + act_parts(M, N) - 1) / act_parts(M, N), n_parts = (M + rows - 1) / rows;
-  const dim3 grid((unsigned)((N + 255) / 256), (unsigned)n_parts);
+  const dim3 grid((unsigned)((ceil8(N) + 255) / 256), (unsigned)n_parts);
   const auto kernel = type == kTypeF16 ? act_backward_kernel<kTypeF16> : act_backward_kernel<kTypeBf16>;
   kernel<<<grid, 256, 0, st>>>(dout, z, M, N, act, rows, dz, dbias ? parts : nullptr);
   if (dbias) {
