@@ -54,22 +54,35 @@ __device__ __forceinline__ bool tile_at(int b, int ntp, int ntq, int& tp, int& t
 
 // ------------------------------------------------------------------ epilogue ----
 
+// Eight neighbouring 16-bit values, n of them (0 .. 8) there.
+__device__ __forceinline__ u32x4 load8(const uint16_t* f, int n) {
+  if (n == 8) return *(const u32x4_any*)f;
+  u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) w[j >> 1] |= (uint32_t)f[j] << (16 * (j & 1));
+  return w;
+}
+template <int TYPE>
+__device__ __forceinline__ void add8(float (&v)[8], u32x4 w) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += from_16((uint16_t)(w[j >> 1] >> (16 * (j & 1))), TYPE);
+}
+// The bias of columns q .., and the residual of (p, q ..); zeros where there is none.
+__device__ __forceinline__ u32x4 bias_at(const DenseGemm& g, int64_t q, int n) {
+  return g.bias ? load8(g.bias + q, n) : (u32x4){0, 0, 0, 0};
+}
+__device__ __forceinline__ u32x4 residual_at(const DenseGemm& g, int64_t p, int64_t q, int n) {
+  return g.res && p < g.P ? load8(g.res + p * g.Q + q, n) : (u32x4){0, 0, 0, 0};
+}
+
 // Eight neighbouring sums of row p from column q on, n of them (0 .. 8) in the matrix; four neighbouring lanes
 // have a block of 32 columns, and all four call it.
 template <int TYPE>
-__device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64_t p, int64_t q, int n) {
+__device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64_t p, int64_t q, int n, u32x4 bias,
+                                        u32x4 residual) {
   const int64_t at = p * g.Q + q;
-  if (g.bias) {
-    if (n == 8) {
-      const u32x4 w = *(const u32x4_any*)(g.bias + q);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += from_16((uint16_t)(w[j >> 1] >> (16 * (j & 1))), TYPE);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) v[j] += from_16(g.bias[q + j], TYPE);
-    }
-  }
+  if (g.bias) add8<TYPE>(v, bias);
   if (g.z) {
     if (g.z_scales) {
       uint32_t m = 0;
@@ -113,17 +126,7 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
     case kActGelu: through(kActGelu); break;
     case kActGeluTanh: through(kActGeluTanh); break;
   }
-  if (g.res) {
-    if (n == 8) {
-      const u32x4 w = *(const u32x4_any*)(g.res + at);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += from_16((uint16_t)(w[j >> 1] >> (16 * (j & 1))), TYPE);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) v[j] += from_16(g.res[at + j], TYPE);
-    }
-  }
+  if (g.res) add8<TYPE>(v, residual);
   if (g.out_type == kTypeF32) {
     float* o = (float*)g.out + at;
     if (n == 8) {
@@ -167,7 +170,7 @@ struct DenseShape {
   static constexpr int LOADS_A = BP / (8 * W), LOADS = (BP + BQ) / (8 * W);     // per wave and stage
   static constexpr int PITCH = 32 * BF + 4, FLUSH = 32 * PITCH * 4;             // floats; bytes of a wave's stretch
   static constexpr int LDS = S * STAGE > W * FLUSH ? S * STAGE : W * FLUSH;
-  static_assert(BP % (8 * W) == 0 && BQ % (8 * W) == 0 && W % 2 == 0);
+  static_assert(BP % (8 * W) == 0 && BQ % (8 * W) == 0 && W % 2 == 0 && 16 % BF == 0);
 };
 
 // A load of 16 bytes per lane to LDS at lds + FROM, `soff` bytes further than the lane's offset (which alone counts for
@@ -357,6 +360,15 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(
   const int r = lane & 31, h = lane >> 5, col = lane % LANES * 8;
   const int64_t q = q0 + wq * 32 * BF + col;
   const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
+  // The residual comes a round of 32 rows ahead.
+  constexpr int PASSES = 32 / ROWS;
+  const int64_t pw = p0 + wp * 32 * AF + lane / LANES;
+  const u32x4 bias = g.parts ? (u32x4){0, 0, 0, 0} : bias_at(g, q, n);
+  u32x4 ahead[PASSES] = {};
+  if (g.res && !g.parts) {
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) ahead[k] = residual_at(g, pw + k * ROWS, q, n);
+  }
   each<AF>([&]<int i>() SWQ_INLINE {
 #pragma unroll
     for (int j = 0; j < BF; ++j)
@@ -367,10 +379,20 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(
 #pragma unroll 1
     for (int k = 0; k < 32; k += ROWS) {
       const int row = k + lane / LANES;
-      if (lane >= ROWS * LANES || row >= 32) continue;
-      const int64_t p = p0 + (wp * AF + i) * 32 + row;
+      const int64_t p = pw + i * 32 + k;
       const f32x4 x = *(const f32x4*)(buf + row * Sh::PITCH + col), y = *(const f32x4*)(buf + row * Sh::PITCH + col + 4);
       float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      const u32x4 residual = ahead[0];
+      if constexpr (i + 1 < AF) {
+        if (g.res && !g.parts) {
+#pragma unroll
+          for (int e = 0; e + 1 < PASSES; ++e) ahead[e] = ahead[e + 1];
+          ahead[PASSES - 1] = residual_at(g, p + 32, q, n);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e + 1 < PASSES; ++e) ahead[e] = ahead[e + 1];
+      }
       if (p >= g.P) continue;
       if (g.parts) {
         if (n > 0) {
@@ -379,7 +401,7 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(
           *(f32x4*)(o + 4) = y;
         }
       } else {
-        finish8<TYPE>(g, v, p, q, n);
+        finish8<TYPE>(g, v, p, q, n, bias, residual);
       }
     }
   });
@@ -401,7 +423,7 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t p
       for (int j = 0; j < 4; ++j) v[j] += x[j], v[4 + j] += y[j];
     }
   }
-  finish8<TYPE>(g, v, p, q, n);
+  finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
 }
 
 // Rows of another length: dst[r, 0 .. ceil8(K)) = src[r, 0 .. K), zeros behind.  A thread has eight elements at a time.
@@ -500,7 +522,8 @@ __global__ __launch_bounds__(1024) void dense_few_kernel(DenseGemm g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += f[e];
     }
-    if (p < g.P) finish8<TYPE>(g, v, p, q, q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0);
+    const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
+    if (p < g.P) finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
   }
 }
 

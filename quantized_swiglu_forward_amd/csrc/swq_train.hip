@@ -205,37 +205,80 @@ hipError_t over_pieces(int64_t R, int64_t K, F launch) {
   return hipGetLastError();
 }
 
-// dz and the sums of its columns: a thread has one column of a stretch of rows.
-constexpr int64_t kActParts = 64;
+// dz and the sums of its columns.  A block has 512 columns (a thread eight of them) of a stretch of rows, four rows at
+// a time; the four meet in LDS, the stretches in a second kernel, both in order.
 template <int TYPE>
 __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dout, Kept z, int64_t M,
                                                            int64_t N, int act, int64_t rows,
                                                            uint16_t* __restrict__ dz, float* __restrict__ parts) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
-  if (n >= (dz ? ld : N)) return;
-  const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(m0 + rows, M);
-  float sum = 0.0f;
-  for (int64_t m = m0; m < m1; ++m) {
-    float d = n < N ? from_16(dout[m * N + n], TYPE) : 0.0f;
-    if (act != kActNone && n < N) {
-      const float v = z.scales ? (float)((const int8_t*)z.data)[m * N + n] * mx8_scale(z.scales[m * blocks + n / 32])
-                               : from_16(((const uint16_t*)z.data)[m * N + n], TYPE);
-      d *= activate_slope(v, act);
+  __shared__ float meet[3][64][8];
+#ifdef SWQ_LDS_POISON
+  lds_poison(meet, sizeof(meet), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int c = threadIdx.x & 63, team = threadIdx.x >> 6;
+  const int64_t q = (int64_t)blockIdx.x * 512 + 8 * c, blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
+  const int n = q + 8 <= N ? 8 : q < N ? (int)(N - q) : 0;
+  const int64_t m1 = min((int64_t)(blockIdx.y + 1) * rows, M);
+  float sum[8] = {};
+  const auto go = [&](auto slope) SWQ_INLINE {
+    if (n > 0) {
+#pragma unroll 2
+      for (int64_t m = (int64_t)blockIdx.y * rows + team; m < m1; m += 4) {
+        float d[8], v[8];
+        load8<TYPE>(dout, m * N + q, n, d);
+        if (act != kActNone) {
+          if (z.scales) decode8(z.data, mx8_scale(z.scales[m * blocks + q / 32]), m * N + q, n, v);
+          else load8<TYPE>(z.data, m * N + q, n, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          d[j] = j < n ? d[j] * slope(v[j]) : 0.0f;
+          sum[j] += d[j];
+        }
+        if (dz) store8<TYPE>(dz, m * ld + q, 8, d);          // (zeros behind a row's end)
+      }
     }
-    sum += d;
-    if (dz) dz[m * ld + n] = to_16(d, TYPE);
+  };
+  switch (act) {
+    case kActNone: go([](float) { return 1.0f; }); break;
+    case kActRelu: go([](float v) { return activate_slope(v, kActRelu); }); break;
+    case kActSilu: go([](float v) { return activate_slope(v, kActSilu); }); break;
+    case kActGelu: go([](float v) { return activate_slope(v, kActGelu); }); break;
+    default: go([](float v) { return activate_slope(v, kActGeluTanh); });
   }
-  if (parts && n < N) parts[(int64_t)blockIdx.y * N + n] = sum;
+  if (!parts) return;
+  if (team) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) meet[team - 1][c][j] = sum[j];
+  }
+  __syncthreads();
+  if (team == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) parts[(int64_t)blockIdx.y * N + q + j] = (sum[j] + meet[0][c][j]) + (meet[1][c][j] + meet[2][c][j]);
+  }
 }
+
+// 64 columns per block, four threads a column.
 template <int TYPE>
-__global__ __launch_bounds__(256) void act_sums_kernel(const float* __restrict__ parts, int64_t n_parts, int64_t N,
+__global__ __launch_bounds__(256) void act_sums_kernel(const float* __restrict__ parts, int n_parts, int64_t N,
                                                        uint16_t* __restrict__ dbias) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float meet[3][64];
+#ifdef SWQ_LDS_POISON
+  lds_poison(meet, sizeof(meet), kPoisonFloat);
+  __syncthreads();
+#endif
+  const int c = threadIdx.x & 63, team = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + c;
   float sum = 0.0f;
-  for (int64_t i = 0; i < n_parts; ++i) sum += parts[i * N + n];
-  dbias[n] = to_16(sum, TYPE);
+  if (n < N) {
+#pragma unroll 8
+    for (int i = team; i < n_parts; i += 4) sum += parts[(int64_t)i * N + n];
+  }
+  if (team) meet[team - 1][c] = sum;
+  __syncthreads();
+  if (team == 0 && n < N) dbias[n] = to_16((sum + meet[0][c]) + (meet[1][c] + meet[2][c]), TYPE);
 }
 
 __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
@@ -278,17 +321,21 @@ hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, i
   });
 }
 
-int64_t act_parts(int64_t M, int64_t) { return M < kActParts ? M : kActParts; }
+// Stretches of rows: about 2048 blocks in all, four rows each at least.
+int64_t act_parts(int64_t M, int64_t N) {
+  const int64_t columns = (N + 511) / 512;
+  return std::max<int64_t>(1, std::min((M + 3) / 4, 2048 / columns));
+}
 
 hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
                                uint16_t* dbias, float* parts, hipStream_t st) {
-  const int64_t rows = (M + act_parts(M, N) - 1) / act_parts(M, N), n_parts = (M + rows - 1) / rows;
-  const dim3 grid((unsigned)((ceil8(N) + 255) / 256), (unsigned)n_parts);
+  const int64_t rows = ((M + act_parts(M, N) - 1) / act_parts(M, N) + 3) / 4 * 4, n_parts = (M + rows - 1) / rows;
+  const dim3 grid((unsigned)((N + 511) / 512), (unsigned)n_parts);
   const auto kernel = type == kTypeF16 ? act_backward_kernel<kTypeF16> : act_backward_kernel<kTypeBf16>;
   kernel<<<grid, 256, 0, st>>>(dout, z, M, N, act, rows, dz, dbias ? parts : nullptr);
   if (dbias) {
     const auto sums = type == kTypeF16 ? act_sums_kernel<kTypeF16> : act_sums_kernel<kTypeBf16>;
-    sums<<<grid.x, 256, 0, st>>>(parts, n_parts, N, dbias);
+    sums<<<(unsigned)((N + 63) / 64), 256, 0, st>>>(parts, (int)n_parts, N, dbias);
   }
   return hipGetLastError();
 }
