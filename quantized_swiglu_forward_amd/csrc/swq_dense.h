@@ -40,12 +40,24 @@ struct DenseGemm {
 // The operands of a planned product that takes whole units: rows of 16-byte units from 16-byte aligned bases, lda and ldb
 // multiples of 8, elements past R in a row's last unit zeros.
 inline bool dense_takes_units(const DenseGemm& g) { return g.kind != 0; }
-void plan_dense_gemm(DenseGemm& g);
+inline int64_t ceil8(int64_t n) { return (n + 7) / 8 * 8; }
+// (false: no launch can hold it)
+bool plan_dense_gemm(DenseGemm& g);
 int64_t dense_parts_bytes(const DenseGemm& g);
 hipError_t launch_dense_gemm(const DenseGemm& g, hipStream_t st);
-// rows of K elements to rows of ceil8(K), zeros behind
-hipError_t launch_dense_pad(const uint16_t* src, int64_t R, int64_t K, uint16_t* dst, hipStream_t st);
-inline int64_t ceil8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// The gradients of one product in one launch: x (Along, Down), w (Down, Down), both plain, and the sums of n_sums
+// partial sums [n_sums][N] (0: none).  Its blocks are set by plan_dense_pair.
+struct DensePair {
+  DenseGemm x, w;
+  int x_blocks, w_blocks, w_first;
+  int n_sums;
+  const float* sums;
+  int64_t N;
+  uint16_t* dbias;
+};
+bool plan_dense_pair(DensePair& d, bool with_x, bool with_w);
+hipError_t launch_dense_pair(const DensePair& d, int type, hipStream_t st);
 
 // A tensor [R, K] in 16 bits, or with scales as an 8-bit checkpoint (K / 32 scales a row, rounded up).
 struct Kept {
@@ -55,9 +67,8 @@ struct Kept {
 
 hipError_t launch_mx8_quantize(const void* x, int64_t R, int64_t K, int type, void* codes, uint8_t* scales,
                                hipStream_t st);
-// (rows of out are ld apart)
 hipError_t launch_mx8_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int type, void* out,
-                                 int64_t ld, hipStream_t st);
+                                 hipStream_t st);
 
 // hidden = silu(gate) up, with gate and up as checkpoints where the codes are not null
 hipError_t launch_swiglu(const uint16_t* gate, const uint16_t* up, int64_t R, int64_t K, int type, uint16_t* hidden,
@@ -65,11 +76,27 @@ hipError_t launch_swiglu(const uint16_t* gate, const uint16_t* up, int64_t R, in
 hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, int64_t R, int64_t K, int type,
                                   uint16_t* dgate, uint16_t* dup, uint16_t* hidden, hipStream_t st);
 
-// dz = dout act'(z) [M, N], rows ceil8(N) apart with zeros behind (null: not wanted), and its column sums (dbias, null: not
-// wanted); parts: float32 [act_parts(M, N)][N].
+// What a product's operands need first, in one launch: rows of 16-byte units, and dz.
+struct PrepRows {           // src [R, K] (with scales a checkpoint) to rows of ceil8(K), zeros behind
+  const void* src;
+  const uint8_t* scales;
+  int64_t R, K;
+  uint16_t* dst;            // null: nothing to do
+};
+struct Prep {
+  PrepRows rows[2];
+  // dz = dout act'(z) [M, N], rows ceil8(N) apart with zeros behind (null: not wanted), and the sums of its columns:
+  // act_parts(M, N) partial ones [..][N] in float32, or where that is 1 dbias itself (both null: not wanted)
+  const uint16_t* dout;     // null: nothing to do
+  Kept z;
+  int64_t M, N;
+  int act;
+  uint16_t* dz;
+  float* sums;
+  uint16_t* dbias;
+};
 int64_t act_parts(int64_t M, int64_t N);
-hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
-                               uint16_t* dbias, float* parts, hipStream_t st);
+hipError_t launch_prep(const Prep& p, int type, hipStream_t st);
 hipError_t launch_zero16(uint16_t* p, int64_t n, hipStream_t st);
 
 // The router's balance loss (parts: balance_workspace bytes) and the gradient of its logits.

@@ -72,7 +72,7 @@ int swiglu_q_dense_linear(const void* x, const void* W, const void* bias, const 
   g.out_type = out_mode;
   g.z = z;
   g.z_scales = (uint8_t*)z_scales;
-  plan_dense_gemm(g);
+  if (!plan_dense_gemm(g)) return SWQ_ERR_SHAPE;
   // Workspace: x and W with rows of whole 16-byte units, the partial sums of a split.
   const bool pad = K % 8 != 0 && dense_takes_units(g);
   const int64_t x_bytes = pad ? align256(M * ceil8(K) * 2) : 0, w_bytes = pad ? align256(N * ceil8(K) * 2) : 0;
@@ -81,11 +81,13 @@ int swiglu_q_dense_linear(const void* x, const void* W, const void* bias, const 
   if (rc != SWQ_OK) return rc;
   (void)hipGetLastError();            // before the first launch: an error left by others is not this call's
   if (pad) {
-    rc = check_status(launch_dense_pad(g.a, M, K, (uint16_t*)ws, stream));
-    if (rc == SWQ_OK) rc = check_status(launch_dense_pad(g.b, N, K, (uint16_t*)(ws + x_bytes), stream));
+    Prep p{};
+    p.rows[0] = {x, nullptr, M, K, (uint16_t*)ws};
+    p.rows[1] = {W, nullptr, N, K, (uint16_t*)(ws + x_bytes)};
+    rc = check_status(launch_prep(p, type, stream));
     if (rc != SWQ_OK) return rc;
-    g.a = (const uint16_t*)ws;
-    g.b = (const uint16_t*)(ws + x_bytes);
+    g.a = p.rows[0].dst;
+    g.b = p.rows[1].dst;
     g.lda = g.ldb = ceil8(K);
   }
   g.parts = (float*)(ws + x_bytes + w_bytes);
@@ -110,53 +112,51 @@ int swiglu_q_dense_linear_backward(const void* dout, const void* x, const void* 
     if (dbias && e == hipSuccess) e = launch_zero16((uint16_t*)dbias, N, stream);
     return check_status(e);
   }
-  DenseGemm gx{}, gw{};
-  gx.type = gx.out_type = gw.type = gw.out_type = type;
-  gx.way_a = kAlong;
-  gx.way_b = gw.way_a = gw.way_b = kDown;
-  gx.lda = gw.lda = ceil8(N);
-  gx.ldb = gw.ldb = ceil8(K);
-  gx.P = M, gx.Q = K, gx.R = N;
-  gw.P = N, gw.Q = K, gw.R = M;
-  gx.out = dx;
-  gw.out = dW;
-  if (dx) plan_dense_gemm(gx);
-  if (dW) plan_dense_gemm(gw);
+  DensePair d{};
+  d.x.type = d.x.out_type = d.w.type = d.w.out_type = type;
+  d.x.lda = d.w.lda = ceil8(N);
+  d.x.ldb = d.w.ldb = ceil8(K);
+  d.x.P = M, d.x.Q = K, d.x.R = N;
+  d.w.P = N, d.w.Q = K, d.w.R = M;
+  d.x.out = dx;
+  d.w.out = dW;
+  d.N = N;
+  if (!plan_dense_pair(d, dx, dW)) return SWQ_ERR_SHAPE;
   // Workspace: dz (where dout itself will not do), x and W with rows of whole 16-byte units, the partial sums of the
-  // splits, which take turns, and of the bias's gradient.
+  // splits and of the bias's gradient.
   const bool has_dz = (act != SWQ_ACT_NONE || N % 8 != 0) && (dx || dW);
   const bool has_x = dW && (x_scales || K % 8 != 0), has_w = dx && K % 8 != 0;
   const int64_t dz_bytes = has_dz ? align256(M * ceil8(N) * 2) : 0, x_bytes = has_x ? align256(M * ceil8(K) * 2) : 0;
   const int64_t w_bytes = has_w ? align256(N * ceil8(K) * 2) : 0;
-  const int64_t parts = align256(std::max(dx ? dense_parts_bytes(gx) : 0, dW ? dense_parts_bytes(gw) : 0));
-  const int64_t sums = dbias ? act_parts(M, N) * N * 4 : 0;
+  const int64_t x_parts = dx ? align256(dense_parts_bytes(d.x)) : 0, w_parts = dW ? align256(dense_parts_bytes(d.w)) : 0;
+  const int64_t n_sums = dbias ? act_parts(M, N) : 0, sums = n_sums > 1 ? n_sums * N * 4 : 0;
   char* ws = nullptr;
-  rc = take(stream_v, dz_bytes + x_bytes + w_bytes + parts + sums, &ws);
+  rc = take(stream_v, dz_bytes + x_bytes + w_bytes + x_parts + w_parts + sums, &ws);
   if (rc != SWQ_OK) return rc;
   (void)hipGetLastError();
-  uint16_t* const dz = has_dz ? (uint16_t*)ws : nullptr;
-  uint16_t* const x16 = (uint16_t*)(ws + dz_bytes);
-  uint16_t* const w16 = (uint16_t*)(ws + dz_bytes + x_bytes);
-  gx.parts = gw.parts = (float*)(ws + dz_bytes + x_bytes + w_bytes);
+  char* at = ws;
+  const auto next = [&](int64_t bytes) { return (void*)(at += bytes, at - bytes); };
+  Prep p{};
+  p.dz = has_dz ? (uint16_t*)next(dz_bytes) : nullptr;
+  if (has_x) p.rows[0] = {x, (const uint8_t*)x_scales, M, K, (uint16_t*)next(x_bytes)};
+  if (has_w) p.rows[1] = {W, nullptr, N, K, (uint16_t*)next(w_bytes)};
+  d.x.parts = (float*)next(x_parts);
+  d.w.parts = (float*)next(w_parts);
   if (has_dz || dbias) {
-    rc = check_status(launch_act_backward((const uint16_t*)dout, Kept{z, (const uint8_t*)z_scales}, M, N, type, act, dz,
-                                          (uint16_t*)dbias, (float*)((char*)gx.parts + parts), stream));
-    if (rc != SWQ_OK) return rc;
+    p.dout = (const uint16_t*)dout;
+    p.z = Kept{z, (const uint8_t*)z_scales};
+    p.M = M;
+    p.N = N;
+    p.act = act;
+    if (n_sums > 1) d.sums = p.sums = (float*)next(sums), d.n_sums = (int)n_sums, d.dbias = (uint16_t*)dbias;
+    else p.dbias = (uint16_t*)dbias;
   }
-  gx.a = gw.a = has_dz ? dz : (const uint16_t*)dout;
-  if (dx) {
-    if (has_w) rc = check_status(launch_dense_pad((const uint16_t*)W, N, K, w16, stream));
-    gx.b = has_w ? w16 : (const uint16_t*)W;
-    if (rc == SWQ_OK) rc = check_status(launch_dense_gemm(gx, stream));
-    if (rc != SWQ_OK) return rc;
-  }
-  if (dW) {
-    if (x_scales) rc = check_status(launch_mx8_dequantize(x, (const uint8_t*)x_scales, M, K, type, x16, ceil8(K), stream));
-    else if (has_x) rc = check_status(launch_dense_pad((const uint16_t*)x, M, K, x16, stream));
-    gw.b = has_x ? x16 : (const uint16_t*)x;
-    if (rc == SWQ_OK) rc = check_status(launch_dense_gemm(gw, stream));
-  }
-  return rc;
+  rc = check_status(launch_prep(p, type, stream));
+  if (rc != SWQ_OK || (!dx && !dW && !d.n_sums)) return rc;
+  d.x.a = d.w.a = has_dz ? p.dz : (const uint16_t*)dout;
+  d.x.b = has_w ? p.rows[1].dst : (const uint16_t*)W;
+  d.w.b = has_x ? p.rows[0].dst : (const uint16_t*)x;
+  return check_status(launch_dense_pair(d, type, stream));
 }
 
 int swiglu_q_mx8_quantize(const void* x, int64_t R, int64_t K, int type, void* codes, void* scales, void* stream) {
@@ -179,7 +179,7 @@ int swiglu_q_mx8_dequantize(const void* codes, const void* scales, int64_t R, in
   if (!aligned(out, type_bytes(type))) return SWQ_ERR_ALIGN;
   if (R == 0) return SWQ_OK;
   (void)hipGetLastError();
-  return check_status(launch_mx8_dequantize(codes, (const uint8_t*)scales, R, K, type, out, K, (hipStream_t)stream));
+  return check_status(launch_mx8_dequantize(codes, (const uint8_t*)scales, R, K, type, out, (hipStream_t)stream));
 }
 
 int swiglu_q_swiglu(const void* gate, const void* up, int64_t R, int64_t K, int type, void* hidden, void* gate_codes,

@@ -76,6 +76,18 @@ __device__ __forceinline__ u32x4 residual_at(const DenseGemm& g, int64_t p, int6
   return g.res && p < g.P ? load8(g.res + p * g.Q + q, n) : (u32x4){0, 0, 0, 0};
 }
 
+template <int TYPE>
+__device__ __forceinline__ void store8(uint16_t* o, const float (&v)[8], int n) {
+  if (n == 8) {
+    *(u32x4_any*)o = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
+                             pack16<TYPE>(v[6], v[7])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) o[j] = to_16(v[j], TYPE);
+  }
+}
+
 // Eight neighbouring sums of row p from column q on, n of them (0 .. 8) in the matrix; four neighbouring lanes
 // have a block of 32 columns, and all four call it.
 template <int TYPE>
@@ -105,15 +117,7 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
       }
       if ((q & 31) == 0 && n > 0) g.z_scales[p * ((g.Q + 31) / 32) + q / 32] = (uint8_t)s.byte;
     } else {
-      uint16_t* z = (uint16_t*)g.z + at;
-      if (n == 8) {
-        *(u32x4_any*)z = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
-                                 pack16<TYPE>(v[6], v[7])};
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n) z[j] = to_16(v[j], TYPE);
-      }
+      store8<TYPE>((uint16_t*)g.z + at, v, n);
     }
   }
   const auto through = [&](int act) SWQ_INLINE {
@@ -138,15 +142,7 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
         if (j < n) o[j] = v[j];
     }
   } else {
-    uint16_t* o = (uint16_t*)g.out + at;
-    if (n == 8) {
-      *(u32x4_any*)o = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
-                               pack16<TYPE>(v[6], v[7])};
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) o[j] = to_16(v[j], TYPE);
-    }
+    store8<TYPE>((uint16_t*)g.out + at, v, n);
   }
 }
 
@@ -163,8 +159,9 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
 //
 // The second operand of the products is a, so that lane 32 h + r has row r's columns 8 e + 4 h .. + 3 in elements
 // 4 e .. 4 e + 3; the sums leave through the wave's own stretch of LDS, 32 rows at a time, as whole lines.
-template <int AF, int BF, int WP, int WQ, int S>
+template <int AF_, int BF_, int WP_, int WQ_, int S_, int OCC_>
 struct DenseShape {
+  static constexpr int AF = AF_, BF = BF_, WP = WP_, WQ = WQ_, S = S_, OCC = OCC_;
   static constexpr int W = WP * WQ, BP = 32 * AF * WP, BQ = 32 * BF * WQ;
   static constexpr int STAGE_A = BP * 128, STAGE = (BP + BQ) * 128;
   static constexpr int LOADS_A = BP / (8 * W), LOADS = (BP + BQ) / (8 * W);     // per wave and stage
@@ -263,21 +260,17 @@ struct Operand {
   }
 };
 
-template <int TYPE, int WAY_A, int WAY_B, int AF, int BF, int WP, int WQ, int S, int OCC>
-__global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(DenseGemm g) {
-  using Sh = DenseShape<AF, BF, WP, WQ, S>;
-  constexpr int W = Sh::W, BP = Sh::BP, BQ = Sh::BQ;
-  __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
-#ifdef SWQ_LDS_POISON
-  lds_poison(lds, sizeof(lds), kPoisonFloat);
-  __syncthreads();
-#endif
+// A tile of g by the block: split `part` of the tile that `block` stands for (none: nothing is done).  PLAIN: nothing but the
+// sums, rounded.
+template <int TYPE, int WAY_A, int WAY_B, bool PLAIN, class Sh>
+__device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int part, char* lds) {
+  constexpr int AF = Sh::AF, BF = Sh::BF, WQ = Sh::WQ, S = Sh::S, W = Sh::W, BP = Sh::BP, BQ = Sh::BQ;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / WQ, wq = wave % WQ;
   int tp, tq;
-  if (!tile_at(blockIdx.x, (int)((g.P + BP - 1) / BP), (int)((g.Q + BQ - 1) / BQ), tp, tq)) return;
+  if (!tile_at(block, (int)((g.P + BP - 1) / BP), (int)((g.Q + BQ - 1) / BQ), tp, tq)) return;
   const int64_t p0 = (int64_t)tp * BP, q0 = (int64_t)tq * BQ;
-  const int64_t r0 = (int64_t)blockIdx.y * g.split_len, r1 = min(r0 + g.split_len, g.R);
+  const int64_t r0 = (int64_t)part * g.split_len, r1 = min(r0 + g.split_len, g.R);
   const int stages = (int)((r1 - r0 + 63) / 64);
 
   Operand<WAY_A, BP, W> oa;
@@ -363,9 +356,10 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(
   // The residual comes a round of 32 rows ahead.
   constexpr int PASSES = 32 / ROWS;
   const int64_t pw = p0 + wp * 32 * AF + lane / LANES;
-  const u32x4 bias = g.parts ? (u32x4){0, 0, 0, 0} : bias_at(g, q, n);
+  const bool whole = g.splits <= 1, ahead_too = !PLAIN && whole && g.res;
+  const u32x4 bias = PLAIN || !whole ? (u32x4){0, 0, 0, 0} : bias_at(g, q, n);
   u32x4 ahead[PASSES] = {};
-  if (g.res && !g.parts) {
+  if (ahead_too) {
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) ahead[k] = residual_at(g, pw + k * ROWS, q, n);
   }
@@ -383,28 +377,75 @@ __global__ __launch_bounds__(64 * WP * WQ, OCC * WP * WQ / 4) void dense_kernel(
       const f32x4 x = *(const f32x4*)(buf + row * Sh::PITCH + col), y = *(const f32x4*)(buf + row * Sh::PITCH + col + 4);
       float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
       const u32x4 residual = ahead[0];
-      if constexpr (i + 1 < AF) {
-        if (g.res && !g.parts) {
-#pragma unroll
-          for (int e = 0; e + 1 < PASSES; ++e) ahead[e] = ahead[e + 1];
-          ahead[PASSES - 1] = residual_at(g, p + 32, q, n);
-        }
-      } else {
+      if (ahead_too) {
 #pragma unroll
         for (int e = 0; e + 1 < PASSES; ++e) ahead[e] = ahead[e + 1];
+        if constexpr (i + 1 < AF) ahead[PASSES - 1] = residual_at(g, p + 32, q, n);
       }
       if (p >= g.P) continue;
-      if (g.parts) {
+      if (!whole) {
         if (n > 0) {
-          float* o = g.parts + ((int64_t)blockIdx.y * g.P + p) * g.part_ld + q;
+          float* o = g.parts + ((int64_t)part * g.P + p) * g.part_ld + q;
           *(f32x4*)o = x;
           *(f32x4*)(o + 4) = y;
         }
+      } else if constexpr (PLAIN) {
+        store8<TYPE>((uint16_t*)g.out + p * g.Q + q, v, n);
       } else {
         finish8<TYPE>(g, v, p, q, n, bias, residual);
       }
     }
   });
+}
+
+template <int TYPE, class Sh>
+__global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_kernel(DenseGemm g) {
+  __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
+  dense_tile<TYPE, kAlong, kAlong, false, Sh>(g, blockIdx.x, blockIdx.y, lds);
+}
+
+// The gradients by x and by W in one launch, the longer tiles first, so that each fills the CUs that the other leaves
+// idle; behind them the bias's gradient, the sums of the stretches' sums, 64 columns a block.  (2048 x 4096 x 14336, one launch
+// each: 212 and 239 us.)
+template <int TYPE, class Sh>
+__global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_pair_kernel(DensePair d) {
+  __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
+#ifdef SWQ_LDS_POISON
+  lds_poison(lds, sizeof(lds), kPoisonFloat);
+  __syncthreads();
+#endif
+  int block = blockIdx.x;
+  const int first = d.w_first ? d.w_blocks : d.x_blocks, both = d.x_blocks + d.w_blocks;
+  if (block < both) {
+    const bool of_w = (block < first) == (d.w_first != 0);
+    if (block >= first) block -= first;
+    if (of_w) {
+      const int each = d.w_blocks / d.w.splits;
+      dense_tile<TYPE, kDown, kDown, true, Sh>(d.w, block % each, block / each, lds);
+    } else {
+      const int each = d.x_blocks / d.x.splits;
+      dense_tile<TYPE, kAlong, kDown, true, Sh>(d.x, block % each, block / each, lds);
+    }
+    return;
+  }
+  const int c = threadIdx.x & 63, team = threadIdx.x >> 6;
+  const int64_t n = (int64_t)(block - both) * 64 + c;
+  float sum = 0.0f;
+  if (n < d.N) {
+#pragma unroll 8
+    for (int i = team; i < d.n_sums; i += Sh::W) sum += d.sums[(int64_t)i * d.N + n];
+  }
+  float* meet = (float*)lds;
+  meet[threadIdx.x] = sum;
+  __syncthreads();
+  if (team == 0 && n < d.N) {
+    for (int i = 1; i < Sh::W; ++i) sum += meet[64 * i + c];
+    d.dbias[n] = to_16(sum, TYPE);
+  }
 }
 
 // The sums of a split, added in its order.
@@ -424,24 +465,6 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t p
     }
   }
   finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
-}
-
-// Rows of another length: dst[r, 0 .. ceil8(K)) = src[r, 0 .. K), zeros behind.  A thread has eight elements at a time.
-__global__ __launch_bounds__(256) void dense_pad_kernel(const uint16_t* __restrict__ src, int64_t K, uint32_t per_row,
-                                                        int64_t n, uint16_t* __restrict__ dst) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per_row, k = 8 * (i - r * per_row);
-    u32x4 w = {0, 0, 0, 0};
-    const uint16_t* s = src + r * K + k;
-    if (k + 8 <= K) {
-      w = *(const u32x4_any*)s;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (k + j < K) w[j >> 1] |= (uint32_t)s[j] << (16 * (j & 1));
-    }
-    *(u32x4*)(dst + 8 * i) = w;
-  }
 }
 
 // ----------------------------------------------------------------- few rows ----
@@ -548,90 +571,154 @@ void launch_few(const DenseGemm& g, hipStream_t st) {
 enum : int { kFewRows = 0, kTiles64 = 1, kTiles128 = 2, kTiles256 = 3 };
 constexpr int kSide[] = {0, 64, 128, 256};
 
-template <int TYPE, int WA, int WB>
-void launch_tiles(const DenseGemm& g, hipStream_t st) {
-  const int64_t side = kSide[g.kind], tiles = (g.P + side - 1) / side * ((g.Q + side - 1) / side);
-  const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)g.splits);
-  switch (g.kind) {
-    case kTiles256: dense_kernel<TYPE, WA, WB, 4, 2, 2, 4, 2, 1><<<grid, 512, 0, st>>>(g); break;
-    case kTiles128: dense_kernel<TYPE, WA, WB, 2, 2, 2, 2, 2, 2><<<grid, 256, 0, st>>>(g); break;
-    default: dense_kernel<TYPE, WA, WB, 1, 1, 2, 2, 4, 2><<<grid, 256, 0, st>>>(g); break;
-  }
+using Shape256 = DenseShape<4, 2, 2, 4, 2, 1>;
+using Shape128 = DenseShape<2, 2, 2, 2, 2, 2>;
+using Shape64 = DenseShape<1, 1, 2, 2, 4, 2>;
+
+int64_t tiles_of(const DenseGemm& g, int kind) {
+  const int64_t side = kSide[kind];
+  return (g.P + side - 1) / side * ((g.Q + side - 1) / side);
+}
+int64_t blocks_of(const DenseGemm& g) { return (tiles_of(g, g.kind) + 7) / 8 * 8; }     // (eight XCDs)
+
+template <int TYPE>
+void launch_forward(const DenseGemm& g, hipStream_t st) {
+  const dim3 grid((unsigned)blocks_of(g), (unsigned)g.splits);
+  if (g.kind == kTiles256) dense_kernel<TYPE, Shape256><<<grid, 512, 0, st>>>(g);
+  else if (g.kind == kTiles128) dense_kernel<TYPE, Shape128><<<grid, 256, 0, st>>>(g);
+  else dense_kernel<TYPE, Shape64><<<grid, 256, 0, st>>>(g);
 }
 
 template <int TYPE>
-void launch_ways(const DenseGemm& g, hipStream_t st) {
-  if (g.way_a == kDown) launch_tiles<TYPE, kDown, kDown>(g, st);
-  else if (g.way_b == kDown) launch_tiles<TYPE, kAlong, kDown>(g, st);
-  else launch_tiles<TYPE, kAlong, kAlong>(g, st);
+void launch_pair(const DensePair& d, int kind, unsigned blocks, hipStream_t st) {
+  if (kind == kTiles256) dense_pair_kernel<TYPE, Shape256><<<blocks, 512, 0, st>>>(d);
+  else if (kind == kTiles128) dense_pair_kernel<TYPE, Shape128><<<blocks, 256, 0, st>>>(d);
+  else dense_pair_kernel<TYPE, Shape64><<<blocks, 256, 0, st>>>(d);
+}
+
+void launch_join(const DenseGemm& g, hipStream_t st) {
+  const uint32_t per_row = (uint32_t)((g.Q + 31) / 32 * 4);
+  const unsigned blocks = (unsigned)((g.P * per_row + 255) / 256);
+  if (g.type == kTypeF16) dense_join_kernel<kTypeF16><<<blocks, 256, 0, st>>>(g, per_row);
+  else dense_join_kernel<kTypeBf16><<<blocks, 256, 0, st>>>(g, per_row);
+}
+
+// One launch holds fewer than 2^32 threads (of more the rest is left out, with no error); splits are for few tiles.
+bool launch_holds(const DenseGemm* g, int kind) {
+  return !g || tiles_of(*g, kind) * (kind == kTiles256 ? 512 : 256) < (int64_t(1) << 31);
+}
+
+void split_into(DenseGemm& g, int64_t splits) {
+  const int64_t stages = (g.R + 63) / 64, len = (stages + splits - 1) / splits;
+  g.splits = (int)((stages + len - 1) / len);
+  g.split_len = len * 64;
+  g.part_ld = ceil8(g.Q);
 }
 
 }  // namespace
 
 // The few-row kernel up to 16 rows, and up to 64 where a row's length is no multiple of 8, which the tiles would have
 // copied first (rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 8.5 / 10.2, 16 x 4096 x 4096 9.9 / 10.5,
-// 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 11 / 18).  Else the tile shape and the split of the inner indexes whose
-// fullest CU is done first, in us.  Measured: a CU takes 0.2 us per stage of a 64 x 64 tile,
-// 0.46 of a 128 x 128 one (alone on its CU 0.47, 0.72 where all CUs are busy) and 1.1 of a 256 x 256 one, 1.5 where all CUs are
-// busy and the card's power limits them; a split writes and reads its float32 sums at 5.5 TB/s and takes
-// another launch.  (tiles of 256 / 128 / 64, us: 2048 x 4096 x 14336 194 / 226 / 358, 512 x 2048 x 5632 44 / 26 / 24,
-// 128 x 2048 x 5632 41 / 19 / 11; its gradient by x, four splits of 64 14, one 27.)
+// 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 11 / 18).
 constexpr int64_t kFewRowsMost = 16, kFewRowsOdd = 64;
-void plan_dense_gemm(DenseGemm& g) {
+
+// The tile shape, one for both of a pair, and the splits of the inner indexes, by the time in us at which the CUs are done.
+// Measured: a CU takes 0.2 us per stage of a 64 x 64 tile, 0.46 of a 128 x 128 one (alone on its CU
+// 0.47, 0.72 where all CUs are busy) and 1.1 of a 256 x 256 one, 1.5 where all CUs are busy and the card's power limits
+// them; a split writes and reads its float32 sums at 5.5 TB/s and takes another launch.  A product alone goes
+// in rounds of tiles; of a pair the longer tiles begin and the shorter ones fill the gaps.  (tiles of 256 / 128 / 64, us: 2048 x 4096 x
+// 14336 194 / 226 / 358, 512 x 2048 x 5632 44 / 26 / 24, 128 x 2048 x 5632 41 / 19 / 11; its gradient by
+// x, four splits of 64 14, one 27.)
+bool plan_tiles(DenseGemm* x, DenseGemm* w) {
   const int cus = device_cus();
-  const int64_t stages = (g.R + 63) / 64;
-  g.part_ld = ceil8(g.Q);
-  g.splits = 1;
-  g.split_len = stages * 64;
-  if (g.way_a == kAlong && g.way_b == kAlong && (g.P <= kFewRowsMost || (g.P <= kFewRowsOdd && g.R % 8 != 0))) {
-    g.kind = kFewRows;
-    return;
-  }
+  static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  DenseGemm* const g[2] = {x ? x : w, x && w ? w : nullptr};
   double best = 1e300;
-  int64_t splits = 1;
-  for (int kind = kTiles64; kind <= kTiles256; ++kind) {
-    const int64_t side = kSide[kind], tiles = (g.P + side - 1) / side * ((g.Q + side - 1) / side);
-    const int64_t most = tiles >= cus ? 2 : std::min<int64_t>(16, stages);
-    for (int64_t s = 1; s <= most; ++s) {
-      const int64_t len = (stages + s - 1) / s, blocks = tiles * s, n = (blocks + cus - 1) / cus;
-      const double load = blocks < cus ? (double)blocks / cus : 1.0;
-      const double each = kind == kTiles256 ? 2.2 + len * (1.1 + 0.4 * load)
-                          : kind == kTiles128 ? 0.7 + len * (n > 1 ? 0.46 : 0.47 + 0.25 * load)
-                                              : 0.3 + len * (n > 1 ? 0.2 : 0.23);
-      const double join = s > 1 ? 2.0 + (8.0 * s + 2.0) * g.P * g.Q / 5.5e6 : 0.0;
-      if (n * each + join < best) best = n * each + join, g.kind = kind, splits = s;
+  int kind = kTiles64;
+  int64_t splits[2] = {1, 1};
+  for (int k = kTiles64; k <= kTiles256; ++k) {
+    if (!launch_holds(g[0], k) || !launch_holds(g[1], k)) continue;
+    const auto block_us = [&](int64_t stages, double load, bool alone) {
+      return k == kTiles256 ? 2.2 + stages * (1.1 + 0.4 * load)
+             : k == kTiles128 ? 0.7 + stages * (alone ? 0.47 + 0.25 * load : 0.46) : 0.3 + stages * (alone ? 0.23 : 0.2);
+    };
+    struct Cost {
+      int64_t blocks, len;
+      double join;
+    } c[2][8];
+    int n[2] = {0, 0};
+    for (int i = 0; i < 2 && g[i]; ++i) {
+      const int64_t stages = (g[i]->R + 63) / 64, tiles = tiles_of(*g[i], k);
+      for (int s : kSplits) {
+        if (s > 1 && (s > stages || tiles * s > 4 * cus)) break;
+        c[i][n[i]++] = {tiles * s, (stages + s - 1) / s, s > 1 ? 4.0 + (8.0 * s + 2.0) * g[i]->P * g[i]->Q / 5.5e6 : 0.0};
+      }
+    }
+    for (int i = 0; i < n[0]; ++i) {
+      for (int j = 0; j < (g[1] ? n[1] : 1); ++j) {
+        const int64_t blocks = c[0][i].blocks + (g[1] ? c[1][j].blocks : 0);
+        const double load = blocks < cus ? (double)blocks / cus : 1.0;
+        double us;
+        if (!g[1]) {
+          const int64_t rounds = (blocks + cus - 1) / cus;
+          us = rounds * block_us(c[0][i].len, load, rounds == 1) + c[0][i].join;
+        } else {
+          const double a = block_us(c[0][i].len, load, false), b = block_us(c[1][j].len, load, false);
+          const double longest = block_us(std::max(c[0][i].len, c[1][j].len), load, true);
+          us = (c[0][i].blocks * a + c[1][j].blocks * b) / cus + 0.5 * std::min(a, b);
+          us = std::max(us, longest) + c[0][i].join + c[1][j].join;
+        }
+        if (us < best) {
+          best = us, kind = k;
+          splits[0] = c[0][i].blocks / tiles_of(*g[0], k);
+          splits[1] = g[1] ? c[1][j].blocks / tiles_of(*g[1], k) : 1;
+        }
+      }
     }
   }
-  const int64_t len = (stages + splits - 1) / splits;
-  g.splits = (int)((stages + len - 1) / len);
-  g.split_len = len * 64;
+  for (int i = 0; i < 2 && g[i]; ++i) {
+    g[i]->kind = kind;
+    split_into(*g[i], splits[i]);
+  }
+  return best < 1e300;
+}
+
+bool plan_dense_gemm(DenseGemm& g) {
+  if (g.P > kFewRowsMost && (g.P > kFewRowsOdd || g.R % 8 == 0)) return plan_tiles(&g, nullptr);
+  g.kind = kFewRows;
+  split_into(g, 1);
+  return true;
+}
+
+bool plan_dense_pair(DensePair& d, bool with_x, bool with_w) {
+  if ((with_x || with_w) && !plan_tiles(with_x ? &d.x : nullptr, with_w ? &d.w : nullptr)) return false;
+  d.x_blocks = with_x ? (int)(blocks_of(d.x) * d.x.splits) : 0;
+  d.w_blocks = with_w ? (int)(blocks_of(d.w) * d.w.splits) : 0;
+  d.w_first = with_w && d.w.split_len > d.x.split_len;
+  return true;
 }
 
 int64_t dense_parts_bytes(const DenseGemm& g) { return g.splits > 1 ? g.splits * g.P * g.part_ld * 4 : 0; }
 
-hipError_t launch_dense_pad(const uint16_t* src, int64_t R, int64_t K, uint16_t* dst, hipStream_t st) {
-  const int64_t per_row = (K + 7) / 8, n = R * per_row;
-  const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20);
-  dense_pad_kernel<<<blocks, 256, 0, st>>>(src, K, (uint32_t)per_row, n, dst);
-  return hipGetLastError();
-}
-
-hipError_t launch_dense_gemm(const DenseGemm& p, hipStream_t st) {
-  DenseGemm g = p;
-  if (g.splits <= 1) g.parts = nullptr;
+hipError_t launch_dense_gemm(const DenseGemm& g, hipStream_t st) {
   if (g.kind == kFewRows) {
     if (g.type == kTypeF16) launch_few<kTypeF16>(g, st);
     else launch_few<kTypeBf16>(g, st);
     return hipGetLastError();
   }
-  if (g.type == kTypeF16) launch_ways<kTypeF16>(g, st);
-  else launch_ways<kTypeBf16>(g, st);
-  if (g.splits > 1) {
-    const uint32_t per_row = (uint32_t)((g.Q + 31) / 32 * 4);
-    const unsigned blocks = (unsigned)((g.P * per_row + 255) / 256);
-    if (g.type == kTypeF16) dense_join_kernel<kTypeF16><<<blocks, 256, 0, st>>>(g, per_row);
-    else dense_join_kernel<kTypeBf16><<<blocks, 256, 0, st>>>(g, per_row);
-  }
+  if (g.type == kTypeF16) launch_forward<kTypeF16>(g, st);
+  else launch_forward<kTypeBf16>(g, st);
+  if (g.splits > 1) launch_join(g, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_dense_pair(const DensePair& d, int type, hipStream_t st) {
+  const int kind = d.x_blocks ? d.x.kind : d.w_blocks ? d.w.kind : kTiles64;
+  const unsigned blocks = (unsigned)(d.x_blocks + d.w_blocks + (d.n_sums ? (d.N + 63) / 64 : 0));
+  if (type == kTypeF16) launch_pair<kTypeF16>(d, kind, blocks, st);
+  else launch_pair<kTypeBf16>(d, kind, blocks, st);
+  if (d.x_blocks && d.x.splits > 1) launch_join(d.x, st);
+  if (d.w_blocks && d.w.splits > 1) launch_join(d.w, st);
   return hipGetLastError();
 }
 

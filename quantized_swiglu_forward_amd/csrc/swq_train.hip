@@ -17,14 +17,13 @@ struct Pieces {
 struct Piece {
   int64_t at;               // its first element
   int64_t block;            // its block's scale
-  int64_t row;
   int n;                    // elements, 0 .. 8
 };
 __device__ __forceinline__ Piece piece_of(const Pieces& t, int64_t i) {
   const int64_t row = i / t.per_row;
   const uint32_t c = (uint32_t)(i - row * t.per_row);
   const int64_t left = t.K - 8 * (int64_t)c;
-  return {row * t.K + 8 * (int64_t)c, row * (t.per_row / 4) + (c >> 2), row, left >= 8 ? 8 : left > 0 ? (int)left : 0};
+  return {row * t.K + 8 * (int64_t)c, row * (t.per_row / 4) + (c >> 2), left >= 8 ? 8 : left > 0 ? (int)left : 0};
 }
 
 template <int TYPE>
@@ -127,14 +126,13 @@ __global__ __launch_bounds__(256) void mx8_quantize_kernel(const void* __restric
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx8_dequantize_kernel(const void* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, Pieces t,
-                                                             int64_t first, int64_t end, void* __restrict__ out,
-                                                             int64_t ld) {
+                                                             int64_t first, int64_t end, void* __restrict__ out) {
   const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= end) return;
   const Piece p = piece_of(t, i);
   float v[8];
   decode8(codes, mx8_scale(scales[p.block]), p.at, p.n, v);
-  store8<TYPE>(out, p.at + p.row * (ld - t.K), p.n, v);
+  store8<TYPE>(out, p.at, p.n, v);
 }
 
 template <int TYPE>
@@ -206,28 +204,24 @@ hipError_t over_pieces(int64_t R, int64_t K, F launch) {
 }
 
 // dz and the sums of its columns.  A block has 512 columns (a thread eight of them) of a stretch of rows, four rows at
-// a time; the four meet in LDS, the stretches in a second kernel, both in order.
+// a time; the four meet in LDS, the stretches' sums in a later kernel, all in order.
 template <int TYPE>
-__global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __restrict__ dout, Kept z, int64_t M,
-                                                           int64_t N, int act, int64_t rows,
-                                                           uint16_t* __restrict__ dz, float* __restrict__ parts) {
-  __shared__ float meet[3][64][8];
-#ifdef SWQ_LDS_POISON
-  lds_poison(meet, sizeof(meet), kPoisonFloat);
-  __syncthreads();
-#endif
+__device__ __forceinline__ void act_backward(const Prep& p, int64_t column_block, int64_t stretch, int64_t rows,
+                                             float (*meet)[64][8]) {
+  const Kept& z = p.z;
+  const int64_t M = p.M, N = p.N;
   const int c = threadIdx.x & 63, team = threadIdx.x >> 6;
-  const int64_t q = (int64_t)blockIdx.x * 512 + 8 * c, blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
+  const int64_t q = column_block * 512 + 8 * c, blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
   const int n = q + 8 <= N ? 8 : q < N ? (int)(N - q) : 0;
-  const int64_t m1 = min((int64_t)(blockIdx.y + 1) * rows, M);
+  const int64_t m1 = min((stretch + 1) * rows, M);
   float sum[8] = {};
   const auto go = [&](auto slope) SWQ_INLINE {
     if (n > 0) {
 #pragma unroll 2
-      for (int64_t m = (int64_t)blockIdx.y * rows + team; m < m1; m += 4) {
-        float d[8], v[8];
-        load8<TYPE>(dout, m * N + q, n, d);
-        if (act != kActNone) {
+      for (int64_t m = stretch * rows + team; m < m1; m += 4) {
+        float d[8], v[8] = {};
+        load8<TYPE>(p.dout, m * N + q, n, d);
+        if (p.act != kActNone) {
           if (z.scales) decode8(z.data, mx8_scale(z.scales[m * blocks + q / 32]), m * N + q, n, v);
           else load8<TYPE>(z.data, m * N + q, n, v);
         }
@@ -236,18 +230,18 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
           d[j] = j < n ? d[j] * slope(v[j]) : 0.0f;
           sum[j] += d[j];
         }
-        if (dz) store8<TYPE>(dz, m * ld + q, 8, d);          // (zeros behind a row's end)
+        if (p.dz) store8<TYPE>(p.dz, m * ld + q, 8, d);      // (zeros behind a row's end)
       }
     }
   };
-  switch (act) {
+  switch (p.act) {
     case kActNone: go([](float) { return 1.0f; }); break;
     case kActRelu: go([](float v) { return activate_slope(v, kActRelu); }); break;
     case kActSilu: go([](float v) { return activate_slope(v, kActSilu); }); break;
     case kActGelu: go([](float v) { return activate_slope(v, kActGelu); }); break;
     default: go([](float v) { return activate_slope(v, kActGeluTanh); });
   }
-  if (!parts) return;
+  if (!p.sums && !p.dbias) return;
   if (team) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) meet[team - 1][c][j] = sum[j];
@@ -255,30 +249,44 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const uint16_t* __res
   __syncthreads();
   if (team == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) parts[(int64_t)blockIdx.y * N + q + j] = (sum[j] + meet[0][c][j]) + (meet[1][c][j] + meet[2][c][j]);
+    for (int j = 0; j < 8; ++j) {
+      if (j >= n) continue;
+      const float all = (sum[j] + meet[0][c][j]) + (meet[1][c][j] + meet[2][c][j]);
+      if (p.dbias) p.dbias[q + j] = to_16(all, TYPE);
+      else p.sums[stretch * N + q + j] = all;
+    }
   }
 }
 
-// 64 columns per block, four threads a column.
+// Rows to whole units; a checkpoint's to its values.
 template <int TYPE>
-__global__ __launch_bounds__(256) void act_sums_kernel(const float* __restrict__ parts, int n_parts, int64_t N,
-                                                       uint16_t* __restrict__ dbias) {
-  __shared__ float meet[3][64];
+__device__ __forceinline__ void prep_rows(const PrepRows& r, int64_t block, int64_t blocks) {
+  const uint32_t per_row = (uint32_t)((r.K + 7) / 8);
+  const int64_t all = r.R * per_row, scale_row = (r.K + 31) / 32;
+  for (int64_t i = block * 256 + threadIdx.x; i < all; i += blocks * 256) {
+    const int64_t row = i / per_row;
+    const uint32_t c = (uint32_t)(i - row * per_row);
+    const int64_t at = row * r.K + 8 * (int64_t)c, left = r.K - 8 * (int64_t)c;
+    float v[8];
+    if (r.scales) decode8(r.src, mx8_scale(r.scales[row * scale_row + (c >> 2)]), at, left < 8 ? (int)left : 8, v);
+    else load8<TYPE>(r.src, at, left < 8 ? (int)left : 8, v);
+    store8<TYPE>(r.dst, 8 * i, 8, v);
+  }
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void prep_kernel(Prep p, int column_blocks, int act_blocks, int64_t rows, int blocks0,
+                                                   int blocks1) {
+  __shared__ float meet[3][64][8];
 #ifdef SWQ_LDS_POISON
   lds_poison(meet, sizeof(meet), kPoisonFloat);
   __syncthreads();
 #endif
-  const int c = threadIdx.x & 63, team = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + c;
-  float sum = 0.0f;
-  if (n < N) {
-#pragma unroll 8
-    for (int i = team; i < n_parts; i += 4) sum += parts[(int64_t)i * N + n];
-  }
-  if (team) meet[team - 1][c] = sum;
-  __syncthreads();
-  if (team == 0 && n < N) dbias[n] = to_16((sum + meet[0][c]) + (meet[1][c] + meet[2][c]), TYPE);
+  int b = blockIdx.x;
+  if (b < act_blocks) return act_backward<TYPE>(p, b % column_blocks, b / column_blocks, rows, meet);
+  b -= act_blocks;
+  if (b < blocks0) return prep_rows<TYPE>(p.rows[0], b, blocks0);
+  prep_rows<TYPE>(p.rows[1], b - blocks0, blocks1);
 }
 
 __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
@@ -297,11 +305,11 @@ hipError_t launch_mx8_quantize(const void* x, int64_t R, int64_t K, int type, vo
 }
 
 hipError_t launch_mx8_dequantize(const void* codes, const uint8_t* scales, int64_t R, int64_t K, int type, void* out,
-                                 int64_t ld, hipStream_t st) {
+                                 hipStream_t st) {
   return over_pieces(R, K, [&](dim3 grid, Pieces t, int64_t i, int64_t end) {
-    if (type == kTypeF32) mx8_dequantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out, ld);
-    else if (type == kTypeF16) mx8_dequantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out, ld);
-    else mx8_dequantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out, ld);
+    if (type == kTypeF32) mx8_dequantize_kernel<kTypeF32><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
+    else if (type == kTypeF16) mx8_dequantize_kernel<kTypeF16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
+    else mx8_dequantize_kernel<kTypeBf16><<<grid, 256, 0, st>>>(codes, scales, t, i, end, out);
   });
 }
 
@@ -321,22 +329,25 @@ hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, i
   });
 }
 
-// Stretches of rows: about 2048 blocks in all, four rows each at least.
+// Stretches of rows: about 2048 blocks in all, four rows each at least, one up to sixteen rows.
 int64_t act_parts(int64_t M, int64_t N) {
   const int64_t columns = (N + 511) / 512;
-  return std::max<int64_t>(1, std::min((M + 3) / 4, 2048 / columns));
+  if (M <= 16) return 1;
+  const int64_t parts = std::max<int64_t>(1, std::min((M + 3) / 4, 2048 / columns));
+  const int64_t rows = ((M + parts - 1) / parts + 3) / 4 * 4;
+  return (M + rows - 1) / rows;
 }
 
-hipError_t launch_act_backward(const uint16_t* dout, Kept z, int64_t M, int64_t N, int type, int act, uint16_t* dz,
-                               uint16_t* dbias, float* parts, hipStream_t st) {
-  const int64_t rows = ((M + act_parts(M, N) - 1) / act_parts(M, N) + 3) / 4 * 4, n_parts = (M + rows - 1) / rows;
-  const dim3 grid((unsigned)((N + 511) / 512), (unsigned)n_parts);
-  const auto kernel = type == kTypeF16 ? act_backward_kernel<kTypeF16> : act_backward_kernel<kTypeBf16>;
-  kernel<<<grid, 256, 0, st>>>(dout, z, M, N, act, rows, dz, dbias ? parts : nullptr);
-  if (dbias) {
-    const auto sums = type == kTypeF16 ? act_sums_kernel<kTypeF16> : act_sums_kernel<kTypeBf16>;
-    sums<<<(unsigned)((N + 63) / 64), 256, 0, st>>>(parts, (int)n_parts, N, dbias);
-  }
+hipError_t launch_prep(const Prep& p, int type, hipStream_t st) {
+  const int64_t columns = (p.N + 511) / 512, parts = p.dout ? act_parts(p.M, p.N) : 0;
+  const int64_t rows = p.dout ? ((p.M + parts - 1) / parts + 3) / 4 * 4 : 0;
+  const auto blocks_for = [](const PrepRows& r) {
+    return r.dst ? (int)std::min<int64_t>((r.R * ((r.K + 7) / 8) + 255) / 256, 4096) : 0;
+  };
+  const int n0 = blocks_for(p.rows[0]), n1 = blocks_for(p.rows[1]), act = (int)(columns * parts);
+  if (act + n0 + n1 == 0) return hipSuccess;
+  const auto kernel = type == kTypeF16 ? prep_kernel<kTypeF16> : prep_kernel<kTypeBf16>;
+  kernel<<<(unsigned)(act + n0 + n1), 256, 0, st>>>(p, (int)columns, act, rows, n0, n1);
   return hipGetLastError();
 }
 
