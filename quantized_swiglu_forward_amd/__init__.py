@@ -421,10 +421,11 @@ _dtypes = ()     # SWQ_TYPE_* -> torch type
 _words = ()      # types of codes
 _bytes = _int8 = _int32 = _float32 = None
 _raw_stream = _device_now = _on_device = None   # torch's current stream of a GPU, current GPU, GPU guard
+_fresh = None    # torch's allocation by shape and strides on the current GPU
 
 
 def _load_types():
-    global _types, _dtypes, _words, _bytes, _int8, _int32, _float32, _raw_stream, _device_now, _on_device
+    global _types, _dtypes, _words, _bytes, _int8, _int32, _float32, _raw_stream, _device_now, _on_device, _fresh
     import torch
     _dtypes = (torch.bfloat16, torch.float32, torch.float16)
     _words = (torch.int32, torch.uint32)
@@ -433,6 +434,9 @@ def _load_types():
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _on_device = torch.cuda.device
+    guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+    _fresh = getattr(guards, "_empty_strided_cuda", None) or (
+        lambda shape, stride, dtype: torch.empty_strided(shape, stride, dtype=dtype, device="cuda"))
     _types = {t: i for i, t in enumerate(_dtypes)}
     return _types
 
@@ -474,6 +478,20 @@ def _mx4_shape(codes, scales, what, K=-1, dims=2):
     if K == 0:                                # (so that the callers' test for no rows is x.numel() == 0)
         raise ValueError(f"{what}: a product needs inputs (K = 0)")
     return c[:-1]
+
+
+def _new(shape, dtype, x, dev):
+    """An uninitialised tensor on x's GPU dev (new_empty takes half as long again)."""
+    if dev != _device_now():
+        return x.new_empty(shape, dtype=dtype)
+    if len(shape) == 2:                      # (tuples, as it insists on)
+        r, c = shape
+        return _fresh((r, c), (c or 1, 1), dtype)
+    stride, step = [], 1
+    for k in reversed(shape):
+        stride.append(step)
+        step *= k or 1
+    return _fresh(tuple(shape), tuple(stride[::-1]), dtype)
 
 
 def _out(out, shape, dtype, x, what):
@@ -697,9 +715,9 @@ def mx8_quantize(x, codes=None, scales=None, stream=None):
         raise ValueError("mx8_quantize: the last dimension must not be empty")
     dev = _same_place("mx8_quantize", x)
     K, n, lead = shape[-1], x.numel(), shape[:-1]
-    codes = x.new_empty(shape, dtype=_int8) if codes is None else _out(codes, shape, _int8, x, "mx8_quantize codes")
+    codes = _new(shape, _int8, x, dev) if codes is None else _out(codes, shape, _int8, x, "mx8_quantize codes")
     each = lead + ((K + 31) // 32,)
-    scales = (x.new_empty(each, dtype=_bytes) if scales is None
+    scales = (_new(each, _bytes, x, dev) if scales is None
               else _out(scales, each, _bytes, x, "mx8_quantize scales"))
     if n:
         _call((_lib or lib()).swiglu_q_mx8_quantize, dev, stream, x.data_ptr(), n // K, K, t, codes.data_ptr(),
@@ -713,7 +731,7 @@ def mx8_dequantize(codes, scales, dtype=None, out=None, stream=None):
     dtype = _dtypes[0] if dtype is None else dtype
     dev = _same_place("mx8_dequantize", codes, scales)
     shape, n = codes.shape, codes.numel()
-    out = codes.new_empty(shape, dtype=dtype) if out is None else _out(out, shape, dtype, codes, "mx8_dequantize")
+    out = _new(shape, dtype, codes, dev) if out is None else _out(out, shape, dtype, codes, "mx8_dequantize")
     t = _type(out, "mx8_dequantize")
     if n:
         _call((_lib or lib()).swiglu_q_mx8_dequantize, dev, stream, codes.data_ptr(), scales.data_ptr(),
@@ -739,12 +757,12 @@ def dense_linear(x, w, bias=None, act=SWQ_ACT_NONE, residual=None, keep=None, ou
     shape = lead + (N,)
     res = _residual(residual, x, shape, "dense_linear")
     dev = _same_place("dense_linear", x, w, bias, residual)
-    out = x.new_empty(shape, dtype=_dtypes[mode]) if out is None else _out(out, shape, _dtypes[mode], x, "dense_linear")
+    out = _new(shape, _dtypes[mode], x, dev) if out is None else _out(out, shape, _dtypes[mode], x, "dense_linear")
     z = scales = None
     if keep == "same":
-        kept = z = x.new_empty(shape)
+        kept = z = _new(shape, x.dtype, x, dev)
     elif keep == "mx8":
-        kept = z, scales = x.new_empty(shape, dtype=_int8), x.new_empty(lead + ((N + 31) // 32,), dtype=_bytes)
+        kept = z, scales = _new(shape, _int8, x, dev), _new(lead + ((N + 31) // 32,), _bytes, x, dev)
     elif keep is not None:
         raise ValueError('dense_linear: keep must be None, "same" or "mx8"')
     n = x.numel()
@@ -779,16 +797,16 @@ def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True
     if not want_x:
         dx = None
     else:
-        dx = (dout.new_empty(lead + (K,)) if dx is None
+        dx = (_new(lead + (K,), dtype, dout, dev) if dx is None
               else _out(dx, lead + (K,), dtype, dout, "dense_linear_backward dx"))
     if not want_w:
         dw = None
     else:
-        dw = dout.new_empty((N, K)) if dw is None else _out(dw, (N, K), dtype, dout, "dense_linear_backward dw")
+        dw = _new((N, K), dtype, dout, dev) if dw is None else _out(dw, (N, K), dtype, dout, "dense_linear_backward dw")
     if not want_b:
         dbias = None
     else:
-        dbias = dout.new_empty((N,)) if dbias is None else _out(dbias, (N,), dtype, dout, "dense_linear_backward dbias")
+        dbias = _new((N,), dtype, dout, dev) if dbias is None else _out(dbias, (N,), dtype, dout, "dense_linear_backward dbias")
     if want_x or want_w or want_b:
         n = dout.numel()
         # (with no rows the gradients of W and the bias are zeros; empty tensors have no address)
@@ -811,17 +829,18 @@ def swiglu(gate, up, keep=False, hidden=None, stream=None):
     if up.dtype != gate.dtype or up.shape != shape or len(shape) < 1 or shape[-1] == 0:
         raise ValueError("swiglu: gate and up must be of one type and shape [..., K], K from 1 on")
     dev = _same_place("swiglu", gate, up)
-    hidden = gate.new_empty(shape) if hidden is None else _out(hidden, shape, gate.dtype, gate, "swiglu hidden")
+    hidden = _new(shape, gate.dtype, gate, dev) if hidden is None else _out(hidden, shape, gate.dtype, gate, "swiglu hidden")
     K, n = shape[-1], gate.numel()
     at = (None,) * 4
     if keep:
         each = shape[:-1] + ((K + 31) // 32,)
-        kept = [gate.new_empty(s, dtype=d) for s, d in ((shape, _int8), (each, _bytes)) * 2]
-        at = [q.data_ptr() for q in kept]
+        gc, uc = _new(shape, _int8, gate, dev), _new(shape, _int8, gate, dev)
+        gs, us = _new(each, _bytes, gate, dev), _new(each, _bytes, gate, dev)
+        at = (gc.data_ptr(), gs.data_ptr(), uc.data_ptr(), us.data_ptr())
     if n:
         _call((_lib or lib()).swiglu_q_swiglu, dev, stream, gate.data_ptr(), up.data_ptr(), n // K, K, t,
               hidden.data_ptr(), *at)
-    return (hidden, (kept[0], kept[1]), (kept[2], kept[3])) if keep else hidden
+    return (hidden, (gc, gs), (uc, us)) if keep else hidden
 
 
 def swiglu_backward(dhidden, gate, up, hidden=False, stream=None):
@@ -834,7 +853,7 @@ def swiglu_backward(dhidden, gate, up, hidden=False, stream=None):
     gate, gs = _kept(gate, t, shape, "swiglu_backward gate")
     up, us = _kept(up, t, shape, "swiglu_backward up")
     dev = _same_place("swiglu_backward", dhidden, gate, gs, up, us)
-    outs = [dhidden.new_empty(shape) for _ in range(3 if hidden else 2)]
+    outs = [_new(shape, dhidden.dtype, dhidden, dev) for _ in range(3 if hidden else 2)]
     K, n = shape[-1], dhidden.numel()
     if n:
         _call((_lib or lib()).swiglu_q_swiglu_backward, dev, stream, dhidden.data_ptr(), gate.data_ptr(),
@@ -858,8 +877,8 @@ def balance_loss(logits, ids, scoring=SWQ_ROUTE_SOFTMAX, stream=None):
     t = _type(logits, "balance_loss")
     T, E, k = _slots(logits, ids, "balance_loss")
     dev = _same_place("balance_loss", logits, ids)
-    loss = logits.new_empty((), dtype=_float32)
-    counts, slopes = logits.new_empty((E,), dtype=_int32), logits.new_empty((E,), dtype=_float32)
+    loss = _new((), _float32, logits, dev)
+    counts, slopes = _new((E,), _int32, logits, dev), _new((E,), _float32, logits, dev)
     at = loss.data_ptr()
     _call((_lib or lib()).swiglu_q_balance_loss, dev, stream, logits.data_ptr() if T else at,
           ids.data_ptr() if T else at, T, E, k, t, scoring, at, counts.data_ptr(), slopes.data_ptr())
@@ -883,7 +902,7 @@ def route_backward(logits, ids, dweights=None, scoring=SWQ_ROUTE_SOFTMAX, slopes
         raise ValueError("route_backward: dloss must be one float32 beside slopes")
     dev = _same_place("route_backward", logits, ids, dweights, slopes, dloss)
     shape = logits.shape
-    dlogits = (logits.new_empty(shape) if dlogits is None
+    dlogits = (_new(shape, logits.dtype, logits, dev) if dlogits is None
                else _out(dlogits, shape, logits.dtype, logits, "route_backward dlogits"))
     if T and E:
         _call((_lib or lib()).swiglu_q_route_backward, dev, stream, logits.data_ptr(), ids.data_ptr(),

@@ -457,6 +457,7 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t p
   const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
   float v[8] = {};
   if (n > 0) {
+#pragma unroll 4
     for (int s = 0; s < g.splits; ++s) {
       const float* f = g.parts + ((int64_t)s * g.P + p) * g.part_ld + q;
       const f32x4 x = *(const f32x4*)f, y = *(const f32x4*)(f + 4);
@@ -470,17 +471,20 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t p
 // ----------------------------------------------------------------- few rows ----
 //
 // Up to 16 RT rows by 16 CT columns per block, both operands along their rows and straight to registers, at any
-// address and of any length.  The waves take chunks of 128 inner indexes in turn, and their sums meet in LDS, added in
-// wave order.  The weights' bytes count here: every weight is read once per block of rows.
+// address and of any length.  The waves take chunks of 256 inner indexes in turn, all loads of a chunk in flight, and
+// their sums meet in LDS, added in wave order.  The weights' bytes count here: every weight is read once per block
+// of rows.  1 x 2048 x 5632 from memory 7.1 us (3.2 TB/s, latency: the launch, one round of loads, the join), 1 x 4096 x
+// 14336 24.4 (4.8 TB/s).  Sixteen waves with chunks of 128 took 8.8 and 36, four waves 8.9 and 26.
+constexpr int kFewWaves = 8;
 template <int TYPE, int RT, int CT>
-__global__ __launch_bounds__(1024) void dense_few_kernel(DenseGemm g) {
-  constexpr int PITCH = 16 * CT + 4, MAX_W = 16;
-  __shared__ __attribute__((aligned(16))) float sums[MAX_W * 16 * RT * PITCH];
+__global__ __launch_bounds__(64 * kFewWaves) void dense_few_kernel(DenseGemm g) {
+  constexpr int PITCH = 16 * CT + 4, W = kFewWaves, U = 8;
+  __shared__ __attribute__((aligned(16))) float sums[W * 16 * RT * PITCH];
 #ifdef SWQ_LDS_POISON
   lds_poison(sums, sizeof(sums), kPoisonFloat);
   __syncthreads();
 #endif
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, W = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, h = lane >> 4;
   const int64_t q0 = (int64_t)blockIdx.x * (16 * CT), p0 = (int64_t)blockIdx.y * (16 * RT);
   const uint16_t* x[RT];
@@ -490,44 +494,37 @@ __global__ __launch_bounds__(1024) void dense_few_kernel(DenseGemm g) {
 #pragma unroll
   for (int j = 0; j < CT; ++j) w[j] = g.b + min(q0 + 16 * j + r, g.Q - 1) * g.ldb + 8 * h;
   f32x4 acc[RT][CT] = {};
-  const int R = (int)g.R, full = R >> 7;
+  const int R = (int)g.R, full = R / (32 * U);
   for (int c = wave; c < full; c += W) {
-    u32x4 a[RT][4], b[CT][4];
+    u32x4 a[RT][U], b[CT][U];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < U; ++s)
 #pragma unroll
-      for (int j = 0; j < CT; ++j) b[j][s] = *(const u32x4_any*)(w[j] + 128 * c + 32 * s);
+      for (int j = 0; j < CT; ++j) b[j][s] = *(const u32x4_any*)(w[j] + 32 * (U * c + s));
 #pragma unroll
-      for (int i = 0; i < RT; ++i) a[i][s] = *(const u32x4_any*)(x[i] + 128 * c + 32 * s);
-    }
+    for (int s = 0; s < U; ++s)
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+      for (int i = 0; i < RT; ++i) a[i][s] = *(const u32x4_any*)(x[i] + 32 * (U * c + s));
+#pragma unroll
+    for (int s = 0; s < U; ++s)
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < CT; ++j) acc[i][j] = mfma_16<TYPE>(b[j][s], a[i][s], acc[i][j]);
   }
-  if ((R & 127) && wave == full % W) {         // the rest, element by element at its end
-    const auto some = [&](const uint16_t* f, int n) SWQ_INLINE {
-      u32x4 v = {0, 0, 0, 0};
-      if (n >= 8) return (u32x4)*(const u32x4_any*)f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) v[e >> 1] |= (uint32_t)f[e] << (16 * (e & 1));
-      return v;
-    };
+  // the rest, a step per wave, element by element at its end
 #pragma unroll 1
-    for (int k = full * 128; k < R; k += 32) {
-      u32x4 a[RT], b[CT];
+  for (int k = 32 * (U * full + wave); k < R; k += 32 * W) {
+    u32x4 a[RT], b[CT];
+    const int n = min(max(R - k - 8 * h, 0), 8);
 #pragma unroll
-      for (int j = 0; j < CT; ++j) b[j] = some(w[j] + k, R - k - 8 * h);
+    for (int j = 0; j < CT; ++j) b[j] = load8(w[j] + k, n);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) a[i] = some(x[i] + k, R - k - 8 * h);
+    for (int i = 0; i < RT; ++i) a[i] = load8(x[i] + k, n);
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < CT; ++j) acc[i][j] = mfma_16<TYPE>(b[j], a[i], acc[i][j]);
-    }
+      for (int j = 0; j < CT; ++j) acc[i][j] = mfma_16<TYPE>(b[j], a[i], acc[i][j]);
   }
   // lane 16 h + r has columns 4 h .. 4 h + 3 of row r
 #pragma unroll
@@ -536,27 +533,32 @@ __global__ __launch_bounds__(1024) void dense_few_kernel(DenseGemm g) {
     for (int j = 0; j < CT; ++j)
       *(f32x4*)(sums + ((wave * RT + i) * 16 + r) * PITCH + 16 * j + 4 * h) = acc[i][j];
   __syncthreads();
-  for (int t = threadIdx.x; t < 32 * RT * CT; t += blockDim.x) {
+  for (int t = threadIdx.x; t < 32 * RT * CT; t += 64 * W) {
     const int row = t / (2 * CT), col = t % (2 * CT) * 8;
     const int64_t p = p0 + row, q = q0 + col;
-    float v[8] = {};
+    if (p >= g.P) continue;
+    f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+#pragma unroll 4
     for (int u = 0; u < W; ++u) {
       const float* f = sums + (u * RT * 16 + row) * PITCH + col;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += f[e];
+      s0 += *(const f32x4*)f;
+      s1 += *(const f32x4*)(f + 4);
     }
+    float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
     const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
-    if (p < g.P) finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
+    finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
   }
 }
 
 template <int TYPE, int RT>
 void launch_few_rows(const DenseGemm& g, hipStream_t st) {
-  const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(1, (g.R + 127) / 128));
-  const int ct = g.z_scales || g.Q >= 32 * 512 ? 2 : 1;      // (a checkpoint's blocks are 32 columns)
+  // 32 columns a block where a checkpoint's blocks need them, and where 16 would give some CUs two blocks and others
+  // one (1 x 2048 x 5632 7.1 us against 9.0; 1 x 4096 x 14336 29.8 against 24.4)
+  const int64_t blocks = (g.Q + 15) / 16, cus = device_cus();
+  const int ct = g.z_scales || (blocks > cus && blocks <= 2 * cus) ? 2 : 1;
   const dim3 grid((unsigned)((g.Q + 16 * ct - 1) / (16 * ct)), (unsigned)((g.P + 16 * RT - 1) / (16 * RT)));
-  if (ct == 2) dense_few_kernel<TYPE, RT, 2><<<grid, 64 * waves, 0, st>>>(g);
-  else dense_few_kernel<TYPE, RT, 1><<<grid, 64 * waves, 0, st>>>(g);
+  if (ct == 2) dense_few_kernel<TYPE, RT, 2><<<grid, 64 * kFewWaves, 0, st>>>(g);
+  else dense_few_kernel<TYPE, RT, 1><<<grid, 64 * kFewWaves, 0, st>>>(g);
 }
 
 template <int TYPE>
