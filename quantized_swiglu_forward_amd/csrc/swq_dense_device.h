@@ -10,6 +10,11 @@ namespace swq {
 typedef __attribute__((ext_vector_type(2), aligned(1))) uint32_t u32x2_any;   // at any address
 typedef __attribute__((ext_vector_type(4), aligned(1))) uint32_t u32x4_any;
 
+// i / n; 64-bit division is a long sequence of instructions.
+__device__ __forceinline__ int64_t over(int64_t i, uint32_t n) {
+  return (uint64_t)i >> 32 ? i / n : (int64_t)((uint32_t)i / n);
+}
+
 // ---- 8-bit checkpoints (MXINT8: int8 codes q, one e8m0 byte b per 32 neighbours of a row, q 2^(b - 133)) ----
 //
 // The step 2^e of a block is the smallest power of two, from 2^-126 on, at which no element's

@@ -452,7 +452,7 @@ __global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_pair_ke
 template <int TYPE>
 __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t per_row) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t p = i / per_row, q = 8 * (i - p * per_row);
+  const int64_t p = over(i, per_row), q = 8 * (i - p * per_row);
   if (p >= g.P) return;                        // four neighbouring lanes leave together
   const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
   float v[8] = {};

@@ -20,7 +20,7 @@ struct Piece {
   int n;                    // elements, 0 .. 8
 };
 __device__ __forceinline__ Piece piece_of(const Pieces& t, int64_t i) {
-  const int64_t row = i / t.per_row;
+  const int64_t row = over(i, t.per_row);
   const uint32_t c = (uint32_t)(i - row * t.per_row);
   const int64_t left = t.K - 8 * (int64_t)c;
   return {row * t.K + 8 * (int64_t)c, row * (t.per_row / 4) + (c >> 2), left >= 8 ? 8 : left > 0 ? (int)left : 0};
@@ -264,7 +264,7 @@ __device__ __forceinline__ void prep_rows(const PrepRows& r, int64_t block, int6
   const uint32_t per_row = (uint32_t)((r.K + 7) / 8);
   const int64_t all = r.R * per_row, scale_row = (r.K + 31) / 32;
   for (int64_t i = block * 256 + threadIdx.x; i < all; i += blocks * 256) {
-    const int64_t row = i / per_row;
+    const int64_t row = over(i, per_row);
     const uint32_t c = (uint32_t)(i - row * per_row);
     const int64_t at = row * r.K + 8 * (int64_t)c, left = r.K - 8 * (int64_t)c;
     float v[8];
