@@ -29,15 +29,6 @@ __device__ __forceinline__ f32x4 mfma_16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                    0);
 }
-template <int TYPE>
-__device__ __forceinline__ f32x16 mfma_wide(u32x4 a, u32x4 b, f32x16 c) {
-  if constexpr (TYPE == kTypeF16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
-                                                   0);
-}
-
 // XCD-aware order of the tiles: the hardware deals consecutive blocks to the eight XCDs in turn, so block b
 // takes tile b / 8 of a contiguous eighth of the order, and an XCD's L2 sees neighbours.  In the
 // order, bands of eight row tiles run along their columns (bands of 4 the same, of 2 and 16 3 % slower, of 1 and 32 5 to 15).
@@ -148,26 +139,31 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
 
 // -------------------------------------------------------------------- tiles ----
 //
-// WP x WQ waves, each 32 AF rows by 32 BF columns of 32 x 32 accumulators.  A stage is 64 inner indexes of both
-// operands in LDS, S stages, filled by loads that write LDS; a step of 16 reads its successor's operands into
-// registers while its products run, and a stage that has been read makes room for the loads of the one S ahead.
+// WP x WQ waves, each AF by BF accumulators of 16 x 16 (rows by columns).  A stage is 64 inner indexes of both operands in
+// LDS, S stages, filled by loads that write LDS.  A step of 32 takes its products row by row; a row's operand is read for
+// the next step as soon as its products are issued, the columns' operands are read ahead into a second set.  In the
+// last step of a stage the waves meet after the first rows, when every read of the stage has long been
+// answered: then the next stage is there, and the one that was read makes room for the loads of the one S ahead.
 //
 // Along: a row's 64 elements are 128 bytes, 16-byte unit u at u ^ (row / 2 & 7), and a lane's operand (eight
-// neighbours of a row) is one read.  Down: an inner index's BP elements are a row of LDS, unit u at u ^ 4 (r & 3)
-// (BP = 64: u ^ 4 (r / 2 & 1)), and an operand is two transposing reads of four inner indexes by
-// 16 columns each.  Either way the rows that a read touches lie in different banks.
+// neighbours of a row) is one read.  Down: an inner index's BP elements are a row of LDS, unit u at
+// u ^ (4 (r & 3) + 2 (r / 8 & 1)) (BP = 64: 4 (r / 2 & 1) for the first), and an operand is two transposing reads of
+// four inner indexes by 16 columns each.  Either way the rows that a read touches lie in different banks.
 //
-// The second operand of the products is a, so that lane 32 h + r has row r's columns 8 e + 4 h .. + 3 in elements
-// 4 e .. 4 e + 3; the sums leave through the wave's own stretch of LDS, 32 rows at a time, as whole lines.
+// The second operand of the products is a, so that lane 16 h + r has row r's columns 4 h .. 4 h + 3; the sums leave
+// through the wave's own stretch of LDS, 32 rows at a time, as whole lines.
+//
+// What bounds it is the card's power: the products alone, no loads and no reads, of 8192 x 4096 x 4096 took 192 us
+// (1.43 PFLOP/s; of 32 x 32 x 16, which adds to twice as many accumulators per product, 210).
 template <int AF_, int BF_, int WP_, int WQ_, int S_, int OCC_>
 struct DenseShape {
-  static constexpr int AF = AF_, BF = BF_, WP = WP_, WQ = WQ_, S = S_, OCC = OCC_;
-  static constexpr int W = WP * WQ, BP = 32 * AF * WP, BQ = 32 * BF * WQ;
-  static constexpr int STAGE_A = BP * 128, STAGE = (BP + BQ) * 128;
-  static constexpr int LOADS_A = BP / (8 * W), LOADS = (BP + BQ) / (8 * W);     // per wave and stage
-  static constexpr int PITCH = 32 * BF + 4, FLUSH = 32 * PITCH * 4;             // floats; bytes of a wave's stretch
+  static constexpr int AF = AF_, BF = BF_, WP = WP_, WQ = WQ_, S = S_, OCC = OCC_, KS = 64;
+  static constexpr int W = WP * WQ, BP = 16 * AF * WP, BQ = 16 * BF * WQ;
+  static constexpr int STAGE_A = BP * KS * 2, STAGE = (BP + BQ) * KS * 2;
+  static constexpr int LOADS_A = BP * KS / (512 * W), LOADS = (BP + BQ) * KS / (512 * W);     // per wave and stage
+  static constexpr int PITCH = 16 * BF + 4, FLUSH = 32 * PITCH * 4;             // floats; bytes of a wave's stretch
   static constexpr int LDS = S * STAGE > W * FLUSH ? S * STAGE : W * FLUSH;
-  static_assert(BP % (8 * W) == 0 && BQ % (8 * W) == 0 && W % 2 == 0 && 16 % BF == 0);
+  static_assert(BP * KS % (512 * W) == 0 && BQ * KS % (512 * W) == 0 && W % 2 == 0 && 32 % BF == 0 && AF % 2 == 0);
 };
 
 // A load of 16 bytes per lane to LDS at lds + FROM, `soff` bytes further than the lane's offset (which alone counts for
@@ -187,7 +183,9 @@ __device__ __forceinline__ void dma16_at(i32x4 rs, uint32_t lds, uint32_t voff, 
 // and ends at R.
 template <int WAY, int BP, int W>
 struct Operand {
-  static constexpr int UNITS = WAY == kAlong ? 8 : BP / 8, LOADS = BP / (8 * W);      // 16-byte units of a row of LDS
+  static constexpr int KS = 64;
+  static constexpr int UNITS = WAY == kAlong ? KS / 8 : BP / 8, LOADS = BP * KS / (512 * W);  // 16-byte units of a row of LDS
+  static constexpr int along_swap(int row) { return row >> 1 & 7; }
   i32x4 rs;
   uint64_t at;              // Down: the stage's address
   int64_t left;             // Down: bytes from there to the end
@@ -195,9 +193,9 @@ struct Operand {
   uint32_t off[LOADS];      // the lane's offsets
   int k, tail;              // Along: the lane's first inner index of a stage; indexes of the last stage
 
-  // Down: rows of LDS whose length is a multiple of 256 bytes begin in the same bank, of 128 every second, of 64
-  // every fourth
-  static constexpr int swap(int r) { return BP % 128 == 0 ? (r & 3) << 2 : BP % 64 == 0 ? (r >> 1 & 1) << 2 : 0; }
+  // Down: rows of LDS of 256 bytes and more begin in the same bank, of 128 every second; a read takes four neighbouring
+  // rows twice, eight rows apart
+  static constexpr int swap(int r) { return (BP >= 128 ? (r & 3) << 2 : (r >> 1 & 1) << 2) ^ (r >> 3 & 1) << 1; }
 
   __device__ __forceinline__ void aim(const uint16_t* x, int64_t ld_, int64_t first, int64_t n, int64_t r0, int64_t r1,
                                       int wave, int lane) {
@@ -205,11 +203,12 @@ struct Operand {
     if constexpr (WAY == kAlong) {
       const int64_t rows = min(n - first, (int64_t)BP);
       rs = make_srsrc(x + first * ld + r0, (uint32_t)((rows * ld - r0) * 2));
-      const int unit = lane % 8 ^ ((8 * wave + lane / 8) >> 1 & 7);         // (W even: the same in every load)
+      const int unit = lane % UNITS ^ along_swap(64 / UNITS * wave + lane / UNITS);     // (W even: the same in every load)
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) off[i] = (uint32_t)((8 * (W * i + wave) + lane / 8) * ld * 2) + unit * 16;
+      for (int i = 0; i < LOADS; ++i)
+        off[i] = (uint32_t)((64 / UNITS * (W * i + wave) + lane / UNITS) * ld * 2) + unit * 16;
       k = unit * 8;
-      tail = (int)((r1 - r0 - 1) & 63) + 1;
+      tail = (int)((r1 - r0 - 1) & (KS - 1)) + 1;
     } else {
       at = (uint64_t)(x + r0 * ld + first);
       left = ((r1 - r0) * ld - first) * 2;
@@ -235,22 +234,22 @@ struct Operand {
   }
   template <int i, int FROM>
   __device__ __forceinline__ void load(int t, uint32_t lds) const {
-    dma16_at<FROM + W * i * 1024>(rs, lds, off[i], WAY == kAlong ? (uint32_t)t * 128u : 0u);
+    dma16_at<FROM + W * i * 1024>(rs, lds, off[i], WAY == kAlong ? (uint32_t)t * (2u * KS) : 0u);
   }
   __device__ __forceinline__ void end() {
     if constexpr (WAY == kDown) {
-      at += (uint64_t)(ld * 128);
-      left -= ld * 128;
+      at += (uint64_t)(ld * (2 * KS));
+      left -= ld * (2 * KS);
     }
   }
-  // the lane's operand of step s, tile `tile` (of 32) of the block's
+  // the lane's operand of step s, tile `tile` (of 16) of the block's
   static __device__ __forceinline__ u32x4 read(const char* lds, int s, int tile, int lane) {
+    const int h = lane >> 4, r = lane & 15;
     if constexpr (WAY == kAlong) {
-      const int r = lane & 31, h = lane >> 5;
-      return *(const u32x4*)(lds + (32 * tile + r) * 128 + (((2 * s + h) ^ (r >> 1 & 7)) * 16));
+      return *(const u32x4*)(lds + (16 * tile + r) * (2 * KS) + (((4 * s + h) ^ along_swap(r)) * 16));
     } else {
-      const int g = lane >> 4, l = lane & 15, r = 16 * s + 8 * (g >> 1) + (l >> 2);
-      const char* a = lds + r * (BP * 2) + (((4 * tile + 2 * (g & 1) + (l >> 1 & 1)) ^ swap(l >> 2)) * 16) + (l & 1) * 8;
+      const int row = 8 * h + (r >> 2);
+      const char* a = lds + (32 * s + row) * (BP * 2) + (((2 * tile + (r >> 1 & 1)) ^ swap(row)) * 16) + (r & 1) * 8;
       typedef __attribute__((address_space(3))) i16x4* lds4;
       const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds_ptr_t)a);
       const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds_ptr_t)(a + 4 * BP * 2));
@@ -271,7 +270,8 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
   if (!tile_at(block, (int)((g.P + BP - 1) / BP), (int)((g.Q + BQ - 1) / BQ), tp, tq)) return;
   const int64_t p0 = (int64_t)tp * BP, q0 = (int64_t)tq * BQ;
   const int64_t r0 = (int64_t)part * g.split_len, r1 = min(r0 + g.split_len, g.R);
-  const int stages = (int)((r1 - r0 + 63) / 64);
+  constexpr int KS = Sh::KS;
+  const int stages = (int)((r1 - r0 + KS - 1) / KS);
 
   Operand<WAY_A, BP, W> oa;
   Operand<WAY_B, BQ, W> ob;
@@ -287,27 +287,26 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
     if constexpr (i == Sh::LOADS - 1) oa.end(), ob.end();
   };
 
-  f32x16 acc[AF][BF];
-  u32x4 a[2][AF], b[2][BF];
-  const auto read = [&]<int set, int i>(int s, int slot) SWQ_INLINE {
-    const char* l = lds + slot * Sh::STAGE;
-    if constexpr (i < BF) b[set][i] = ob.read(l + Sh::STAGE_A, s, wq * BF + i, lane);
-    else a[set][i - BF] = oa.read(l, s, wp * AF + i - BF, lane);
+  f32x4 acc[AF][BF];
+  u32x4 a[AF], b[2][BF];
+  const auto read_a = [&]<int i>(int s, int slot) SWQ_INLINE {
+    a[i] = oa.read(lds + slot * Sh::STAGE, s, wp * AF + i, lane);
+  };
+  const auto read_b = [&]<int set, int j>(int slot) SWQ_INLINE {
+    b[set][j] = ob.read(lds + slot * Sh::STAGE + Sh::STAGE_A, set, wq * BF + j, lane);
   };
   const auto meet = [&]() SWQ_INLINE {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  // A step's products; before(n) is issued in front of the n-th.
-  constexpr int FRAGS = AF + BF, M = AF * BF;
-  constexpr int READS = (FRAGS + M - 1) / M, ISSUES = (Sh::LOADS + M - 1) / M;
-  constexpr int READS2 = (2 * FRAGS + M - 1) / M;      // before the barrier, so that it does not wait for them
-  const auto products = [&]<int SET>(auto before) SWQ_INLINE {
-    each<M>([&]<int n>() SWQ_INLINE {
-      constexpr int i = n / BF, j = n % BF;
+  // The products of rows FROM .. TO - 1 of a step; before(n) is issued in front of the n-th, after(i) behind a row's.
+  const auto products = [&]<int SET, int FROM, int TO>(auto before, auto after) SWQ_INLINE {
+    each<(TO - FROM) * BF>([&]<int n>() SWQ_INLINE {
+      constexpr int i = FROM + n / BF, j = n % BF;
       before.template operator()<n>();
-      acc[i][j] = mfma_wide<TYPE>(b[SET][j], a[SET][i], acc[i][j]);
+      acc[i][j] = mfma_16<TYPE>(b[SET][j], a[i], acc[i][j]);
+      if constexpr (j == BF - 1) after.template operator()<i>();
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -315,47 +314,48 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
 #pragma unroll
   for (int i = 0; i < AF; ++i)
 #pragma unroll
-    for (int j = 0; j < BF; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    for (int j = 0; j < BF; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
   wait_vmcnt<(S - 1) * Sh::LOADS>();
   meet();
   int slot = 0;
-  each<FRAGS>([&]<int i>() SWQ_INLINE { read.template operator()<0, i>(0, 0); });
+  each<BF>([&]<int j>() SWQ_INLINE { read_b.template operator()<0, j>(0); });
+  each<AF>([&]<int i>() SWQ_INLINE { read_a.template operator()<i>(0, 0); });
   // Loads are issued past the last stage too (they read nothing), so the counts hold to the end.
+  constexpr int EARLY = AF >= 4 ? AF / 4 : 1, LEFT = (AF - EARLY) * BF;
+  constexpr int FREE = BF + EARLY + Sh::LOADS, PER = (FREE + LEFT - 1) / LEFT;
   for (int t = 0; t < stages; ++t) {
-    each<3>([&]<int s>() SWQ_INLINE {
-      products.template operator()<s & 1>([&]<int n>() SWQ_INLINE {
-        constexpr int PER = s == 2 ? READS2 : READS;
-        each<PER>([&]<int e>() SWQ_INLINE {
-          if constexpr (n * PER + e < FRAGS) read.template operator()<(s + 1) & 1, n * PER + e>(s + 1, slot);
-        });
-      });
-    });
+    products.template operator()<0, 0, AF>(
+        [&]<int n>() SWQ_INLINE {
+          if constexpr (n < BF) read_b.template operator()<1, n>(slot);
+        },
+        [&]<int i>() SWQ_INLINE { read_a.template operator()<i>(1, slot); });
+    products.template operator()<1, 0, EARLY>([&]<int n>() SWQ_INLINE {}, [&]<int i>() SWQ_INLINE {});
     wait_vmcnt<(S - 2) * Sh::LOADS>();           // stage t + 1 is there
     meet();
     const int was = slot;
     slot = slot + 1 == S ? 0 : slot + 1;
-    products.template operator()<1>([&]<int n>() SWQ_INLINE {
-      each<READS>([&]<int e>() SWQ_INLINE {
-        if constexpr (n * READS + e < FRAGS) read.template operator()<0, n * READS + e>(0, slot);
-      });
-      each<ISSUES>([&]<int e>() SWQ_INLINE {
-        if constexpr (n * ISSUES + e < Sh::LOADS) load.template operator()<n * ISSUES + e>(t + S, was);
-      });
-    });
+    products.template operator()<1, EARLY, AF>(
+        [&]<int n>() SWQ_INLINE {
+          each<PER>([&]<int e>() SWQ_INLINE {
+            constexpr int k = n * PER + e;
+            if constexpr (k < BF) read_b.template operator()<0, k>(slot);
+            else if constexpr (k < BF + EARLY) read_a.template operator()<k - BF>(0, slot);
+            else if constexpr (k < FREE) load.template operator()<k - BF - EARLY>(t + S, was);
+          });
+        },
+        [&]<int i>() SWQ_INLINE { read_a.template operator()<i>(0, slot); });
   }
   wait_vmcnt<0>();           // no load past the end may still write LDS
   meet();
 
   float* buf = (float*)(lds + wave * Sh::FLUSH);
-  constexpr int LANES = 4 * BF, ROWS = 64 / LANES;                     // of a row; rows at a time
-  const int r = lane & 31, h = lane >> 5, col = lane % LANES * 8;
-  const int64_t q = q0 + wq * 32 * BF + col;
+  constexpr int LANES = 2 * BF, ROWS = 64 / LANES;                     // of a row; rows at a time
+  const int r = lane & 15, h = lane >> 4, col = lane % LANES * 8;
+  const int64_t q = q0 + wq * 16 * BF + col;
   const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
   // The residual comes a round of 32 rows ahead.
   constexpr int PASSES = 32 / ROWS;
-  const int64_t pw = p0 + wp * 32 * AF + lane / LANES;
+  const int64_t pw = p0 + wp * 16 * AF + lane / LANES;
   const bool whole = g.splits <= 1, ahead_too = !PLAIN && whole && g.res;
   const u32x4 bias = PLAIN || !whole ? (u32x4){0, 0, 0, 0} : bias_at(g, q, n);
   u32x4 ahead[PASSES] = {};
@@ -363,13 +363,11 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) ahead[k] = residual_at(g, pw + k * ROWS, q, n);
   }
-  each<AF>([&]<int i>() SWQ_INLINE {
+  each<AF / 2>([&]<int i>() SWQ_INLINE {
 #pragma unroll
-    for (int j = 0; j < BF; ++j)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *(f32x4*)(buf + r * Sh::PITCH + 32 * j + 8 * e + 4 * h) =
-            (f32x4){acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+      for (int j = 0; j < BF; ++j) *(f32x4*)(buf + (16 * e + r) * Sh::PITCH + 16 * j + 4 * h) = acc[2 * i + e][j];
 #pragma unroll 1
     for (int k = 0; k < 32; k += ROWS) {
       const int row = k + lane / LANES;
@@ -380,7 +378,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
       if (ahead_too) {
 #pragma unroll
         for (int e = 0; e + 1 < PASSES; ++e) ahead[e] = ahead[e + 1];
-        if constexpr (i + 1 < AF) ahead[PASSES - 1] = residual_at(g, p + 32, q, n);
+        if constexpr (2 * i + 2 < AF) ahead[PASSES - 1] = residual_at(g, p + 32, q, n);
       }
       if (p >= g.P) continue;
       if (!whole) {
@@ -573,9 +571,15 @@ void launch_few(const DenseGemm& g, hipStream_t st) {
 enum : int { kFewRows = 0, kTiles64 = 1, kTiles128 = 2, kTiles256 = 3 };
 constexpr int kSide[] = {0, 64, 128, 256};
 
-using Shape256 = DenseShape<4, 2, 2, 4, 2, 1>;
-using Shape128 = DenseShape<2, 2, 2, 2, 2, 2>;
-using Shape64 = DenseShape<1, 1, 2, 2, 4, 2>;
+#ifndef V256
+#define V256 8, 4, 2, 4, 2, 1
+#endif
+using Shape256 = DenseShape<V256>;
+#ifndef V128
+#define V128 4, 4, 2, 2, 2, 2
+#endif
+using Shape128 = DenseShape<V128>;
+using Shape64 = DenseShape<2, 2, 2, 2, 4, 2>;
 
 int64_t tiles_of(const DenseGemm& g, int kind) {
   const int64_t side = kSide[kind];
@@ -586,15 +590,15 @@ int64_t blocks_of(const DenseGemm& g) { return (tiles_of(g, g.kind) + 7) / 8 * 8
 template <int TYPE>
 void launch_forward(const DenseGemm& g, hipStream_t st) {
   const dim3 grid((unsigned)blocks_of(g), (unsigned)g.splits);
-  if (g.kind == kTiles256) dense_kernel<TYPE, Shape256><<<grid, 512, 0, st>>>(g);
-  else if (g.kind == kTiles128) dense_kernel<TYPE, Shape128><<<grid, 256, 0, st>>>(g);
+  if (g.kind == kTiles256) dense_kernel<TYPE, Shape256><<<grid, 64 * Shape256::W, 0, st>>>(g);
+  else if (g.kind == kTiles128) dense_kernel<TYPE, Shape128><<<grid, 64 * Shape128::W, 0, st>>>(g);
   else dense_kernel<TYPE, Shape64><<<grid, 256, 0, st>>>(g);
 }
 
 template <int TYPE>
 void launch_pair(const DensePair& d, int kind, unsigned blocks, hipStream_t st) {
-  if (kind == kTiles256) dense_pair_kernel<TYPE, Shape256><<<blocks, 512, 0, st>>>(d);
-  else if (kind == kTiles128) dense_pair_kernel<TYPE, Shape128><<<blocks, 256, 0, st>>>(d);
+  if (kind == kTiles256) dense_pair_kernel<TYPE, Shape256><<<blocks, 64 * Shape256::W, 0, st>>>(d);
+  else if (kind == kTiles128) dense_pair_kernel<TYPE, Shape128><<<blocks, 64 * Shape128::W, 0, st>>>(d);
   else dense_pair_kernel<TYPE, Shape64><<<blocks, 256, 0, st>>>(d);
 }
 
