@@ -159,11 +159,11 @@ template <int AF_, int BF_, int WP_, int WQ_, int S_, int OCC_>
 struct DenseShape {
   static constexpr int AF = AF_, BF = BF_, WP = WP_, WQ = WQ_, S = S_, OCC = OCC_, KS = 64;
   static constexpr int W = WP * WQ, BP = 16 * AF * WP, BQ = 16 * BF * WQ;
-  static constexpr int STAGE_A = BP * KS * 2, STAGE = (BP + BQ) * KS * 2;
   static constexpr int LOADS_A = BP * KS / (512 * W), LOADS = (BP + BQ) * KS / (512 * W);     // per wave and stage
+  static constexpr int STAGE_A = LOADS_A * W * 1024, STAGE = LOADS * W * 1024;
   static constexpr int PITCH = 16 * BF + 4, FLUSH = 32 * PITCH * 4;             // floats; bytes of a wave's stretch
   static constexpr int LDS = S * STAGE > W * FLUSH ? S * STAGE : W * FLUSH;
-  static_assert(BP * KS % (512 * W) == 0 && BQ * KS % (512 * W) == 0 && W % 2 == 0 && 32 % BF == 0 && AF % 2 == 0);
+  static_assert(BP * KS % (512 * W) == 0 && BQ * KS % (512 * W) == 0 && W % 2 == 0 && AF % 2 == 0 && BF % 2 == 0);
 };
 
 // A load of 16 bytes per lane to LDS at lds + FROM, `soff` bytes further than the lane's offset (which alone counts for
@@ -354,14 +354,15 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
   const int64_t q = q0 + wq * 16 * BF + col;
   const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
   // The residual comes a round of 32 rows ahead.
-  constexpr int PASSES = 32 / ROWS;
+  constexpr int PASSES = (32 + ROWS - 1) / ROWS;
   const int64_t pw = p0 + wp * 16 * AF + lane / LANES;
+  const bool idle = lane >= ROWS * LANES;      // (of rows that do not fill the wave)
   const bool whole = g.splits <= 1, ahead_too = !PLAIN && whole && g.res;
   const u32x4 bias = PLAIN || !whole ? (u32x4){0, 0, 0, 0} : bias_at(g, q, n);
   u32x4 ahead[PASSES] = {};
   if (ahead_too) {
 #pragma unroll
-    for (int k = 0; k < PASSES; ++k) ahead[k] = residual_at(g, pw + k * ROWS, q, n);
+    for (int k = 0; k < PASSES; ++k) ahead[k] = residual_at(g, pw + k * ROWS, q, idle ? 0 : n);
   }
   each<AF / 2>([&]<int i>() SWQ_INLINE {
 #pragma unroll
@@ -370,7 +371,7 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
       for (int j = 0; j < BF; ++j) *(f32x4*)(buf + (16 * e + r) * Sh::PITCH + 16 * j + 4 * h) = acc[2 * i + e][j];
 #pragma unroll 1
     for (int k = 0; k < 32; k += ROWS) {
-      const int row = k + lane / LANES;
+      const int row = min(k + lane / LANES, 31);
       const int64_t p = pw + i * 32 + k;
       const f32x4 x = *(const f32x4*)(buf + row * Sh::PITCH + col), y = *(const f32x4*)(buf + row * Sh::PITCH + col + 4);
       float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
@@ -378,9 +379,9 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
       if (ahead_too) {
 #pragma unroll
         for (int e = 0; e + 1 < PASSES; ++e) ahead[e] = ahead[e + 1];
-        if constexpr (2 * i + 2 < AF) ahead[PASSES - 1] = residual_at(g, p + 32, q, n);
+        if constexpr (2 * i + 2 < AF) ahead[PASSES - 1] = residual_at(g, p + 32, q, idle ? 0 : n);
       }
-      if (p >= g.P) continue;
+      if (p >= g.P || idle || k + lane / LANES >= 32) continue;
       if (!whole) {
         if (n > 0) {
           float* o = g.parts + ((int64_t)part * g.P + p) * g.part_ld + q;
@@ -568,22 +569,16 @@ void launch_few(const DenseGemm& g, hipStream_t st) {
 
 // -------------------------------------------------------------------- choice ----
 
-enum : int { kFewRows = 0, kTiles64 = 1, kTiles128 = 2, kTiles256 = 3 };
-constexpr int kSide[] = {0, 64, 128, 256};
+enum : int { kFewRows = 0, kTiles64 = 1, kTiles128 = 2, kTiles256 = 3, kTiles192 = 4 };
+constexpr int kRows[] = {0, 64, 128, 256, 256}, kColumns[] = {0, 64, 128, 256, 192};
 
-#ifndef V256
-#define V256 8, 4, 2, 4, 2, 1
-#endif
-using Shape256 = DenseShape<V256>;
-#ifndef V128
-#define V128 4, 4, 2, 2, 2, 2
-#endif
-using Shape128 = DenseShape<V128>;
+using Shape256 = DenseShape<8, 4, 2, 4, 2, 1>;
+using Shape192 = DenseShape<4, 6, 4, 2, 2, 1>;
+using Shape128 = DenseShape<4, 4, 2, 2, 2, 2>;
 using Shape64 = DenseShape<2, 2, 2, 2, 4, 2>;
 
 int64_t tiles_of(const DenseGemm& g, int kind) {
-  const int64_t side = kSide[kind];
-  return (g.P + side - 1) / side * ((g.Q + side - 1) / side);
+  return (g.P + kRows[kind] - 1) / kRows[kind] * ((g.Q + kColumns[kind] - 1) / kColumns[kind]);
 }
 int64_t blocks_of(const DenseGemm& g) { return (tiles_of(g, g.kind) + 7) / 8 * 8; }     // (eight XCDs)
 
@@ -591,6 +586,7 @@ template <int TYPE>
 void launch_forward(const DenseGemm& g, hipStream_t st) {
   const dim3 grid((unsigned)blocks_of(g), (unsigned)g.splits);
   if (g.kind == kTiles256) dense_kernel<TYPE, Shape256><<<grid, 64 * Shape256::W, 0, st>>>(g);
+  else if (g.kind == kTiles192) dense_kernel<TYPE, Shape192><<<grid, 64 * Shape192::W, 0, st>>>(g);
   else if (g.kind == kTiles128) dense_kernel<TYPE, Shape128><<<grid, 64 * Shape128::W, 0, st>>>(g);
   else dense_kernel<TYPE, Shape64><<<grid, 256, 0, st>>>(g);
 }
@@ -611,7 +607,7 @@ void launch_join(const DenseGemm& g, hipStream_t st) {
 
 // One launch holds fewer than 2^32 threads (of more the rest is left out, with no error); splits are for few tiles.
 bool launch_holds(const DenseGemm* g, int kind) {
-  return !g || tiles_of(*g, kind) * (kind == kTiles256 ? 512 : 256) < (int64_t(1) << 31);
+  return !g || tiles_of(*g, kind) * (kind >= kTiles256 ? 512 : 256) < (int64_t(1) << 31);
 }
 
 void split_into(DenseGemm& g, int64_t splits) {
@@ -630,22 +626,27 @@ constexpr int64_t kFewRowsMost = 16, kFewRowsOdd = 64;
 
 // The tile shape, one for both of a pair, and the splits of the inner indexes, by the time in us at which the CUs are done.
 // Measured: a CU takes 0.2 us per stage of a 64 x 64 tile, 0.46 of a 128 x 128 one (alone on its CU
-// 0.47, 0.72 where all CUs are busy) and 1.1 of a 256 x 256 one, 1.5 where all CUs are busy and the card's power limits
+// 0.47, 0.72 where all CUs are busy) and 1.1 of a 256 x 256 one, 1.45 where all CUs are busy and the card's power limits
 // them; a split writes and reads its float32 sums at 5.5 TB/s and takes another launch.  A product alone goes
-// in rounds of tiles; of a pair the longer tiles begin and the shorter ones fill the gaps.  (tiles of 256 / 128 / 64, us: 2048 x 4096 x
-// 14336 194 / 226 / 358, 512 x 2048 x 5632 44 / 26 / 24, 128 x 2048 x 5632 41 / 19 / 11; its gradient by
-// x, four splits of 64 14, one 27.)
-bool plan_tiles(DenseGemm* x, DenseGemm* w) {
+// in rounds of tiles, where tiles of 256 x 192 may fill a last round better; of a pair the longer tiles begin and the
+// shorter ones fill the gaps.  Tiles of 256 / 256 x 192 / 128 / 64, us (rows x K x N):
+//   forward  2048 x 4096 x 14336 203 / 240 / 238 / 359    2048 x 2048 x 5632 52 / 48 / 61 / 76
+//            512 x 2048 x 5632 33 / 40 / 28 / 23          128 x 2048 x 5632 22 / 21 / 18 / 9.5
+//   both gradients (256 / 128 / 64)  2048 x 4096 x 14336 429 / 492 / 900   2048 x 2048 x 5632 120 / 105 / 158
+//            128 x 2048 x 5632 30 / 23 / 30               1000 x 1000 x 1000 30 / 15 / 13
+// (Tiles of 256 x 224, which 14336 columns fill in two rounds of 256 CUs, gained 1 %: idle CUs leave the others
+// their power.)
+bool plan_tiles(DenseGemm* x, DenseGemm* w, bool gradients) {
   const int cus = device_cus();
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   DenseGemm* const g[2] = {x ? x : w, x && w ? w : nullptr};
   double best = 1e300;
   int kind = kTiles64;
   int64_t splits[2] = {1, 1};
-  for (int k = kTiles64; k <= kTiles256; ++k) {
+  for (int k = kTiles64; k <= (gradients ? kTiles256 : kTiles192); ++k) {
     if (!launch_holds(g[0], k) || !launch_holds(g[1], k)) continue;
     const auto block_us = [&](int64_t stages, double load, bool alone) {
-      return k == kTiles256 ? 2.2 + stages * (1.1 + 0.4 * load)
+      return k >= kTiles256 ? 2.2 + stages * (1.1 + 0.35 * load) * (kColumns[k] + 8) / 264
              : k == kTiles128 ? 0.7 + stages * (alone ? 0.47 + 0.25 * load : 0.46) : 0.3 + stages * (alone ? 0.23 : 0.2);
     };
     struct Cost {
@@ -690,14 +691,14 @@ bool plan_tiles(DenseGemm* x, DenseGemm* w) {
 }
 
 bool plan_dense_gemm(DenseGemm& g) {
-  if (g.P > kFewRowsMost && (g.P > kFewRowsOdd || g.R % 8 == 0)) return plan_tiles(&g, nullptr);
+  if (g.P > kFewRowsMost && (g.P > kFewRowsOdd || g.R % 8 == 0)) return plan_tiles(&g, nullptr, false);
   g.kind = kFewRows;
   split_into(g, 1);
   return true;
 }
 
 bool plan_dense_pair(DensePair& d, bool with_x, bool with_w) {
-  if ((with_x || with_w) && !plan_tiles(with_x ? &d.x : nullptr, with_w ? &d.w : nullptr)) return false;
+  if ((with_x || with_w) && !plan_tiles(with_x ? &d.x : nullptr, with_w ? &d.w : nullptr, true)) return false;
   d.x_blocks = with_x ? (int)(blocks_of(d.x) * d.x.splits) : 0;
   d.w_blocks = with_w ? (int)(blocks_of(d.w) * d.w.splits) : 0;
   d.w_first = with_w && d.w.split_len > d.x.split_len;
