@@ -35,12 +35,39 @@ __device__ __forceinline__ Mx8Step mx8_step(uint32_t amax_bits) {
   if (top >= 127.5f && e < 121) ++e;           // (2^121 is the last: byte 255 says NaN)
   return {__uint_as_float((uint32_t)(127 - e) << 23), (uint32_t)(e + 133)};
 }
-__device__ __forceinline__ int mx8_code(float v, Mx8Step s) {
-  return s.byte == 255 ? 0 : (int)__builtin_amdgcn_fmed3f(rintf(v * s.inverse), -127.0f, 127.0f);
+
+// The largest magnitude's bits of eight values (a NaN's are the largest).
+__device__ __forceinline__ uint32_t mx8_amax(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = __builtin_elementwise_maximum(fabsf(v[j]), m);
+  return __float_as_uint(m) & 0x7FFFFFFFu;
 }
-__device__ __forceinline__ uint32_t pack_codes(int a, int b, int c, int d) {
-  return ((uint32_t)a & 255u) | ((uint32_t)b & 255u) << 8 | ((uint32_t)c & 255u) << 16 | (uint32_t)d << 24;
+
+// Eight codes.  Adding 1.5 2^23 rounds a value below 2^22 to a whole number, ties to even, and leaves it in the low
+// bits.  Only next to float32's largest value can that be 128, and only a NaN block (byte 255) holds values that are no
+// numbers: both go the long way.
+__device__ __forceinline__ u32x2 mx8_codes(const float (&v)[8], Mx8Step s) {
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(fmaf(v[j], s.inverse, 12582912.0f));
+  if (__any(s.byte >= 254)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float r = __builtin_amdgcn_fmed3f(rintf(v[j] * s.inverse), -127.0f, 127.0f);
+      q[j] = s.byte == 255 ? 0u : (uint32_t)(int)r;
+    }
+  }
+  u32x2 w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x04000C0Cu);
+    w[i] = lo | hi;
+  }
+  return w;
 }
+
 // 2^(b - 133) (bytes below 7, which the quantiser never writes: subnormal), NaN for 255
 __device__ __forceinline__ float mx8_scale(uint32_t byte) {
   if (byte == 255) return __uint_as_float(0x7FC00000u);

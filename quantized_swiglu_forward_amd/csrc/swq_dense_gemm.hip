@@ -88,16 +88,15 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
   if (g.bias) add8<TYPE>(v, bias);
   if (g.z) {
     if (g.z_scales) {
-      uint32_t m = 0;
+      if (n < 8) {                     // (what is behind the last column counts for nothing)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, j < n ? __float_as_uint(v[j]) & 0x7FFFFFFFu : 0u);
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : 0.0f;
+      }
+      uint32_t m = mx8_amax(v);
       m = max(m, (uint32_t)__shfl_xor((int)m, 1));
       m = max(m, (uint32_t)__shfl_xor((int)m, 2));
       const Mx8Step s = mx8_step(m);
-      int c[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = mx8_code(v[j], s);
-      const u32x2 w = {pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7])};
+      const u32x2 w = mx8_codes(v, s);
       uint8_t* z = (uint8_t*)g.z + at;
       if (n == 8) {
         *(u32x2_any*)z = w;

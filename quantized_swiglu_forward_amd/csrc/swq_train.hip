@@ -89,18 +89,13 @@ __device__ __forceinline__ void decode8(const void* codes, float scale, int64_t 
 }
 
 // The block's maximum over its four pieces (neighbouring lanes), codes and scale.
-__device__ __forceinline__ void encode8(const float* v, const Piece& p, void* codes, uint8_t* scales) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+__device__ __forceinline__ void encode8(const float (&v)[8], const Piece& p, void* codes, uint8_t* scales) {
+  uint32_t m = mx8_amax(v);
   m = max(m, (uint32_t)__shfl_xor((int)m, 1));
   m = max(m, (uint32_t)__shfl_xor((int)m, 2));
   const Mx8Step s = mx8_step(m);
-  int q[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = mx8_code(v[j], s);
+  const u32x2 w = mx8_codes(v, s);
   uint8_t* c = (uint8_t*)codes + p.at;
-  const u32x2 w = {pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7])};
   if (p.n == 8) {
     *(u32x2_any*)c = w;
   } else {
