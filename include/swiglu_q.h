@@ -377,7 +377,8 @@ int swiglu_q_moe_mlp(const void *x, const int32_t *ids, const float *weights,
 #define SWQ_ACT_GELU_TANH  4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2       */
 
 /* x [R, K] (bf16, float32 or binary16 by `type`) to a checkpoint, and the values [R, K]
- * of one in `type` (one rounding; exact in bf16 and float32). */
+ * of one in `type` (exact in bf16 and float32; binary16 rounds what is finer than its own
+ * grid and holds what lies past its largest value, by half a step at most for a checkpoint of binary16 values, at that). */
 int swiglu_q_mx8_quantize(const void *x, int64_t R, int64_t K, int type, void *codes, void *scales, void *stream);
 int swiglu_q_mx8_dequantize(const void *codes, const void *scales, int64_t R, int64_t K, int type, void *out,
                             void *stream);

@@ -776,8 +776,8 @@ def dense_linear(x, w, bias=None, act=SWQ_ACT_NONE, residual=None, keep=None, ou
 def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True, True), dx=None, dw=None, dbias=None,
                           stream=None):
     """(dx [..., K], dw [N, K], dbias [N]) of ``dense_linear`` for dout [..., N], in dout's type (bf16 or
-    float16); None where want says False.  x and z (not needed with SWQ_ACT_NONE) are tensors of
-    that type or checkpoints (codes, scales).  The residual's gradient is dout itself."""
+    float16); None where want says False.  x (needed for dw) and z (needed unless act is SWQ_ACT_NONE) are tensors
+    of that type or checkpoints (codes, scales).  The residual's gradient is dout itself."""
     t = _type(dout, "dense_linear_backward", wide=False)
     if len(w.shape) != 2 or w.dtype != dout.dtype or len(dout.shape) < 1 or w.shape[0] != dout.shape[-1]:
         raise ValueError(f"dense_linear_backward: w must be {dout.dtype} [N, K] with dout's N")
@@ -786,7 +786,11 @@ def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True
         raise ValueError("dense_linear_backward: a product needs inputs and outputs (K = 0 or N = 0)")
     want_x, want_w, want_b = want
     lead = dout.shape[:-1]
-    x, xs = _kept(x, t, lead + (K,), "dense_linear_backward x")
+    xs = None
+    if x is not None:
+        x, xs = _kept(x, t, lead + (K,), "dense_linear_backward x")
+    elif want_w:
+        raise ValueError("dense_linear_backward: dw needs x")
     zs = None
     if z is not None:
         z, zs = _kept(z, t, dout.shape, "dense_linear_backward z")
@@ -810,14 +814,14 @@ def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True
     if want_x or want_w or want_b:
         n = dout.numel()
         # (with no rows the gradients of W and the bias are zeros; empty tensors have no address)
-        at = [None if q is None else q.data_ptr() for q in (xs, z, zs, dx, dw, dbias)]
+        at = [None if q is None else q.data_ptr() for q in (x, xs, z, zs, dx, dw, dbias)]
         if n:
-            _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, dout.data_ptr(), x.data_ptr(), at[0],
-                  w.data_ptr(), at[1], at[2], n // N, K, N, t, act, *at[3:])
+            _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, dout.data_ptr(), at[0], at[1],
+                  w.data_ptr(), at[2], at[3], n // N, K, N, t, act, *at[4:])
         elif want_w or want_b:
             full = w.data_ptr()
             _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, full, full, None, full, full, None, 0, K,
-                  N, t, act, None, *at[4:])
+                  N, t, act, None, *at[5:])
     return dx, dw, dbias
 
 

@@ -618,10 +618,14 @@ void split_into(DenseGemm& g, int64_t splits) {
 
 }  // namespace
 
-// The few-row kernel up to 16 rows, and up to 64 where a row's length is no multiple of 8, which the tiles would have
-// copied first (rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 8.5 / 10.2, 16 x 4096 x 4096 9.9 / 10.5,
-// 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 11 / 18).
-constexpr int64_t kFewRowsMost = 16, kFewRowsOdd = 64;
+// The few-row kernel: up to 16 rows, and of small products up to 32, or 128 where a row's length is no multiple of 8,
+// which the tiles would have copied first.  Rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 8.5 / 10.2,
+// 16 x 4096 x 4096 10.5 / 10.5, 24 x 2048 x 2048 7.0 / 8.8, 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 10 / 18,
+// 100 x 517 x 1001 9.0 / 10.2, 128 x 1003 x 2049 22 / 14.
+constexpr int64_t kFewRowsMost = 16, kFewRowsSmall = 32, kFewRowsOdd = 128, kFewSmall = int64_t(1) << 27;
+bool takes_few_rows(const DenseGemm& g) {
+  return g.P <= kFewRowsMost || (g.P <= (g.R % 8 ? kFewRowsOdd : kFewRowsSmall) && g.P * g.Q * g.R <= kFewSmall);
+}
 
 // The tile shape, one for both of a pair, and the splits of the inner indexes, by the time in us at which the CUs are done.
 // Measured: a CU takes 0.2 us per stage of a 64 x 64 tile, 0.46 of a 128 x 128 one (alone on its CU
@@ -690,7 +694,7 @@ bool plan_tiles(DenseGemm* x, DenseGemm* w, bool gradients) {
 }
 
 bool plan_dense_gemm(DenseGemm& g) {
-  if (g.P > kFewRowsMost && (g.P > kFewRowsOdd || g.R % 8 == 0)) return plan_tiles(&g, nullptr, false);
+  if (!takes_few_rows(g)) return plan_tiles(&g, nullptr, false);
   g.kind = kFewRows;
   split_into(g, 1);
   return true;

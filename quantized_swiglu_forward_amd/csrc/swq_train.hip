@@ -88,6 +88,15 @@ __device__ __forceinline__ void decode8(const void* codes, float scale, int64_t 
   for (int j = 0; j < 8; ++j) v[j] = mx8_value(w[j >> 2], j & 3, scale);
 }
 
+// Values of a checkpoint as TYPE: what rounds past binary16's largest value (a code's half step above it) is that value.
+template <int TYPE>
+__device__ __forceinline__ void hold8(float (&v)[8]) {
+  if constexpr (TYPE == kTypeF16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = v[j] != v[j] ? v[j] : __builtin_amdgcn_fmed3f(v[j], -65504.0f, 65504.0f);
+  }
+}
+
 // The block's maximum over its four pieces (neighbouring lanes), codes and scale.
 __device__ __forceinline__ void encode8(const float (&v)[8], const Piece& p, void* codes, uint8_t* scales) {
   uint32_t m = mx8_amax(v);
@@ -127,6 +136,7 @@ __global__ __launch_bounds__(256) void mx8_dequantize_kernel(const void* __restr
   const Piece p = piece_of(t, i);
   float v[8];
   decode8(codes, mx8_scale(scales[p.block]), p.at, p.n, v);
+  hold8<TYPE>(v);
   store8<TYPE>(out, p.at, p.n, v);
 }
 
@@ -198,22 +208,23 @@ hipError_t over_pieces(int64_t R, int64_t K, F launch) {
   return hipGetLastError();
 }
 
-// dz and the sums of its columns.  A block has 512 columns (a thread eight of them) of a stretch of rows, four rows at
-// a time; the four meet in LDS, the stretches' sums in a later kernel, all in order.
+// dz and the sums of its columns.  A block has a stretch of rows of 8 L columns (512; of narrow tensors the power of two
+// that holds a row), eight of a row to a thread, 256 / L rows at a time; these meet in LDS, the stretches' sums in a
+// later kernel, all in order.
 template <int TYPE>
-__device__ __forceinline__ void act_backward(const Prep& p, int64_t column_block, int64_t stretch, int64_t rows,
-                                             float (*meet)[64][8]) {
+__device__ __forceinline__ void act_backward(const Prep& p, int64_t column_block, int64_t stretch, int64_t rows, int L,
+                                             float* meet) {
   const Kept& z = p.z;
   const int64_t M = p.M, N = p.N;
-  const int c = threadIdx.x & 63, team = threadIdx.x >> 6;
-  const int64_t q = column_block * 512 + 8 * c, blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
+  const int c = threadIdx.x & (L - 1), team = threadIdx.x / L, teams = 256 / L;
+  const int64_t q = column_block * 8 * L + 8 * c, blocks = (N + 31) / 32, ld = (N + 7) / 8 * 8;
   const int n = q + 8 <= N ? 8 : q < N ? (int)(N - q) : 0;
   const int64_t m1 = min((stretch + 1) * rows, M);
   float sum[8] = {};
   const auto go = [&](auto slope) SWQ_INLINE {
     if (n > 0) {
 #pragma unroll 2
-      for (int64_t m = stretch * rows + team; m < m1; m += 4) {
+      for (int64_t m = stretch * rows + team; m < m1; m += teams) {
         float d[8], v[8] = {};
         load8<TYPE>(p.dout, m * N + q, n, d);
         if (p.act != kActNone) {
@@ -237,19 +248,17 @@ __device__ __forceinline__ void act_backward(const Prep& p, int64_t column_block
     default: go([](float v) { return activate_slope(v, kActGeluTanh); });
   }
   if (!p.sums && !p.dbias) return;
-  if (team) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) meet[team - 1][c][j] = sum[j];
-  }
+  for (int j = 0; j < 8; ++j) meet[(team * L + c) * 8 + j] = sum[j];
   __syncthreads();
-  if (team == 0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j >= n) continue;
-      const float all = (sum[j] + meet[0][c][j]) + (meet[1][c][j] + meet[2][c][j]);
-      if (p.dbias) p.dbias[q + j] = to_16(all, TYPE);
-      else p.sums[stretch * N + q + j] = all;
-    }
+  for (int t = threadIdx.x; t < 8 * L; t += 256) {
+    const int64_t column = column_block * 8 * L + t;
+    if (column >= N) continue;
+    float all = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < teams; ++i) all += meet[i * L * 8 + t];
+    if (p.dbias) p.dbias[column] = to_16(all, TYPE);
+    else p.sums[stretch * N + column] = all;
   }
 }
 
@@ -265,20 +274,21 @@ __device__ __forceinline__ void prep_rows(const PrepRows& r, int64_t block, int6
     float v[8];
     if (r.scales) decode8(r.src, mx8_scale(r.scales[row * scale_row + (c >> 2)]), at, left < 8 ? (int)left : 8, v);
     else load8<TYPE>(r.src, at, left < 8 ? (int)left : 8, v);
+    if (r.scales) hold8<TYPE>(v);
     store8<TYPE>(r.dst, 8 * i, 8, v);
   }
 }
 
 template <int TYPE>
-__global__ __launch_bounds__(256) void prep_kernel(Prep p, int column_blocks, int act_blocks, int64_t rows, int blocks0,
-                                                   int blocks1) {
-  __shared__ float meet[3][64][8];
+__global__ __launch_bounds__(256) void prep_kernel(Prep p, int column_blocks, int act_blocks, int64_t rows, int L,
+                                                   int blocks0, int blocks1) {
+  __shared__ float meet[256 * 8];
 #ifdef SWQ_LDS_POISON
   lds_poison(meet, sizeof(meet), kPoisonFloat);
   __syncthreads();
 #endif
   int b = blockIdx.x;
-  if (b < act_blocks) return act_backward<TYPE>(p, b % column_blocks, b / column_blocks, rows, meet);
+  if (b < act_blocks) return act_backward<TYPE>(p, b % column_blocks, b / column_blocks, rows, L, meet);
   b -= act_blocks;
   if (b < blocks0) return prep_rows<TYPE>(p.rows[0], b, blocks0);
   prep_rows<TYPE>(p.rows[1], b - blocks0, blocks1);
@@ -324,25 +334,38 @@ hipError_t launch_swiglu_backward(const uint16_t* dhidden, Kept gate, Kept up, i
   });
 }
 
-// Stretches of rows: about 2048 blocks in all, four rows each at least, one up to sixteen rows.
-int64_t act_parts(int64_t M, int64_t N) {
-  const int64_t columns = (N + 511) / 512;
-  if (M <= 16) return 1;
-  const int64_t parts = std::max<int64_t>(1, std::min((M + 3) / 4, 2048 / columns));
-  const int64_t rows = ((M + parts - 1) / parts + 3) / 4 * 4;
-  return (M + rows - 1) / rows;
+namespace {
+
+// Lanes to a row, and stretches of rows: about 2048 blocks in all, four rows to a thread each at least; one up to
+// sixteen rows.
+int act_lanes(int64_t N) {
+  int L = 1;
+  while (L < 64 && 8 * L < N) L *= 2;
+  return L;
+}
+int64_t act_rows(int64_t M, int64_t N) {
+  const int L = act_lanes(N);
+  const int64_t columns = (N + 8 * L - 1) / (8 * L), teams = 256 / L;
+  if (M <= 16) return 16;
+  const int64_t parts = std::max<int64_t>(1, std::min((M + 4 * teams - 1) / (4 * teams), 2048 / columns));
+  return ((M + parts - 1) / parts + teams - 1) / teams * teams;
 }
 
+}  // namespace
+
+int64_t act_parts(int64_t M, int64_t N) { return (M + act_rows(M, N) - 1) / act_rows(M, N); }
+
 hipError_t launch_prep(const Prep& p, int type, hipStream_t st) {
-  const int64_t columns = (p.N + 511) / 512, parts = p.dout ? act_parts(p.M, p.N) : 0;
-  const int64_t rows = p.dout ? ((p.M + parts - 1) / parts + 3) / 4 * 4 : 0;
+  const int L = p.dout ? act_lanes(p.N) : 1;
+  const int64_t columns = p.dout ? (p.N + 8 * L - 1) / (8 * L) : 0, parts = p.dout ? act_parts(p.M, p.N) : 0;
+  const int64_t rows = p.dout ? act_rows(p.M, p.N) : 0;
   const auto blocks_for = [](const PrepRows& r) {
     return r.dst ? (int)std::min<int64_t>((r.R * ((r.K + 7) / 8) + 255) / 256, 4096) : 0;
   };
   const int n0 = blocks_for(p.rows[0]), n1 = blocks_for(p.rows[1]), act = (int)(columns * parts);
   if (act + n0 + n1 == 0) return hipSuccess;
   const auto kernel = type == kTypeF16 ? prep_kernel<kTypeF16> : prep_kernel<kTypeBf16>;
-  kernel<<<(unsigned)(act + n0 + n1), 256, 0, st>>>(p, (int)columns, act, rows, n0, n1);
+  kernel<<<(unsigned)(act + n0 + n1), 256, 0, st>>>(p, (int)columns, act, rows, L, n0, n1);
   return hipGetLastError();
 }
 
