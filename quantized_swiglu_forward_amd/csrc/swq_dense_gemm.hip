@@ -166,12 +166,12 @@ struct DenseShape {
 };
 
 // A load of 16 bytes per lane to LDS at lds + FROM, `soff` bytes further than the lane's offset (which alone counts for
-// the range check).
+// the range check; the wait state is what a load that writes LDS needs behind a write of m0).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 template <int FROM>
 __device__ __forceinline__ void dma16_at(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_add_u32 m0, %0, %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                ::"s"(lds), "v"(voff), "s"(rs), "s"(soff), "n"(FROM) : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
@@ -472,11 +472,26 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t p
 // address and of any length.  The waves take chunks of 256 inner indexes in turn, all loads of a chunk in flight, and
 // their sums meet in LDS, added in wave order.  The weights' bytes count here: every weight is read once per block
 // of rows.  1 x 2048 x 5632 from memory 7.1 us (3.2 TB/s, latency: the launch, one round of loads, the join), 1 x 4096 x
-// 14336 24.4 (4.8 TB/s).  Sixteen waves with chunks of 128 took 8.8 and 36, four waves 8.9 and 26.
+// 14336 23.7 (5.0 TB/s).  Sixteen waves with chunks of 128 took 8.8 and 36, four waves 8.9 and 26.  ODD: the rows begin at
+// odd elements (32 x 1003 x 2049 7.0 us; by 16-byte loads at any address 8.6; 32 x 1024 x 2048 5.3).
 constexpr int kFewWaves = 8;
-template <int TYPE, int RT, int CT>
+// Eight neighbours at any address: as aligned words, which load several times faster than 16 bytes at an odd
+// element.  (A word holds one of the eight at least, so none lies outside the tensor's pages.)
+template <bool ODD>
+__device__ __forceinline__ u32x4 load8_odd(const uint16_t* f) {
+  typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t u32x4_words;
+  if constexpr (!ODD) return *(const u32x4_words*)f;
+  const uint32_t shift = (uint32_t)(uintptr_t)f & 2u;
+  const uint32_t* w = (const uint32_t*)((uintptr_t)f - shift);
+  const u32x4 v = *(const u32x4_words*)w;
+  const uint32_t next = w[3 + (shift >> 1)];
+  return (u32x4){__builtin_amdgcn_alignbyte(v[1], v[0], shift), __builtin_amdgcn_alignbyte(v[2], v[1], shift),
+                 __builtin_amdgcn_alignbyte(v[3], v[2], shift), __builtin_amdgcn_alignbyte(next, v[3], shift)};
+}
+
+template <int TYPE, int RT, int CT, bool ODD>
 __global__ __launch_bounds__(64 * kFewWaves) void dense_few_kernel(DenseGemm g) {
-  constexpr int PITCH = 16 * CT + 4, W = kFewWaves, U = 8;
+  constexpr int PITCH = 16 * CT + 4, W = kFewWaves, U = ODD && RT > 1 ? 4 : 8;
   __shared__ __attribute__((aligned(16))) float sums[W * 16 * RT * PITCH];
 #ifdef SWQ_LDS_POISON
   lds_poison(sums, sizeof(sums), kPoisonFloat);
@@ -498,11 +513,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few_kernel(DenseGemm g) 
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
-      for (int j = 0; j < CT; ++j) b[j][s] = *(const u32x4_any*)(w[j] + 32 * (U * c + s));
+      for (int j = 0; j < CT; ++j) b[j][s] = load8_odd<ODD>(w[j] + 32 * (U * c + s));
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) a[i][s] = *(const u32x4_any*)(x[i] + 32 * (U * c + s));
+      for (int i = 0; i < RT; ++i) a[i][s] = load8_odd<ODD>(x[i] + 32 * (U * c + s));
+    __builtin_amdgcn_sched_barrier(0);         // (all of them on their way first)
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
@@ -555,8 +571,12 @@ void launch_few_rows(const DenseGemm& g, hipStream_t st) {
   const int64_t blocks = (g.Q + 15) / 16, cus = device_cus();
   const int ct = g.z_scales || (blocks > cus && blocks <= 2 * cus) ? 2 : 1;
   const dim3 grid((unsigned)((g.Q + 16 * ct - 1) / (16 * ct)), (unsigned)((g.P + 16 * RT - 1) / (16 * RT)));
-  if (ct == 2) dense_few_kernel<TYPE, RT, 2><<<grid, 64 * kFewWaves, 0, st>>>(g);
-  else dense_few_kernel<TYPE, RT, 1><<<grid, 64 * kFewWaves, 0, st>>>(g);
+  const auto go = [&]<bool ODD>() {
+    if (ct == 2) dense_few_kernel<TYPE, RT, 2, ODD><<<grid, 64 * kFewWaves, 0, st>>>(g);
+    else dense_few_kernel<TYPE, RT, 1, ODD><<<grid, 64 * kFewWaves, 0, st>>>(g);
+  };
+  if (g.R & 1) go.template operator()<true>();
+  else go.template operator()<false>();
 }
 
 template <int TYPE>
@@ -619,9 +639,9 @@ void split_into(DenseGemm& g, int64_t splits) {
 }  // namespace
 
 // The few-row kernel: up to 16 rows, and of small products up to 32, or 128 where a row's length is no multiple of 8,
-// which the tiles would have copied first.  Rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 8.5 / 10.2,
-// 16 x 4096 x 4096 10.5 / 10.5, 24 x 2048 x 2048 7.0 / 8.8, 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 10 / 18,
-// 100 x 517 x 1001 9.0 / 10.2, 128 x 1003 x 2049 22 / 14.
+// which the tiles would have copied first.  Rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 7.3 / 10.2,
+// 16 x 4096 x 4096 9.6 / 10.5, 24 x 2048 x 2048 7.0 / 8.8, 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 8.7 / 18,
+// 128 x 517 x 1001 7.7 / 10.2, 128 x 1003 x 2049 22 / 14.
 constexpr int64_t kFewRowsMost = 16, kFewRowsSmall = 32, kFewRowsOdd = 128, kFewSmall = int64_t(1) << 27;
 bool takes_few_rows(const DenseGemm& g) {
   return g.P <= kFewRowsMost || (g.P <= (g.R % 8 ? kFewRowsOdd : kFewRowsSmall) && g.P * g.Q * g.R <= kFewSmall);
