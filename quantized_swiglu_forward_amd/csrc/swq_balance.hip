@@ -193,7 +193,8 @@ __device__ __forceinline__ double block_sum(double v, double* meet) {
 // A block sums the p and counts the slots of `rows` tokens, its groups of lanes in turn: sums in registers, then over
 // the block through LDS, counts in LDS (integers, so that no order matters).  Its sums go to
 // sums[block][pitch], its counts to counts[block][pitch], its slots and tokens with a slot to totals[block][2]; a
-// block that is alone concludes.
+// block that is alone concludes.  Latency bounds it, a row's loads and reductions: 8192 x 256 (4.5 MB) takes 5.6 us and
+// its join 5.2 to 6.0; 65 x 64, alone, 4.5.  Atomics on float sums would have needed cleared memory and an order.
 template <int TYPE, int G, int R, int KR, bool SIGMOID, int THREADS>
 __global__ __launch_bounds__(THREADS) void balance_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
                                                           int64_t T, int E, int k, int64_t rows, int pitch,
@@ -272,7 +273,8 @@ __global__ __launch_bounds__(THREADS) void balance_kernel(const void* __restrict
   }
 }
 
-// 32 experts per block, a thread with four of them and a slice of the blocks' sums.  The block that is last by the
+// 32 experts per block, a thread with four of them and a slice of the blocks' sums (one block for all of them took 7.1 to 8.8 us:
+// a CU alone draws the 512 KB that long).  The block that is last by the
 // ticket adds the blocks' parts of the loss, in their order.
 constexpr int kJoinExperts = 32, kJoinThreads = 256;
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(const float* __restrict__ sums,
@@ -343,7 +345,8 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(const float*
   *loss = (float)(by * all);
 }
 
-// The gradient, G lanes per token as above; slot j is in lane j % G.
+// The gradient, G lanes per token as above; slot j is in lane j % G.  One reading of logits and ids and one writing:
+// 8192 x 256 bf16, top 8, 5.9 to 7.5 us (8.9 MB, a launch's 2.5 and one round of dependent loads and reductions); 65 x 64 3.8.
 template <int TYPE, int G, int R, int KR, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restrict__ logits,
                                                              const int* __restrict__ ids,

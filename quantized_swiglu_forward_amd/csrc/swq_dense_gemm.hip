@@ -153,7 +153,10 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
 // through the wave's own stretch of LDS, 32 rows at a time, as whole lines.
 //
 // What bounds it is the card's power: the products alone, no loads and no reads, of 8192 x 4096 x 4096 took 192 us
-// (1.43 PFLOP/s; of 32 x 32 x 16, which adds to twice as many accumulators per product, 210).
+// (1.43 PFLOP/s; of 32 x 32 x 16, which adds to twice as many accumulators per product, 210), the kernel takes 202 to 211
+// (1.30 to 1.36 PFLOP/s), 8192 x 8192 x 8192 818 (1.34).  Of 2048 x 4096 x 14336 (203 to 219) the 448 tiles fill seven
+// eighths of two rounds; an epilogue of GELU, bias and residual adds 23, with SiLU and a checkpoint 29, as nothing
+// else runs on the CU meanwhile.
 template <int AF_, int BF_, int WP_, int WQ_, int S_, int OCC_>
 struct DenseShape {
   static constexpr int AF = AF_, BF = BF_, WP = WP_, WQ = WQ_, S = S_, OCC = OCC_, KS = 64;
@@ -407,8 +410,8 @@ __global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_kernel(
 }
 
 // The gradients by x and by W in one launch, the longer tiles first, so that each fills the CUs that the other leaves
-// idle; behind them the bias's gradient, the sums of the stretches' sums, 64 columns a block.  (2048 x 4096 x 14336, one launch
-// each: 212 and 239 us.)
+// idle; behind them the bias's gradient, the sums of the stretches' sums, 64 columns a block.  2048 x 4096 x 14336 takes 385
+// to 415 us (1.16 to 1.25 PFLOP/s, matrix units 55 % of the cycles busy, 1.3 GB past the L2s), one launch each 212 + 239.
 template <int TYPE, class Sh>
 __global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_pair_kernel(DensePair d) {
   __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
