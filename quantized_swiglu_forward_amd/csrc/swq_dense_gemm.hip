@@ -67,11 +67,19 @@ __device__ __forceinline__ u32x4 residual_at(const DenseGemm& g, int64_t p, int6
   return g.res && p < g.P ? load8(g.res + p * g.Q + q, n) : (u32x4){0, 0, 0, 0};
 }
 
-template <int TYPE>
+// STREAM: stores marked as not to be kept, for the tiles.  256 tiles of 256 x 256 leave 33 MB at once, as much as
+// the L2s hold, which would drive the operands out: 2 to 9 % of the time (8192 x 2560 x 4096 with GELU and a checkpoint 151
+// against 166 us, 2048 x 2048 x 5632 53 against 56).
+template <bool STREAM, class T>
+__device__ __forceinline__ void put(T* o, T w) {
+  if constexpr (STREAM) __builtin_nontemporal_store(w, o);
+  else *o = w;
+}
+template <int TYPE, bool STREAM>
 __device__ __forceinline__ void store8(uint16_t* o, const float (&v)[8], int n) {
   if (n == 8) {
-    *(u32x4_any*)o = (u32x4){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
-                             pack16<TYPE>(v[6], v[7])};
+    put<STREAM>((u32x4_any*)o, (u32x4_any){pack16<TYPE>(v[0], v[1]), pack16<TYPE>(v[2], v[3]), pack16<TYPE>(v[4], v[5]),
+                                           pack16<TYPE>(v[6], v[7])});
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -79,9 +87,15 @@ __device__ __forceinline__ void store8(uint16_t* o, const float (&v)[8], int n) 
   }
 }
 
+// The largest of four neighbouring lanes.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));
+}
+
 // Eight neighbouring sums of row p from column q on, n of them (0 .. 8) in the matrix; four neighbouring lanes
-// have a block of 32 columns, and all four call it.
-template <int TYPE>
+// have a block of 32 columns, and all four call it.  STREAM: as above.
+template <int TYPE, bool STREAM>
 __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64_t p, int64_t q, int n, u32x4 bias,
                                         u32x4 residual) {
   const int64_t at = p * g.Q + q;
@@ -92,14 +106,11 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : 0.0f;
       }
-      uint32_t m = mx8_amax(v);
-      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-      const Mx8Step s = mx8_step(m);
+      const Mx8Step s = mx8_step(max_of_four(mx8_amax(v)));
       const u32x2 w = mx8_codes(v, s);
       uint8_t* z = (uint8_t*)g.z + at;
       if (n == 8) {
-        *(u32x2_any*)z = w;
+        put<STREAM>((u32x2_any*)z, (u32x2_any)w);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -107,7 +118,7 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
       }
       if ((q & 31) == 0 && n > 0) g.z_scales[p * ((g.Q + 31) / 32) + q / 32] = (uint8_t)s.byte;
     } else {
-      store8<TYPE>((uint16_t*)g.z + at, v, n);
+      store8<TYPE, STREAM>((uint16_t*)g.z + at, v, n);
     }
   }
   const auto through = [&](int act) SWQ_INLINE {
@@ -124,15 +135,15 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
   if (g.out_type == kTypeF32) {
     float* o = (float*)g.out + at;
     if (n == 8) {
-      *(u32x4_any*)o = __builtin_bit_cast(u32x4, (f32x4){v[0], v[1], v[2], v[3]});
-      *(u32x4_any*)(o + 4) = __builtin_bit_cast(u32x4, (f32x4){v[4], v[5], v[6], v[7]});
+      put<STREAM>((u32x4_any*)o, __builtin_bit_cast(u32x4_any, (f32x4){v[0], v[1], v[2], v[3]}));
+      put<STREAM>((u32x4_any*)(o + 4), __builtin_bit_cast(u32x4_any, (f32x4){v[4], v[5], v[6], v[7]}));
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < n) o[j] = v[j];
     }
   } else {
-    store8<TYPE>((uint16_t*)g.out + at, v, n);
+    store8<TYPE, STREAM>((uint16_t*)g.out + at, v, n);
   }
 }
 
@@ -371,8 +382,8 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int j = 0; j < BF; ++j) *(f32x4*)(buf + (16 * e + r) * Sh::PITCH + 16 * j + 4 * h) = acc[2 * i + e][j];
-#pragma unroll 1
-    for (int k = 0; k < 32; k += ROWS) {
+#pragma unroll(64 % LANES ? 1 : 2)
+    for (int k = 0; k < 32; k += ROWS) {             // (two at once: 1 to 4 % faster, of rows of twelve lanes 4 % slower)
       const int row = min(k + lane / LANES, 31);
       const int64_t p = pw + i * 32 + k;
       const f32x4 x = *(const f32x4*)(buf + row * Sh::PITCH + col), y = *(const f32x4*)(buf + row * Sh::PITCH + col + 4);
@@ -391,9 +402,9 @@ __device__ __forceinline__ void dense_tile(const DenseGemm& g, int block, int pa
           *(f32x4*)(o + 4) = y;
         }
       } else if constexpr (PLAIN) {
-        store8<TYPE>((uint16_t*)g.out + p * g.Q + q, v, n);
+        store8<TYPE, true>((uint16_t*)g.out + p * g.Q + q, v, n);
       } else {
-        finish8<TYPE>(g, v, p, q, n, bias, residual);
+        finish8<TYPE, true>(g, v, p, q, n, bias, residual);
       }
     }
   });
@@ -466,7 +477,7 @@ __global__ __launch_bounds__(256) void dense_join_kernel(DenseGemm g, uint32_t p
       for (int j = 0; j < 4; ++j) v[j] += x[j], v[4 + j] += y[j];
     }
   }
-  finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
+  finish8<TYPE, false>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
 }
 
 // ----------------------------------------------------------------- few rows ----
@@ -563,7 +574,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few_kernel(DenseGemm g) 
     }
     float v[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
     const int n = q + 8 <= g.Q ? 8 : q < g.Q ? (int)(g.Q - q) : 0;
-    finish8<TYPE>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
+    finish8<TYPE, false>(g, v, p, q, n, bias_at(g, q, n), residual_at(g, p, q, n));
   }
 }
 
