@@ -163,11 +163,12 @@ __device__ __forceinline__ void finish8(const DenseGemm& g, float (&v)[8], int64
 // The second operand of the products is a, so that lane 16 h + r has row r's columns 4 h .. 4 h + 3; the sums leave
 // through the wave's own stretch of LDS, 32 rows at a time, as whole lines.
 //
-// What bounds it is the card's power: the products alone, no loads and no reads, of 8192 x 4096 x 4096 took 192 us
-// (1.43 PFLOP/s; of 32 x 32 x 16, which adds to twice as many accumulators per product, 210), the kernel takes 202 to 211
-// (1.30 to 1.36 PFLOP/s), 8192 x 8192 x 8192 818 (1.34).  Of 2048 x 4096 x 14336 (203 to 219) the 448 tiles fill seven
-// eighths of two rounds; an epilogue of GELU, bias and residual adds 23, with SiLU and a checkpoint 29, as nothing
-// else runs on the CU meanwhile.
+// What bounds it: matrix units 71 % of the cycles busy at the 1.9 GHz that the card's power leaves (8192 x 8192 x 8192
+// in 784 to 838 us, 1.31 to 1.40 PFLOP/s).  Without its loads the same loop takes 624, with all of them from L2 726: the
+// misses' latency, a stage's loads having one stage's time to come, and the loads' share of power and LDS.  Products of
+// 32 x 32 x 16 took a tenth longer.  8192 x 4096 x 4096 takes 202 to 215, 2048 x 4096 x 14336 203 to 217 (448 tiles fill
+// seven eighths of two rounds of 256 CUs); of that 8 to 14 a round are the stores of 256 tiles at once, as
+// nothing else runs on a CU meanwhile.  An epilogue of GELU, bias and residual adds 18 us there, of SiLU, residual and checkpoint 24.
 template <int AF_, int BF_, int WP_, int WQ_, int S_, int OCC_>
 struct DenseShape {
   static constexpr int AF = AF_, BF = BF_, WP = WP_, WQ = WQ_, S = S_, OCC = OCC_, KS = 64;
@@ -422,7 +423,7 @@ __global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_kernel(
 
 // The gradients by x and by W in one launch, the longer tiles first, so that each fills the CUs that the other leaves
 // idle; behind them the bias's gradient, the sums of the stretches' sums, 64 columns a block.  2048 x 4096 x 14336 takes 385
-// to 415 us (1.16 to 1.25 PFLOP/s, matrix units 55 % of the cycles busy, 1.3 GB past the L2s), one launch each 212 + 239.
+// to 415 us (1.16 to 1.25 PFLOP/s, matrix units 54 % of the cycles busy, 1.3 GB past the L2s), one launch each 210 + 220.
 template <int TYPE, class Sh>
 __global__ __launch_bounds__(64 * Sh::W, Sh::OCC * Sh::W / 4) void dense_pair_kernel(DensePair d) {
   __shared__ __attribute__((aligned(1024))) char lds[Sh::LDS];
