@@ -400,7 +400,7 @@ int swiglu_q_dense_linear(const void *x, const void *W, const void *bias, const 
  * each NULL where not wanted (not all three); the residual's gradient is dout itself.
  * dout [M, N], W and the gradients in `type`; x (needed for dW) and z (needed unless act is
  * SWQ_ACT_NONE) in `type`, or checkpoints where their scales are not NULL (x, z the codes).  act'(0) of
- * SWQ_ACT_RELU is 0.  dz is float32, rounded to `type` for the products (dbias sums it unrounded); float32
+ * SWQ_ACT_RELU is 0, act' of an infinity (a z past its type's largest value is kept as one) its limit, 0 or 1.  dz is float32, rounded to `type` for the products (dbias sums it unrounded); float32
  * sums, one rounding.  M == 0 writes dW and dbias as zeros.
  */
 int swiglu_q_dense_linear_backward(const void *dout, const void *x, const void *x_scales, const void *W, const void *z,

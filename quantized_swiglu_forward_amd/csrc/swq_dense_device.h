@@ -116,18 +116,23 @@ __device__ __forceinline__ float activate(float z, int act) {
 }
 
 // d activate / dz (relu: 0 at 0).  Where an intermediate square overflows, the exponential that multiplies it is 0
-// and the derivative its limit.
+// and the derivative its limit.  An infinite z (a kept z past its 16-bit type's largest value is one) is a factor of float32's
+// largest value instead, as the other factor is 0 there; of a NaN the other factor is one too.
+__device__ __forceinline__ float as_factor(float z) {
+  constexpr float top = 3.402823466e38f;
+  return __builtin_amdgcn_fmed3f(z, -top, top);
+}
 __device__ __forceinline__ float activate_slope(float z, int act) {
   if (act == kActNone) return 1.0f;
   if (act == kActRelu) return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
   if (act == kActSilu) {
     const float s = sigma(z);
-    return s * fmaf(z, 1.0f - s, 1.0f);
+    return s * fmaf(as_factor(z), 1.0f - s, 1.0f);
   }
   if (act == kActGelu) {
     float e;
     const float tail = normal_tail(z, e);
-    return fmaf(z * e, 0.39894228040143268f, z < 0.0f ? tail : 1.0f - tail);
+    return fmaf(as_factor(z) * e, 0.39894228040143268f, z < 0.0f ? tail : 1.0f - tail);
   }
   const float s = gelu_sigma(z), d = s * (1.0f - s);
   return d > 0.0f ? fmaf(z * d, 1.5957691216057308f * fmaf(3.0f * 0.044715f * z, z, 1.0f), s) : s;

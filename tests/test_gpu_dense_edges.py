@@ -1,0 +1,52 @@
+"""Ends of what the products with 16-bit weights and the router's gradient take, on the GPU: values past the type's largest,
+masked experts, the most rows, operands that are not read."""
+import pytest
+import torch
+
+import dense_reference as ref
+import quantized_swiglu_forward_amd as swq
+from gpu_helpers import say
+from test_gpu_dense import BF16, F16, F32, normal
+
+pytestmark = pytest.mark.gpu
+
+ACTS = [swq.SWQ_ACT_RELU, swq.SWQ_ACT_SILU, swq.SWQ_ACT_GELU, swq.SWQ_ACT_GELU_TANH]
+
+
+@pytest.mark.parametrize("M,N", [(5, 40), (150, 200)])
+@pytest.mark.parametrize("act", ACTS)
+def test_pre_activations_past_binary16(act, M, N):
+    """z of +-72000 is an infinity in binary16; its derivatives are 1 and 0 all the same (act' is within 2^-60 of them
+    from |z| = 50 on), as they are from a checkpoint, which holds such values."""
+    K = 16
+    x, w = normal(1, M, K, dtype=F16), torch.full((N, K), 45.0, dtype=F16, device="cuda")
+    x[0], x[1], x[M - 1] = 100.0, -100.0, 100.0
+    dout = normal(2, M, N, dtype=F16)
+    say("past binary16", act, M, N)
+    out, z = swq.dense_linear(x, w, act=act, keep="same", out_mode=swq.SWQ_LINEAR_F32)
+    want = ref.act(ref.wide(x) @ ref.wide(w).t(), act)
+    assert torch.isfinite(out).all() and torch.isinf(z[0]).all() and torch.isinf(z[1]).all()
+    assert float(out[0].min()) == 72000.0 and float(out[1].abs().max()) == 0.0 == float(want[1].abs().max())
+    wz = ref.wide(z).clamp(-72000.0, 72000.0)
+    got = dict(zip(("dx", "dw", "dbias"), swq.dense_linear_backward(dout, x, w, z, act=act)))
+    for name, (v, tol) in ref.backward(dout, ref.wide(x), w, wz, act, F16).items():
+        ref.close(got[name], v, tol, name)
+    _, z8 = swq.dense_linear(x, w, act=act, keep="mx8")
+    dx8 = swq.dense_linear_backward(dout, x, w, z8, act=act)[0]
+    for row in (0, 1, M - 1):
+        assert torch.equal(dx8[row], got["dx"][row])
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_slopes_at_infinities(act, dtype):
+    """A kept z of +-inf, next to the type's largest values: 1 and 0; a NaN stays one.  dbias of one row is dz itself."""
+    top = torch.finfo(dtype).max
+    z = torch.tensor([[float("inf"), float("-inf"), top, -top, float("nan"), 0.0, 1.0, -1.0, 60.0, -200.0]], dtype=dtype,
+                     device="cuda")
+    dout, w = torch.full_like(z, 3.0), torch.zeros(z.shape[1], 8, dtype=dtype, device="cuda")
+    say("slopes at infinities", act, dtype)
+    db = swq.dense_linear_backward(dout, None, w, z, act=act, want=(False, False, True))[2].tolist()
+    assert db[:4] == [3.0, 0.0, 3.0, 0.0] and db[4] != db[4] and db[8:] == [3.0, 0.0], db
+    want = 3.0 * ref.slope(torch.tensor([0.0, 1.0, -1.0]).double(), act)
+    ref.close(torch.tensor(db[5:8]), want, 3.0 * ref.SLOPE_ERR + ref.rounding(want, dtype) * 1.01)
