@@ -439,8 +439,8 @@ int swiglu_q_balance_loss(const void *logits, const int32_t *ids, int64_t T, int
  * The gradient dlogits [T, E] (in the logits' type) of the routing weights that swiglu_q_route
  * gave for ids, dweights float32 [T, k] (NULL: none), and of the balance loss, slopes as
  * swiglu_q_balance_loss left them (NULL: none) times *dloss, a float32 on the device (NULL: 1).
- * The choice of the experts and the counts are constants.  A slot whose id is outside [0, E) adds nothing (its
- * dweights entry is not read as a number), an expert whose logit is -inf or NaN gets 0, and so does
+ * The choice of the experts and the counts are constants.  A slot whose id is outside [0, E), or whose
+ * expert's logit is -inf or NaN, adds nothing (its dweights entry is not read as a number); such an expert gets 0, and so does
  * a token without a slot.  The same id in two slots counts as two slots.
  */
 int swiglu_q_route_backward(const void *logits, const int32_t *ids, const float *dweights, const float *slopes,

@@ -366,6 +366,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const void* __restr
   for (int s = 0; s < KR; ++s) {
     dw[s] = id[s] >= 0 && dweights ? dweights[t * k + lane + G * s] : 0.0f;
     lv[s] = id[s] >= 0 ? logit_at<TYPE>(logits, t * E + id[s]) : kMinusInf;
+    dw[s] = lv[s] == kMinusInf ? 0.0f : dw[s];           // (a masked expert's weight is 0, whatever stands in its dweights)
     slot[s] = dw[s];
   }
 #pragma unroll

@@ -50,3 +50,28 @@ def test_slopes_at_infinities(act, dtype):
     assert db[:4] == [3.0, 0.0, 3.0, 0.0] and db[4] != db[4] and db[8:] == [3.0, 0.0], db
     want = 3.0 * ref.slope(torch.tensor([0.0, 1.0, -1.0]).double(), act)
     ref.close(torch.tensor(db[5:8]), want, 3.0 * ref.SLOPE_ERR + ref.rounding(want, dtype) * 1.01)
+
+
+@pytest.mark.parametrize("scoring", range(4))
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,E,k", [(1, 8, 3), (33, 7, 4), (70, 100, 20), (40, 417, 10)])
+def test_slots_of_masked_experts(T, E, k, dtype, scoring):
+    """A slot whose expert's logit is -inf or NaN has the weight 0 whatever the others are: what stands in its dweights is
+    not read as a number."""
+    logits = normal(T + E, T, E, dtype=dtype, scale=2.0)
+    ids = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:k] for t in range(T)]).int().cuda()
+    dw = normal(5, T, k, dtype=F32)
+    hidden = torch.zeros(T, k, dtype=torch.bool, device="cuda")
+    hidden[:, 0] = True
+    hidden[::3, k - 1] = True
+    masked = torch.zeros(T, E, dtype=torch.bool, device="cuda").scatter(1, ids.long(), hidden)
+    logits[masked] = float("-inf")
+    logits[0, ids[0, 0]] = float("nan")
+    slopes = normal(6, E, dtype=F32).abs()
+    say("masked experts", T, E, k, dtype, scoring)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        for s in (None, slopes):
+            got = swq.route_backward(logits, ids, torch.where(hidden, torch.full_like(dw, bad), dw), scoring, slopes=s)
+            want = swq.route_backward(logits, ids, torch.where(hidden, torch.zeros_like(dw), dw), scoring, slopes=s)
+            assert torch.isfinite(got).all() and torch.equal(got, want), (bad, s is None)
+            assert not got[masked].any()
