@@ -639,9 +639,12 @@ void launch_join(const DenseGemm& g, hipStream_t st) {
   else dense_join_kernel<kTypeBf16><<<blocks, 256, 0, st>>>(g, per_row);
 }
 
-// One launch holds fewer than 2^32 threads (of more the rest is left out, with no error); splits are for few tiles.
-bool launch_holds(const DenseGemm* g, int kind) {
-  return !g || tiles_of(*g, kind) * (kind >= kTiles256 ? 512 : 256) < (int64_t(1) << 31);
+// One launch holds fewer than 2^32 threads (of more the rest is left out, with no error).  Splits (four blocks a CU at most)
+// and the sums of the bias's gradient (2^14 blocks at most) are counted as 2^15 blocks.  So products from about 2^39 outputs on,
+// more than the card's memory holds, are refused.
+bool launch_holds(const DenseGemm* x, const DenseGemm* w, int kind) {
+  const int64_t blocks = tiles_of(*x, kind) + (w ? tiles_of(*w, kind) : 0) + (int64_t(1) << 15);
+  return blocks * (kind >= kTiles256 ? 512 : 256) < (int64_t(1) << 32);
 }
 
 void split_into(DenseGemm& g, int64_t splits) {
@@ -682,7 +685,7 @@ bool plan_tiles(DenseGemm* x, DenseGemm* w, bool gradients) {
   int kind = kTiles64;
   int64_t splits[2] = {1, 1};
   for (int k = kTiles64; k <= (gradients ? kTiles256 : kTiles192); ++k) {
-    if (!launch_holds(g[0], k) || !launch_holds(g[1], k)) continue;
+    if (!launch_holds(g[0], g[1], k)) continue;
     const auto block_us = [&](int64_t stages, double load, bool alone) {
       return k >= kTiles256 ? 2.2 + stages * (1.1 + 0.35 * load) * (kColumns[k] + 8) / 264
              : k == kTiles128 ? 0.7 + stages * (alone ? 0.47 + 0.25 * load : 0.46) : 0.3 + stages * (alone ? 0.23 : 0.2);

@@ -1,0 +1,38 @@
+"""Sizes at the ends of what the products with 16-bit weights take, without a GPU."""
+import pytest
+import torch
+
+import quantized_swiglu_forward_amd as swq
+
+P = 1 << 20    # a fake, aligned "device" address: validation never dereferences it
+LINEAR = dict(x=P, W=P, bias=P, residual=P, M=4, K=16, N=64, type=0, act=2, out_mode=0, out=P, stream=0)
+BACK = dict(dout=P, x=P, x_scales=None, W=P, z=None, z_scales=None, M=4, K=16, N=64, type=0, act=0, dx=P, dW=P, dbias=P,
+            stream=0)
+MOST = 1 << 30
+
+
+@pytest.mark.parametrize("fn,base,kw", [
+    (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=512)),                 # 2^23 tiles of 512 threads
+    (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=1 << 20)),
+    (swq.swiglu_q_dense_linear_backward, BACK, dict(M=MOST, K=512)),
+    (swq.swiglu_q_dense_linear_backward, BACK, dict(M=MOST, K=512, dW=None, dbias=None)),
+    (swq.swiglu_q_dense_linear_backward, BACK, dict(M=64, K=1 << 20, N=1 << 20, dx=None)),
+])
+def test_more_threads_than_a_launch(fn, base, kw):
+    """A launch of 2^32 threads or more would be cut off without an error: such a product is refused."""
+    assert fn(**{**base, **kw}) == swq.SWQ_ERR_SHAPE
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch on addresses that are none")
+@pytest.mark.parametrize("fn,base,kw", [
+    (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=1)),
+    (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=64)),
+    (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=256)),
+    (swq.swiglu_q_dense_linear, LINEAR, dict(M=1 << 17, N=1 << 20)),
+    (swq.swiglu_q_dense_linear_backward, BACK, dict(M=MOST, N=8)),
+    (swq.swiglu_q_dense_linear_backward, BACK, dict(M=MOST, N=8, K=256)),
+    (swq.swiglu_q_dense_linear_backward, BACK, dict(M=8, K=1 << 18, N=1 << 18)),
+])
+def test_sizes_that_are_taken(fn, base, kw):
+    """What the card's memory could hold is not refused: without a GPU the call fails only where it needs one."""
+    assert fn(**{**base, **kw}) in (swq.SWQ_ERR_HIP, swq.SWQ_ERR_WORKSPACE)

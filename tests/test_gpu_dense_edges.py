@@ -75,3 +75,24 @@ def test_slots_of_masked_experts(T, E, k, dtype, scoring):
             want = swq.route_backward(logits, ids, torch.where(hidden, torch.zeros_like(dw), dw), scoring, slopes=s)
             assert torch.isfinite(got).all() and torch.equal(got, want), (bad, s is None)
             assert not got[masked].any()
+
+
+def test_most_rows():
+    """2^30 rows: tiles of 2^31 threads, forward and backward, at the first, middle and last rows; all other rows are zeros."""
+    M, K, N = 1 << 30, 8, 8
+    w = normal(1, N, K)
+    say("most rows")
+    x = torch.zeros(M, K, dtype=BF16, device="cuda")
+    pick = torch.tensor([0, 1, 255, 256, M // 2 - 1, M // 2, M - 257, M - 2, M - 1]).cuda()
+    rows = normal(2, len(pick), K)
+    x[pick] = rows
+    y = swq.dense_linear(x, w)
+    want, _, err = ref.linear(rows, w, None, None, 0)
+    ref.close(y[pick], want, err + ref.rounding(want, BF16) * 1.01, "out")
+    assert int(torch.count_nonzero(y)) == N * len(pick)
+    dout = normal(3, len(pick), N)
+    y[pick] = dout
+    dx, dw, db = swq.dense_linear_backward(y, x, w)
+    assert int(torch.count_nonzero(dx)) == K * len(pick)
+    for name, (v, tol) in ref.backward(dout, ref.wide(rows), w, None, 0, BF16).items():
+        ref.close({"dx": dx[pick], "dw": dw, "dbias": db}[name], v, tol, name)
