@@ -835,8 +835,8 @@ def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True
             _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, dout.data_ptr(), at[0], at[1],
                   w.data_ptr(), at[2], at[3], n // N, K, N, t, act, *at[4:])
         elif want_w or want_b:
-            full = w.data_ptr()
-            _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, full, full, None, full, full, None, 0, K,
+            none = 1 << 12                        # an address that is not read
+            _call((_lib or lib()).swiglu_q_dense_linear_backward, dev, stream, none, none, None, none, none, None, 0, K,
                   N, t, act, None, *at[5:])
     return dx, dw, dbias
 

@@ -102,7 +102,7 @@ int swiglu_q_dense_linear_backward(const void* dout, const void* x, const void* 
   if (!type16_ok(type) || !act_ok(act)) return SWQ_ERR_UNSUPPORTED;
   int rc = check_shape(M, K, N);
   if (rc != SWQ_OK) return rc;
-  if (!aligned(dout, 16) || !aligned(W, 16) || !aligned(x, x_scales ? 1 : 16) || !kept_aligned(z, z_scales) ||
+  if (!aligned(dout, 16) || (dx && !aligned(W, 16)) || (dW && !aligned(x, x_scales ? 1 : 16)) || !kept_aligned(z, z_scales) ||
       !aligned(dx, 2) || !aligned(dW, 2) || !aligned(dbias, 2))
     return SWQ_ERR_ALIGN;
   (void)hipGetLastError();

@@ -36,3 +36,13 @@ def test_more_threads_than_a_launch(fn, base, kw):
 def test_sizes_that_are_taken(fn, base, kw):
     """What the card's memory could hold is not refused: without a GPU the call fails only where it needs one."""
     assert fn(**{**base, **kw}) in (swq.SWQ_ERR_HIP, swq.SWQ_ERR_WORKSPACE)
+
+
+def test_operands_that_are_not_read():
+    """x without dW may lie at any address, with it it may not (no rows and no dW: nothing to launch); likewise W without dx."""
+    none = dict(M=0, dW=None, dbias=None)
+    assert swq.swiglu_q_dense_linear_backward(**{**BACK, **none, "x": P + 2}) == swq.SWQ_OK
+    assert swq.swiglu_q_dense_linear_backward(**{**BACK, **none, "W": P + 2}) == swq.SWQ_ERR_ALIGN
+    assert swq.swiglu_q_dense_linear_backward(**{**BACK, "x": P + 2, "dx": None}) == swq.SWQ_ERR_ALIGN
+    assert swq.swiglu_q_dense_linear_backward(**{**BACK, "x": P + 2}) == swq.SWQ_ERR_ALIGN
+    assert swq.swiglu_q_dense_linear_backward(**{**BACK, "W": P + 2}) == swq.SWQ_ERR_ALIGN

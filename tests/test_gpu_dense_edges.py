@@ -96,3 +96,20 @@ def test_most_rows():
     assert int(torch.count_nonzero(dx)) == K * len(pick)
     for name, (v, tol) in ref.backward(dout, ref.wide(rows), w, None, 0, BF16).items():
         ref.close({"dx": dx[pick], "dw": dw, "dbias": db}[name], v, tol, name)
+
+
+def test_operands_that_are_not_read():
+    """x where dw is not wanted and w where dx is not may lie at any address."""
+    M, K, N = 20, 40, 24
+    x, w, dout = normal(1, M * K + 1)[1:].view(M, K), normal(2, N * K + 1)[1:].view(N, K), normal(3, M, N)
+    say("operands that are not read")
+    dx, dw, db = swq.dense_linear_backward(dout, x.clone(), w.clone())
+    assert torch.equal(swq.dense_linear_backward(dout, x, w.clone(), want=(True, False, False))[0], dx)
+    assert torch.equal(swq.dense_linear_backward(dout, x.clone(), w, want=(False, True, False))[1], dw)
+    assert torch.equal(swq.dense_linear_backward(dout, x, w, want=(False, False, True))[2], db)
+    for want, xs, ws in (((True, False, False), x, w), ((False, True, False), x, w), ((True, True, True), x, w.clone()),
+                         ((True, True, True), x.clone(), w)):
+        with pytest.raises(swq.SwigluQError):
+            swq.dense_linear_backward(dout, xs, ws, want=want)
+    zeros = swq.dense_linear_backward(dout[:0], x[:0], w, want=(False, True, True))
+    assert zeros[1].shape == (N, K) and not zeros[1].any() and not zeros[2].any()
