@@ -113,3 +113,36 @@ def test_operands_that_are_not_read():
             swq.dense_linear_backward(dout, xs, ws, want=want)
     zeros = swq.dense_linear_backward(dout[:0], x[:0], w, want=(False, True, True))
     assert zeros[1].shape == (N, K) and not zeros[1].any() and not zeros[2].any()
+
+
+@pytest.mark.parametrize("T,E,k,scoring", [(129, 8, 2, 0), (70003, 300, 6, 1), ((1 << 24) + 100, 8, 2, 0), (3000001, 4, 1, 3),
+                                           (1 << 20, 256, 8, 2)])
+def test_balance_loss_of_many_tokens(T, E, k, scoring):
+    """The loss where many blocks share the tokens.  A block has max(32, T / 256) of them and adds them in 32 groups (8 from 257
+    experts on) one by one; behind that come at most 2 additions between the groups of a wave, 7 between waves and 8 between
+    blocks, the rest is in 64 bits.  So a sum of p is off by that many 2^-24 of itself, and p by 2^-20 as in the router's
+    other tests.  Each block counts for far more than that: a sum without any one of them lies outside."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    ids, _ = swq.route(logits, k, scoring)
+    say("balance loss of many tokens", T, E, k, scoring)
+    loss, counts, slopes = swq.balance_loss(logits, ids, scoring)
+    again = swq.balance_loss(logits, ids, scoring)
+    assert all(torch.equal(a, b) for a, b in zip((loss, counts, slopes), again))
+    wc = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    assert torch.equal(counts.long(), wc)
+    rows = max(32, -(-T // 256))
+    share = torch.zeros(-(-T // rows), dtype=torch.float64, device="cuda")       # of each block
+    for t in range(0, T, rows * 16):
+        v = logits[t:t + rows * 16].double()
+        p = torch.softmax(v, -1) if scoring < 2 else torch.sigmoid(v)
+        p = p @ wc.double() / p.sum(-1)
+        share[t // rows:t // rows + -(-len(p) // rows)] = torch.nn.functional.pad(p, (0, -len(p) % rows)).view(-1, rows).sum(-1)
+    share *= E / (T * k) / T
+    want, tol = float(share.sum()), None
+    adds = -(-rows // (32 if E <= 256 else 8)) + 2 + 7 + 8
+    tol = (adds * 2.0 ** -24 + 2.0 ** -20) * want
+    assert abs(float(loss) - want) <= tol
+    assert float(share.min()) > 3.0 * tol                    # (a planted mistake: any block left out)
+    by = E / (T * k) / T
+    ref.close(slopes, wc.cpu().double() * by, 2.0 ** -23 * wc.cpu().double() * by, "slopes")
