@@ -421,7 +421,9 @@ _dtypes = ()     # SWQ_TYPE_* -> torch type
 _words = ()      # types of codes
 _bytes = _int8 = _int32 = _float32 = None
 _raw_stream = _device_now = _on_device = None   # torch's current stream of a GPU, current GPU, GPU guard
-_fresh = None    # torch's allocation by shape and strides on the current GPU
+# torch's allocation by shape and strides on the current GPU, without its dispatcher (so no mode that watches or fills new
+# tensors sees it; the kernels write every element); its public one where this torch has no such call
+_fresh = None
 
 
 def _load_types():

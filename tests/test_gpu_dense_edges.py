@@ -146,3 +146,44 @@ def test_balance_loss_of_many_tokens(T, E, k, scoring):
     assert float(share.min()) > 3.0 * tol                    # (a planted mistake: any block left out)
     by = E / (T * k) / T
     ref.close(slopes, wc.cpu().double() * by, 2.0 ** -23 * wc.cpu().double() * by, "slopes")
+
+
+def test_outputs_however_allocated(monkeypatch):
+    """Outputs are the same tensors (shape, strides, type, device, values) whether the short way to torch's allocator made them
+    or its public one, on the current stream and another, with and without inference mode."""
+    M, K, N, E, k = 40, 70, 33, 9, 3
+    x, w, b, dout = normal(1, M, K), normal(2, N, K), normal(3, N), normal(4, M, N)
+    gate, up = normal(5, 2, 3, 40), normal(6, 2, 3, 40)
+    logits, e = normal(7, M, E), torch.empty(0, K, dtype=BF16, device="cuda")
+    say("outputs however allocated")
+
+    def run():
+        y, z = swq.dense_linear(x, w, b, act=swq.SWQ_ACT_SILU, keep="mx8")
+        y2, z2 = swq.dense_linear(x, w, b, act=swq.SWQ_ACT_SILU, keep="same", out_mode=swq.SWQ_LINEAR_F32)
+        h, g8, u8 = swq.swiglu(gate, up, keep=True)
+        ids, _ = swq.route(logits, k)
+        x8 = swq.mx8_quantize(x)
+        out = [y, *z, y2, z2, *x8, swq.mx8_dequantize(*x8), h, *g8, *u8, *swq.swiglu_backward(h, g8, u8, hidden=True),
+               *swq.dense_linear_backward(dout, x8, w, z, act=swq.SWQ_ACT_SILU), *swq.balance_loss(logits, ids),
+               swq.route_backward(logits, ids, slopes=swq.balance_loss(logits, ids)[2]),
+               swq.dense_linear(e, w), *swq.mx8_quantize(e)]
+        torch.cuda.synchronize()
+        return out
+
+    def public(shape, stride, dtype):
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
+    short = run()
+    with torch.inference_mode():
+        quiet = run()
+    monkeypatch.setattr(swq, "_fresh", public)
+    want = run()
+    with torch.inference_mode():
+        assert [t.is_inference() for t in quiet] == [t.is_inference() for t in run()]
+    with torch.cuda.stream(torch.cuda.Stream()):
+        other = run()
+    for got in (short, quiet, other):
+        assert len(got) == len(want)
+        for a, b_ in zip(got, want):
+            assert (a.shape, a.stride(), a.dtype, a.device) == (b_.shape, b_.stride(), b_.dtype, b_.device)
+            assert a.is_contiguous() and torch.equal(a, b_)
