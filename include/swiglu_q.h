@@ -365,9 +365,10 @@ int swiglu_q_moe_mlp(const void *x, const int32_t *ids, const float *weights,
  * neighbours of a row, scales uint8 [R, ceil(K / 32)] (a row's last block may be
  * shorter): the value is q 2^(b - 133), 255 = NaN (the Open Compute Project's MXINT8:
  * codes of six fraction bits times 2^(b - 127)).  A block's step is the smallest power of two, from 2^-126
- * on, at which no code passes 127, so a value is off by at most half a step, 1/127 of the
- * block's largest magnitude; ties to even; a block with an infinity or a NaN gets the NaN scale and zero
- * codes.
+ * to 2^121, at which no code passes 127; ties to even.  So a value is off by at most half a step.  That is at most 1/127 of the
+ * block's largest magnitude where this is 2^-120 or more; smaller blocks keep the step 2^-126.  At 2^121 a code that would be
+ * 128 is held at 127: float32 values from 127.5 2^121 on are off by up to a whole step.  A block with an infinity or a NaN
+ * gets the NaN scale and zero codes.
  */
 
 /* Activations. */
@@ -401,7 +402,8 @@ int swiglu_q_dense_linear(const void *x, const void *W, const void *bias, const 
  * each NULL where not wanted (not all three); the residual's gradient is dout itself.
  * dout [M, N], W and the gradients in `type`; x (needed for dW) and z (needed unless act is
  * SWQ_ACT_NONE) in `type`, or checkpoints where their scales are not NULL (x, z the codes).  act'(0) of
- * SWQ_ACT_RELU is 0, act' of an infinity (a z past its type's largest value is kept as one) its limit, 0 or 1.  dz is float32, rounded to `type` for the products (dbias sums it unrounded); float32
+ * SWQ_ACT_RELU is 0, act' of an infinity (a z past its type's largest value is kept as one) its limit, 0 or 1.  dz is float32, rounded once to
+ * `type` for the products (binary16: past 65504 to an infinity, as every output), dbias sums it unrounded; float32
  * sums, one rounding.  M == 0 writes dW and dbias as zeros.
  */
 int swiglu_q_dense_linear_backward(const void *dout, const void *x, const void *x_scales, const void *W, const void *z,
@@ -418,7 +420,7 @@ int swiglu_q_swiglu(const void *gate, const void *up, int64_t R, int64_t K, int 
 /*
  * Its gradients: dgate = dhidden up silu'(gate), dup = dhidden silu(gate), and with hidden not NULL
  * the hidden tensor again (the down projection's dW needs it).  gate and up in `type`, or
- * checkpoints where their scales are not NULL.
+ * checkpoints where their scales are not NULL: then all three are those of the values that these hold.
  */
 int swiglu_q_swiglu_backward(const void *dhidden, const void *gate, const void *gate_scales, const void *up,
                              const void *up_scales, int64_t R, int64_t K, int type, void *dgate, void *dup,

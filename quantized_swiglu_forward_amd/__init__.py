@@ -761,7 +761,8 @@ def dense_linear(x, w, bias=None, act=SWQ_ACT_NONE, residual=None, keep=None, ou
     """``act(z) + residual``, ``z = x W^T + bias``, for x [..., K], W [N, K], bias [N] and residual
     [..., N], all bf16 or all float16.  Returns ``out`` [..., N] in x's type, or float32 with SWQ_LINEAR_F32; with
     keep the pair (out, z), z for ``dense_linear_backward``: keep="same" in x's type, keep="mx8" as
-    a checkpoint (codes, scales)."""
+    a checkpoint (codes, scales).  x and w begin at multiples of 16 bytes.  Nothing is recorded for torch's backward pass, as
+    of every function here: the caller asks for the gradients."""
     t = _type(x, "dense_linear", wide=False)
     if len(w.shape) != 2 or w.dtype != x.dtype or len(x.shape) < 1 or w.shape[1] != x.shape[-1]:
         raise ValueError(f"dense_linear: w must be {x.dtype} [N, K] with x's K")
@@ -795,7 +796,8 @@ def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True
                           stream=None):
     """(dx [..., K], dw [N, K], dbias [N]) of ``dense_linear`` for dout [..., N], in dout's type (bf16 or
     float16); None where want says False.  x (needed for dw) and z (needed unless act is SWQ_ACT_NONE) are tensors
-    of that type or checkpoints (codes, scales).  The residual's gradient is dout itself."""
+    of that type or checkpoints (codes, scales).  The residual's gradient is dout itself.  dout, w where dx is wanted and x
+    where dw is begin at multiples of 16 bytes.  dz is rounded to dout's type for dx and dw (float16: past 65504 an infinity)."""
     t = _type(dout, "dense_linear_backward", wide=False)
     if len(w.shape) != 2 or w.dtype != dout.dtype or len(dout.shape) < 1 or w.shape[0] != dout.shape[-1]:
         raise ValueError(f"dense_linear_backward: w must be {dout.dtype} [N, K] with dout's N")
@@ -845,7 +847,8 @@ def dense_linear_backward(dout, x, w, z=None, act=SWQ_ACT_NONE, want=(True, True
 
 def swiglu(gate, up, keep=False, hidden=None, stream=None):
     """``silu(gate) * up`` for gate and up [..., K] (bf16 or float16).  With keep the triple (hidden, gate,
-    up), gate and up as checkpoints for ``swiglu_backward``."""
+    up), gate and up as checkpoints for ``swiglu_backward``, which is the caller's to call: nothing is recorded for torch's
+    backward pass."""
     t = _type(gate, "swiglu", wide=False)
     shape = gate.shape
     if up.dtype != gate.dtype or up.shape != shape or len(shape) < 1 or shape[-1] == 0:
@@ -867,7 +870,8 @@ def swiglu(gate, up, keep=False, hidden=None, stream=None):
 
 def swiglu_backward(dhidden, gate, up, hidden=False, stream=None):
     """(dgate, dup) of ``swiglu`` for dhidden [..., K] (bf16 or float16), with hidden=True the triple (dgate, dup,
-    hidden), the forward call's result again.  gate and up are tensors of that type or checkpoints."""
+    hidden).  gate and up are tensors of that type or checkpoints; from checkpoints the gradients and hidden are those of the
+    values that these hold, not of the tensors that they were made from."""
     t = _type(dhidden, "swiglu_backward", wide=False)
     shape = dhidden.shape
     if len(shape) < 1 or shape[-1] == 0:

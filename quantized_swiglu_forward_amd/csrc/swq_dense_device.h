@@ -20,7 +20,8 @@ __device__ __forceinline__ int64_t over(int64_t i, uint32_t n) {
 // The step 2^e of a block is the smallest power of two, from 2^-126 on, at which no element's
 // code passes 127: amax lies in [64, 128) steps, or in [127.5, 128) the step is the next one.
 // Codes of 7 bits times a power of two are exact in bf16 (and in binary16 down to its own grid, which the
-// values of binary16 inputs lie on): the one rounding is the code's, at most half a step, amax / 127.
+// values of binary16 inputs lie on): the one rounding is the code's, at most half a step, that is amax / 127 from
+// amax = 2^-120 on (next to float32's largest value, where the step can be no larger, a whole one).
 // A block with an infinity or a NaN gets byte 255 (NaN) and zero codes.
 
 struct Mx8Step {

@@ -659,7 +659,9 @@ void split_into(DenseGemm& g, int64_t splits) {
 // The few-row kernel: up to 16 rows, and of small products up to 32, or 128 where a row's length is no multiple of 8,
 // which the tiles would have copied first.  Rows x K x N, few rows / tiles, us: 8 x 2048 x 5632 7.3 / 10.2,
 // 16 x 4096 x 4096 9.6 / 10.5, 24 x 2048 x 2048 7.0 / 8.8, 32 x 4096 x 4096 13.2 / 11.3, 37 x 1003 x 2049 8.7 / 18,
-// 128 x 517 x 1001 7.7 / 10.2, 128 x 1003 x 2049 22 / 14.
+// 128 x 517 x 1001 7.7 / 10.2, 128 x 1003 x 2049 22 / 14.  The rule
+// is made for these and does badly by large weights: with 14336 outputs 16 rows of 4096 take 35 (17 rows, by tiles, 26), and where K is
+// no multiple of 8 the copy of W makes a step from 16 to 17 rows: K = 4095 58 to 75, K = 8190 69 to 165 (K = 8192 69 to 48).
 constexpr int64_t kFewRowsMost = 16, kFewRowsSmall = 32, kFewRowsOdd = 128, kFewSmall = int64_t(1) << 27;
 bool takes_few_rows(const DenseGemm& g) {
   return g.P <= kFewRowsMost || (g.P <= (g.R % 8 ? kFewRowsOdd : kFewRowsSmall) && g.P * g.Q * g.R <= kFewSmall);

@@ -117,9 +117,10 @@ __device__ __forceinline__ void encode8(const float (&v)[8], const Piece& p, voi
 
 // The elementwise kernels: eight neighbours to a thread, so that every tensor moves in 16-byte pieces (codes in 8), a
 // block's maximum is two exchanges between lanes, and nothing is read twice.  Memory bounds them: 8192 x 10240 bf16
-// quantised in 47 us and back in 38 (5.4 and 6.7 TB/s, codes and a part of the values still in the last-level cache);
-// the SwiGLU of 2048 x 14336 with both checkpoints 43 to 48 (235 MB), its gradient with the hidden tensor 51 to 53 (235 MB).  Small
-// tensors take a launch's 2.5 to 3 us.
+// quantised in 47 us and back in 38 (5.4 and 6.7 TB/s, codes and a part of the values still in the last-level cache; of
+// other tensors 45); the SwiGLU of 2048 x 14336 with both checkpoints 41 to 48 (237 MB), its gradient with the hidden tensor 51
+// to 55 (295 MB).  Rows of odd lengths, 16 bytes at odd elements: 8192 x 10241 49 and 50, 2048 x 14337 46 and 57, so 4 to 11 %
+// longer.  Small tensors take a launch's 2.5 to 3 us.
 template <int TYPE>
 __global__ __launch_bounds__(256) void mx8_quantize_kernel(const void* __restrict__ x, Pieces t, int64_t first,
                                                            int64_t end, void* __restrict__ codes,
@@ -216,7 +217,12 @@ hipError_t over_pieces(int64_t R, int64_t K, F launch) {
 // dz and the sums of its columns.  A block has a stretch of rows of 8 L columns (512; of narrow tensors the power of two
 // that holds a row), eight of a row to a thread, 256 / L rows at a time; these meet in LDS, the stretches' sums in a
 // later kernel, all in order.  One pass over dout and z is all there is to do, so memory bounds it: with x's checkpoint decoded by
-// other blocks of the launch, 2048 x 4096 x 14336 takes 33 to 37 us (4.7 TB/s).
+// other blocks of the launch, 2048 x 4096 x 14336 takes 33 to 37 us (4.7 TB/s); the sums alone 25 to 27, of 14337 columns 31 to 35.
+//
+// dz is rounded to the operands' 16 bits here, once: that is what the matrix units take, and the precision that a layer's
+// gradient has wherever it is kept as a tensor.  dx and dW are off by 0.0023 (bf16) and 0.00029 (binary16) in norm for it, 0.0017
+// and 0.00021 with a float32 dz, which would need two products (a high and a low part) in place of each.  The bias's sums take dz
+// before the rounding.  Past binary16's largest value dz is an infinity, as any gradient that needs a smaller loss scale.
 template <int TYPE>
 __device__ __forceinline__ void act_backward(const Prep& p, int64_t column_block, int64_t stretch, int64_t rows, int L,
                                              float* meet) {

@@ -1,7 +1,8 @@
-"""Sizes at the ends of what the products with 16-bit weights take, without a GPU."""
+"""Sizes at the ends of what the products with 16-bit weights take, and the bounds of a checkpoint's values, without a GPU."""
 import pytest
 import torch
 
+import dense_reference as ref
 import quantized_swiglu_forward_amd as swq
 
 P = 1 << 20    # a fake, aligned "device" address: validation never dereferences it
@@ -46,3 +47,24 @@ def test_operands_that_are_not_read():
     assert swq.swiglu_q_dense_linear_backward(**{**BACK, "x": P + 2, "dx": None}) == swq.SWQ_ERR_ALIGN
     assert swq.swiglu_q_dense_linear_backward(**{**BACK, "x": P + 2}) == swq.SWQ_ERR_ALIGN
     assert swq.swiglu_q_dense_linear_backward(**{**BACK, "W": P + 2}) == swq.SWQ_ERR_ALIGN
+
+
+@pytest.mark.parametrize("low,high", [(-149, -127), (-126, -121), (-120, -118), (-3, 3), (125, 128)])
+def test_how_far_a_checkpoint_is_off(low, high):
+    """The documented bounds, over float32's whole range: half a step, 1/127 of the block's largest magnitude from 2^-120 on, a
+    whole step from 127.5 2^121 on.  (The GPU's codes and scales are these, bit by bit, in the tests of the checkpoints.)"""
+    g = torch.Generator().manual_seed(high)
+    # (one rounding, to float32, where this is the checkpoint's input)
+    x = (torch.rand(60, 64, generator=g).double() * torch.exp2(torch.randint(low, high + 1, (60, 1), generator=g).double()))
+    x = (x * torch.where(torch.rand(60, 64, generator=g) < 0.5, -1.0, 1.0)).clamp(max=torch.finfo(torch.float32).max).float()
+    x[0, 0] = torch.finfo(torch.float32).max if high == 128 else 2.0 ** low
+    codes, scales = (torch.from_numpy(t) for t in ref.mx8(x))
+    off = (ref.mx8_values(codes, scales) - x.double()).abs()
+    half = ref.mx8_half_steps(scales, 64)
+    top = x.double().abs().view(60, 2, 32).amax(-1).repeat_interleave(32, -1)
+    last = x.double().abs() >= 127.5 * 2.0 ** 121
+    assert bool((off <= torch.where(last, 2 * half, half)).all()) and bool((scales >= 7).all()) and bool((scales <= 254).all())
+    assert bool((off <= top / 127)[top >= 2.0 ** -120].all())
+    # both exceptions are there (values are 2^low times a factor below 1, so with low = -120 some blocks lie under the border; a
+    # whole step of 127.5 and more is under 1/127 of them)
+    assert bool((off > half).any()) == (high == 128) and bool((off > top / 127).any()) == (low <= -120)
