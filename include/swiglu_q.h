@@ -357,7 +357,8 @@ int swiglu_q_moe_mlp(const void *x, const int32_t *ids, const float *weights,
  * written, no clearing needed between graph replays.  Sizes are any (no multiples):
  * rows up to 2^30, inputs and outputs up to 2^20; products of about 2^39 outputs and more (dx, dW; a terabyte), which
  * one launch cannot hold, return SWQ_ERR_SHAPE.  x, W and dout of the products need 16-byte
- * alignment (where they are read: x for dW, W for dx), checkpoints none, everything else its element size.  The products and the
+ * alignment (where they are read: x for dW, W for dx), checkpoints none, everything else its element size.  Outputs overlap neither
+ * inputs nor each other, but the linear's out may be its residual.  The products and the
  * balance loss take a workspace of the (device, stream), with the rules for graphs and
  * concurrent calls given at the top.
  *

@@ -24,7 +24,6 @@ def test_more_threads_than_a_launch(fn, base, kw):
     assert fn(**{**base, **kw}) == swq.SWQ_ERR_SHAPE
 
 
-@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch on addresses that are none")
 @pytest.mark.parametrize("fn,base,kw", [
     (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=1)),
     (swq.swiglu_q_dense_linear, LINEAR, dict(M=MOST, N=64)),
@@ -36,6 +35,8 @@ def test_more_threads_than_a_launch(fn, base, kw):
 ])
 def test_sizes_that_are_taken(fn, base, kw):
     """What the card's memory could hold is not refused: without a GPU the call fails only where it needs one."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on addresses that are none")
     assert fn(**{**base, **kw}) in (swq.SWQ_ERR_HIP, swq.SWQ_ERR_WORKSPACE)
 
 
