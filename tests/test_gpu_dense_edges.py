@@ -1,5 +1,5 @@
 """Ends of what the products with 16-bit weights and the router's gradient take, on the GPU: values past the type's largest,
-masked experts, the most rows, operands that are not read."""
+masked experts, the most rows, operands that are not read, the balance loss of many tokens, outputs however allocated."""
 import pytest
 import torch
 
